@@ -1,4 +1,4 @@
-"""ctypes binding of libnvfp4moe.so (include/nvfp4moe.h).
+"""ctypes binding of libnvfp4moe.so (include/nvfp4moe.h, include/nvfp4moe_ops.h).
 
 Argument marshalling only: torch tensors supply device memory and the current HIP stream, and
 every step of the computation runs in the library's HIP kernels. There is no fallback. If the
@@ -7,6 +7,7 @@ library is missing, or a tensor is not on the GPU, the call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 
@@ -15,6 +16,7 @@ import torch  # loads torch's HIP runtime first; the library binds to that same 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libnvfp4moe.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "nvfp4moe.h")
+OPS_HEADER = os.path.join(os.path.dirname(HERE), "include", "nvfp4moe_ops.h")
 
 NVFP4_OK = 0
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ERR_ALIGN",
@@ -34,6 +36,11 @@ class nvfp4_weights(C.Structure):
 
 class fp8_channel_weights(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("channel_scale", C.c_void_p), ("rows", C.c_int32), ("k", C.c_int32)]
+
+
+class nvfp4_lora(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scale", C.c_void_p),
+                ("adapters", C.c_int32), ("rows", C.c_int32), ("k", C.c_int32), ("rank", C.c_int32)]
 
 
 _LIB = None
@@ -71,6 +78,16 @@ _SIGS = {
                                           C.POINTER(nvfp4_weights), _vp, _vp, _vp]),
     "nvfp4_moe_layer": (C.c_int, [_vp, _i32, _i32, _i32, _vp, C.POINTER(nvfp4_weights), _i32,
                                   C.POINTER(nvfp4_weights), _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_moe_permute": (C.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4_moe_unpermute": (C.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4_moe_unpermute_grad": (C.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "nvfp4_lora_add_ws_bytes": (_sz, [_i32, _i32, _i32]),
+    "nvfp4_lora_add": (C.c_int, [_vp, _i32, _i32, _i32, _vp, C.POINTER(nvfp4_lora), _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_linear_lora_ws_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "nvfp4_linear_lora": (C.c_int, [_vp, _vp, _i32, C.POINTER(nvfp4_weights), C.POINTER(nvfp4_lora), _vp, _vp, _sz,
+                                    _vp]),
+    "nvfp4_linear_swiglu_lora": (C.c_int, [_vp, _vp, _i32, C.POINTER(nvfp4_weights), _i32, C.POINTER(nvfp4_lora), _vp,
+                                           _vp, _sz, _vp]),
 }
 
 
@@ -91,9 +108,9 @@ def lib() -> C.CDLL:
     return _LIB
 
 
-def header_functions() -> list[str]:
-    """Names of the functions declared in include/nvfp4moe.h."""
-    txt = open(HEADER).read()
+def header_functions(path: str = HEADER) -> list[str]:
+    """Names of the functions declared in include/nvfp4moe.h (or the header given)."""
+    txt = open(path).read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(nvfp4_\w+)\s*\(", txt, flags=re.M)))
 
 
@@ -655,3 +672,204 @@ def nvfp4_moe_w2_reduce_with_shared(plan: torch.Tensor, M: int, topk: int, E: in
         _dev(shared_sigma, "shared_sigma", torch.float32), _dev(shared_y, "shared_y", torch.float32),
         _dev(out, "out", torch.float16), ws.data_ptr(), ws.numel(), _stream(stream)))
     return out
+
+
+# ---- rows moved by the plan, and low-rank adapters (include/nvfp4moe_ops.h) --------------------------
+
+@functools.lru_cache(maxsize=256)
+def _plan_bytes(M: int, topk: int, E: int) -> int:
+    return nvfp4_moe_plan_bytes(M, topk, E)
+
+
+def _alloc(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An output or workspace that the call writes on `stream`: allocated on that stream, so that the
+    allocator hands its memory on only behind the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _one_device(*tensors):
+    """Raise unless every tensor lies on the current device, where the launch goes."""
+    for t in tensors:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _opt(t, name: str, dtype: torch.dtype):
+    return None if t is None else _dev(t, name, dtype)
+
+
+def _row_plan(plan: torch.Tensor, M: int, topk: int, E: int):
+    need = _plan_bytes(M, topk, E)
+    if plan.numel() * plan.element_size() < need or need == 0:
+        _bytes(plan, "plan", need)
+
+
+def nvfp4_moe_permute(plan: torch.Tensor, M: int, topk: int, E: int, x: torch.Tensor,
+                      topk_weights: torch.Tensor | None = None, xs: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Tokens sorted by expert: row pos(t, k) of xs is x[t], times topk_weights[t, k] where given (one
+    fp16 rounding). Returns xs fp16 [M*topk, K] in bucket order; rows >= n_valid are left as they are."""
+    if x.dim() != 2 or x.shape[0] != M:
+        raise ValueError(f"x must have shape ({M}, K), got {tuple(x.shape)}")
+    K = x.shape[1]
+    _row_plan(plan, M, topk, E)
+    if topk_weights is not None:
+        _shape(topk_weights, "topk_weights", (M, topk))
+    if xs is None:
+        xs = _alloc((M * topk, K), torch.float16, x.device, stream)
+    _rows(xs, "xs", M * topk, K)
+    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(x, "x", torch.float16),
+            _opt(topk_weights, "topk_weights", torch.float32), K, _dev(xs, "xs", torch.float16), _stream(stream))
+    _one_device(plan, x, topk_weights, xs)
+    _check("nvfp4_moe_permute", lib().nvfp4_moe_permute(*args))
+    return xs
+
+
+def nvfp4_moe_unpermute(plan: torch.Tensor, M: int, topk: int, E: int, ys: torch.Tensor,
+                        topk_weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Expert rows back to their tokens: out[t] = sum over the valid slots, in slot order, of
+    topk_weights[t, k] * ys[pos(t, k)] (weights None: of the rows themselves, the gradient of
+    nvfp4_moe_permute). Returns out fp16 [M, K]."""
+    if ys.dim() != 2 or ys.shape[0] < M * topk:
+        raise ValueError(f"ys must have shape [>= {M * topk}, K], got {tuple(ys.shape)}")
+    K = ys.shape[1]
+    _row_plan(plan, M, topk, E)
+    if topk_weights is not None:
+        _shape(topk_weights, "topk_weights", (M, topk))
+    if out is None:
+        out = _alloc((M, K), torch.float16, ys.device, stream)
+    _shape(out, "out", (M, K))
+    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(ys, "ys", torch.float16),
+            _opt(topk_weights, "topk_weights", torch.float32), K, _dev(out, "out", torch.float16), _stream(stream))
+    _one_device(plan, ys, topk_weights, out)
+    _check("nvfp4_moe_unpermute", lib().nvfp4_moe_unpermute(*args))
+    return out
+
+
+def nvfp4_moe_unpermute_grad(plan: torch.Tensor, M: int, topk: int, E: int, dout: torch.Tensor, ys: torch.Tensor,
+                             topk_weights: torch.Tensor | None, dys: torch.Tensor | None = None,
+                             dweights: torch.Tensor | None = None, want_dys: bool = True, stream=None):
+    """The gradient of nvfp4_moe_unpermute with weights. Returns (dys fp16 [M*topk, K] in bucket order, rows
+    >= n_valid left as they are, or None without want_dys; dweights FP32 [M, topk], 0 for skipped pairs)."""
+    if dout.dim() != 2 or dout.shape[0] != M:
+        raise ValueError(f"dout must have shape ({M}, K), got {tuple(dout.shape)}")
+    K = dout.shape[1]
+    _row_plan(plan, M, topk, E)
+    _rows(ys, "ys", M * topk, K)
+    if topk_weights is not None:
+        _shape(topk_weights, "topk_weights", (M, topk))
+    if not want_dys:
+        dys = None
+    elif dys is None:
+        dys = _alloc((M * topk, K), torch.float16, dout.device, stream)
+    if dys is not None:
+        _rows(dys, "dys", M * topk, K)
+    if dweights is None:
+        dweights = _alloc((M, topk), torch.float32, dout.device, stream)
+    _shape(dweights, "dweights", (M, topk))
+    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(dout, "dout", torch.float16), _dev(ys, "ys", torch.float16),
+            _opt(topk_weights, "topk_weights", torch.float32), K, _opt(dys, "dys", torch.float16),
+            _dev(dweights, "dweights", torch.float32), _stream(stream))
+    _one_device(plan, dout, ys, topk_weights, dys, dweights)
+    _check("nvfp4_moe_unpermute_grad", lib().nvfp4_moe_unpermute_grad(*args))
+    return dys, dweights
+
+
+class LoRATensor:
+    """Device storage of one projection's low-rank adapters: a fp16 [L, rank, K], b fp16 [L, N, rank],
+    scale float32 [L]. Adapters of a smaller rank are padded with zero rows of a and zero columns of b."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+        if a.dim() != 3 or b.dim() != 3 or scale.dim() != 1:
+            raise ValueError("a/b must be [L,rank,K]/[L,N,rank], scale [L]")
+        self.a, self.b, self.scale = a, b, scale
+        self.adapters, self.rank, self.k = a.shape
+        self.rows = b.shape[1]
+        if b.shape[0] != self.adapters or b.shape[2] != self.rank or scale.shape[0] != self.adapters:
+            raise ValueError("inconsistent low-rank adapter shapes")
+
+    def desc(self) -> nvfp4_lora:
+        """The C descriptor; built once and reused while a, b and scale are the same tensor objects
+        (their storage must not be reallocated in place)."""
+        c = self.__dict__.get("_desc")
+        if c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale:
+            return c[3]
+        d = nvfp4_lora(_dev(self.a, "a", torch.float16), _dev(self.b, "b", torch.float16),
+                       _dev(self.scale, "scale", torch.float32), self.adapters, self.rows, self.k, self.rank)
+        self._desc = (self.a, self.b, self.scale, d)
+        return d
+
+
+def nvfp4_lora_add_ws_bytes(P: int, K: int, rank: int) -> int:
+    return int(lib().nvfp4_lora_add_ws_bytes(P, K, rank))
+
+
+def nvfp4_linear_lora_ws_bytes(M: int, rows: int, K: int, rank: int) -> int:
+    return int(lib().nvfp4_linear_lora_ws_bytes(M, rows, K, rank))
+
+
+def _lora_ws(ws, need: int, device, stream) -> torch.Tensor:
+    if ws is None:
+        return _alloc((max(need, 16),), torch.uint8, device, stream)
+    _bytes(ws, "ws", need)
+    return ws
+
+
+def nvfp4_lora_add(plan: torch.Tensor, M: int, topk: int, x: torch.Tensor, lora: LoRATensor, y: torch.Tensor,
+                   order: int = 0, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """out = y + scale_a (x A_a^T) B_a^T for every row's adapter a; plan: nvfp4_moe_plan of the adapter
+    ids [M, topk] over lora.adapters. x fp16 [M*topk, K], y fp16 [M*topk, N]; rows in pair order (order
+    0) or in the plan's bucket order (order 1; rows >= n_valid are left as they are). out may be y."""
+    P = M * topk
+    _shape(x, "x", (P, lora.k))
+    _shape(y, "y", (P, lora.rows))
+    _row_plan(plan, M, topk, lora.adapters)
+    if out is None:
+        out = _alloc((P, lora.rows), torch.float16, x.device, stream)
+    _shape(out, "out", (P, lora.rows))
+    ws = _lora_ws(ws, nvfp4_lora_add_ws_bytes(P, lora.k, lora.rank), x.device, stream)
+    args = (_dev(plan, "plan", torch.int32), M, topk, order, _dev(x, "x", torch.float16), C.byref(lora.desc()),
+            _dev(y, "y", torch.float16), _dev(out, "out", torch.float16), _dev(ws, "ws", ws.dtype),
+            ws.numel() * ws.element_size(), _stream(stream))
+    _one_device(plan, x, lora.a, y, out, ws)
+    _check("nvfp4_lora_add", lib().nvfp4_lora_add(*args))
+    return out
+
+
+def _linear_lora(fn: str, plan, x, w: NVFP4Tensor, lora: LoRATensor, layout, out, name: str, cols: int, ws, stream):
+    if x.dim() != 2 or x.shape[1] != w.k:
+        raise ValueError(f"x must have shape (M, {w.k}), got {tuple(x.shape)}")
+    M = x.shape[0]
+    if (lora.rows, lora.k) != (w.rows, w.k):
+        raise ValueError(f"the adapters are for a {lora.rows} x {lora.k} weight, not {w.rows} x {w.k}")
+    _row_plan(plan, M, 1, lora.adapters)
+    if out is None:
+        out = _alloc((M, cols), torch.float16, x.device, stream)
+    _shape(out, name, (M, cols))
+    ws = _lora_ws(ws, nvfp4_linear_lora_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
+    head = (_dev(plan, "plan", torch.int32), _dev(x, "x", torch.float16), M, C.byref(w.desc()))
+    tail = (C.byref(lora.desc()), _dev(out, name, torch.float16), _dev(ws, "ws", ws.dtype),
+            ws.numel() * ws.element_size(), _stream(stream))
+    _one_device(plan, x, w.codes, lora.a, out, ws)
+    _check(fn, getattr(lib(), fn)(*head, *(() if layout is None else (layout,)), *tail))
+    return out
+
+
+def nvfp4_linear_lora(plan: torch.Tensor, x: torch.Tensor, w: NVFP4Tensor, lora: LoRATensor,
+                      y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_linear with each token's low-rank adapter: y = fp16(x W^T + scale_a (x A_a^T) B_a^T). plan:
+    nvfp4_moe_plan of the adapter ids [M, 1] over lora.adapters (-1: no adapter). Returns y [M, N]."""
+    return _linear_lora("nvfp4_linear_lora", plan, x, w, lora, None, y, "y", w.rows, ws, stream)
+
+
+def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tensor, lora: LoRATensor, layout: int = 0,
+                             h: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """nvfp4_linear_swiglu with each token's low-rank adapter on the gate and up rows (lora.rows = 2I, in
+    w13's row order) before SwiGLU. Returns h fp16 [M, I]."""
+    return _linear_lora("nvfp4_linear_swiglu_lora", plan, x, w13, lora, layout, h, "h", w13.rows // 2, ws, stream)

@@ -56,28 +56,32 @@ SAN_LIB = os.path.join(BUILD, "san", "libnvfp4moe_san.so")
 
 
 def build_host_sanitized(verbose: bool = False) -> str:
-    """A host-sanitizer build of the library for the host-side checks (tests/test_sanitizers.py):
-    abi.hip, which holds every argument check, compiled with AddressSanitizer and
-    UndefinedBehaviorSanitizer on its host code only (the device code is built as usual), linked
+    """A host-sanitizer build of the library for the host-side checks (tests/test_sanitizers.py): the
+    abi*.hip sources, which hold every argument check, compiled with AddressSanitizer and
+    UndefinedBehaviorSanitizer on their host code only (the device code is built as usual), linked
     with the regular objects of the other sources. Loaded into a Python that preloads clang's ASan
     runtime; it is never launched on a GPU."""
-    if not all(os.path.exists(os.path.join(BUILD, n)) for n in ("linear.o", "moe_gemm.o", "moe_plan.o",
-                                                                 "moe_prefill.o")):
+    names = sorted(os.path.splitext(os.path.basename(s))[0] for s in glob.glob(os.path.join(CSRC, "*.hip")))
+    checks = [n for n in names if n.startswith("abi")]
+    others = [os.path.join(BUILD, n + ".o") for n in names if n not in checks]
+    if not all(map(os.path.exists, others)):
         build(verbose)
     san = os.path.join(BUILD, "san")
     os.makedirs(san, exist_ok=True)
     host_san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                 "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
-    obj = os.path.join(san, "abi.o")
-    cmd = [HIPCC] + CFLAGS + host_san + ["-c", os.path.join(CSRC, "abi.hip"), "-o", obj]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed for abi.hip (host sanitizers):\n{r.stderr}")
-    others = [os.path.join(BUILD, n) for n in ("linear.o", "moe_gemm.o", "moe_plan.o", "moe_prefill.o")]
+    objs = []
+    for n in checks:
+        obj = os.path.join(san, n + ".o")
+        cmd = [HIPCC] + CFLAGS + host_san + ["-c", os.path.join(CSRC, n + ".hip"), "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed for {n}.hip (host sanitizers):\n{r.stderr}")
+        objs.append(obj)
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Xarch_host", "-fsanitize=address",
-           "-Xarch_host", "-fsanitize=undefined", "-shared-libsan", "-o", SAN_LIB, obj] + others
+           "-Xarch_host", "-fsanitize=undefined", "-shared-libsan", "-o", SAN_LIB] + objs + others
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

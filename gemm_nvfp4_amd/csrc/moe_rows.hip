@@ -1,0 +1,231 @@
+// moe_rows.hip -- rows moved by the routing plan: tokens sorted by expert (permute), expert rows summed
+// back into their tokens with the routing weights (unpermute), and that sum's gradient.
+//
+//   permute         xs[pos(p)] = w[p] x[t]                            p = t*topk + k, pos = pos_of_pair
+//   unpermute       out[t]     = sum_k w[p] ys[pos(p)]                in slot order, one fp16 rounding
+//   unpermute_grad  dys[pos(p)] = w[p] dout[t],  dw[p] = dout[t] . ys[pos(p)]
+//
+// All three only move rows, so HBM bounds them; the work is split by token (never by bucket row), so
+// that a token's own row is read or written once whatever topk is, and every bucket row once. A thread
+// holds one 16-byte piece (8 elements) of the token's row and walks the token's slots: the stores (or
+// loads) of all slots are in flight together. Elements are FP32 between the load and the one rounding.
+#include "nvfp4_device.hpp"
+#include "ops.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int ROW_THREADS = 256;
+constexpr int SLOTS = 16;  // slots whose rows are in flight at once
+
+__device__ __forceinline__ f16x8 round8(const float (&v)[8])
+{
+    f16x8 r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = f16_of_f32(v[e]);
+    return r;
+}
+
+// Index of this block along the token axis, which is split over x and z: a launch holds fewer than
+// 2^32 threads along one axis.
+constexpr int GRID_X = 1 << 20;
+__device__ __forceinline__ int token_block() { return (int)blockIdx.z * GRID_X + (int)blockIdx.x; }
+
+// This thread's token and piece: rows of 2^lg lanes (a block holds ROW_THREADS >> lg tokens), piece
+// segments over blockIdx.y. UNI: a wave lies within one token, whose index is then made wave-uniform, so
+// that positions and weights are scalar loads.
+template <bool UNI>
+__device__ __forceinline__ bool row_piece(int lg, int M, int pieces, int &t, int &pc)
+{
+    t = token_block() * (ROW_THREADS >> lg) + (int)(threadIdx.x >> lg);
+    if (UNI) t = __builtin_amdgcn_readfirstlane(t);
+    pc = (blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+    return t < M && pc < pieces;
+}
+
+template <bool UNI>
+__global__ __launch_bounds__(ROW_THREADS) void permute_kernel(const int32_t *__restrict__ pos_of_pair,
+                                                              const f16 *__restrict__ x, const float *__restrict__ w,
+                                                              int M, int topk, int pieces, int lg, f16 *__restrict__ xs)
+{
+    int t, pc;
+    if (!row_piece<UNI>(lg, M, pieces, t, pc)) return;
+    const f16x8 v = *reinterpret_cast<const f16x8 *>(x + ((size_t)t * pieces + pc) * 8);
+    const int32_t *pos = pos_of_pair + (size_t)t * topk;
+    for (int k = 0; k < topk; ++k) {
+        const int j = pos[k];
+        if (j < 0) continue;
+        f16x8 o = v;
+        if (w) {
+            const float wk = w[(size_t)t * topk + k];
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = wk * (float)v[e];
+            o = round8(f);
+        }
+        *reinterpret_cast<f16x8 *>(xs + ((size_t)j * pieces + pc) * 8) = o;
+    }
+}
+
+template <bool UNI>
+__global__ __launch_bounds__(ROW_THREADS) void unpermute_kernel(const int32_t *__restrict__ pos_of_pair,
+                                                                const f16 *__restrict__ ys, const float *__restrict__ w,
+                                                                int M, int topk, int pieces, int lg,
+                                                                f16 *__restrict__ out)
+{
+    int t, pc;
+    if (!row_piece<UNI>(lg, M, pieces, t, pc)) return;
+    const int32_t *pos = pos_of_pair + (size_t)t * topk;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < topk; k0 += SLOTS) {
+        f16x8 v[SLOTS];
+        int j[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) j[i] = k0 + i < topk ? pos[k0 + i] : -1;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            if (j[i] >= 0) v[i] = *reinterpret_cast<const f16x8 *>(ys + ((size_t)j[i] * pieces + pc) * 8);
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            if (j[i] >= 0) {
+                const float wk = w ? w[(size_t)t * topk + k0 + i] : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = fmaf(wk, (float)v[i][e], s[e]);
+            }
+    }
+    *reinterpret_cast<f16x8 *>(out + ((size_t)t * pieces + pc) * 8) = round8(s);
+}
+
+// Sums of SLOTS values over the wave's 64 lanes in 17 exchanges instead of 6 per value: in each of the
+// first four steps a lane hands over half of its values and keeps the sums of the other half. Lane l
+// ends with the sum of value slot_of_lane(l).
+__device__ __forceinline__ float wave_sums(float (&a)[SLOTS])
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = SLOTS / 2, o = 32; h >= 1; h >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float give = up ? a[i] : a[i + h];
+            const float keep = up ? a[i + h] : a[i];
+            a[i] = keep + __shfl_xor(give, o, 64);
+        }
+    }
+    float s = a[0];
+    s += __shfl_xor(s, 2, 64);
+    s += __shfl_xor(s, 1, 64);
+    return s;
+}
+__device__ __forceinline__ int slot_of_lane(int lane) { return lane >> 2; }
+
+// One block per token; its waves share the row's pieces, hold each slot's partial dot product in a
+// register and add them across the wave and, through LDS, across the waves in ascending order.
+__global__ __launch_bounds__(ROW_THREADS) void unpermute_grad_kernel(const int32_t *__restrict__ pos_of_pair,
+                                                                     const f16 *__restrict__ dout,
+                                                                     const f16 *__restrict__ ys,
+                                                                     const float *__restrict__ w, int M, int topk,
+                                                                     int pieces,
+                                                                     f16 *__restrict__ dys, float *__restrict__ dw)
+{
+    __shared__ float part[ROW_THREADS / 64][SLOTS];
+    const int t = token_block(), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (t >= M) return;  // the whole block
+    const int32_t *pos = pos_of_pair + (size_t)t * topk;
+    for (int k0 = 0; k0 < topk; k0 += SLOTS) {
+        int j[SLOTS];
+        float wk[SLOTS], acc[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            j[i] = k0 + i < topk ? pos[k0 + i] : -1;
+            wk[i] = dys && k0 + i < topk ? w[(size_t)t * topk + k0 + i] : 0.f;
+            acc[i] = 0.f;
+        }
+        for (int pc = threadIdx.x; pc < pieces; pc += blockDim.x) {
+            const f16x8 d = *reinterpret_cast<const f16x8 *>(dout + ((size_t)t * pieces + pc) * 8);
+            f16x8 v[SLOTS];
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (j[i] >= 0) v[i] = *reinterpret_cast<const f16x8 *>(ys + ((size_t)j[i] * pieces + pc) * 8);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (j[i] >= 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[i] = fmaf((float)d[e], (float)v[i][e], acc[i]);
+                    if (dys) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = wk[i] * (float)d[e];
+                        *reinterpret_cast<f16x8 *>(dys + ((size_t)j[i] * pieces + pc) * 8) = round8(f);
+                    }
+                }
+        }
+        const float sum = wave_sums(acc);
+        if (k0 > 0) __syncthreads();  // the previous slots' sums have been read
+        if ((lane & 3) == 0) part[wave][slot_of_lane(lane)] = sum;
+        __syncthreads();
+        const int i = threadIdx.x;
+        if (i < SLOTS && k0 + i < topk) {
+            float s = part[0][i];
+            for (int v = 1; v < (int)(blockDim.x >> 6); ++v) s += part[v][i];
+            dw[(size_t)t * topk + k0 + i] = s;  // a skipped pair's partial sums are all +0
+        }
+    }
+}
+
+// log2 of the lanes per row (16 to 256): the fewest idle lanes in the row's last segment, the widest
+// of equals.
+int row_lanes_log2(int pieces)
+{
+    int best = 8;
+    int64_t best_lanes = INT64_MAX;
+    for (int lg = 8; lg >= 4; --lg) {
+        const int64_t lanes = ((int64_t)(pieces + (1 << lg) - 1) >> lg) << lg;
+        if (lanes < best_lanes) best_lanes = lanes, best = lg;
+    }
+    return best;
+}
+
+dim3 token_grid(int64_t blocks, int segments)
+{
+    return dim3((unsigned)(blocks < GRID_X ? blocks : GRID_X), (unsigned)segments,
+                (unsigned)((blocks + GRID_X - 1) / GRID_X));
+}
+
+dim3 row_grid(int M, int pieces, int lg)
+{
+    const int rows = ROW_THREADS >> lg;
+    return token_grid(((int64_t)M + rows - 1) / rows, (pieces + (1 << lg) - 1) >> lg);
+}
+
+const f16 *half(const uint16_t *p) { return reinterpret_cast<const f16 *>(p); }
+f16 *half(uint16_t *p) { return reinterpret_cast<f16 *>(p); }
+
+}  // namespace
+
+int run_permute(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *x, const float *w, int32_t K, uint16_t *xs,
+                hipStream_t s)
+{
+    const int pieces = K / 8, lg = row_lanes_log2(pieces);
+    return launch(lg >= 6 ? permute_kernel<true> : permute_kernel<false>, row_grid(M, pieces, lg), dim3(ROW_THREADS), 0, s,
+                  pv.pos_of_pair, half(x), w, M, topk, pieces, lg, half(xs));
+}
+
+int run_unpermute(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *ys, const float *w, int32_t K,
+                  uint16_t *out, hipStream_t s)
+{
+    const int pieces = K / 8, lg = row_lanes_log2(pieces);
+    return launch(lg >= 6 ? unpermute_kernel<true> : unpermute_kernel<false>, row_grid(M, pieces, lg), dim3(ROW_THREADS), 0,
+                  s, pv.pos_of_pair, half(ys), w, M, topk, pieces, lg, half(out));
+}
+
+int run_unpermute_grad(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *dout, const uint16_t *ys,
+                       const float *w, int32_t K, uint16_t *dys, float *dw, hipStream_t s)
+{
+    const int pieces = K / 8;
+    const int threads = pieces >= ROW_THREADS ? ROW_THREADS : (pieces + 63) / 64 * 64;
+    return launch(unpermute_grad_kernel, token_grid(M, 1), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout),
+                  half(ys), w, M, topk, pieces, half(dys), dw);
+}
+
+}  // namespace nvfp4
