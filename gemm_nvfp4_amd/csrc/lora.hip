@@ -15,8 +15,10 @@
 //           i%4 for row i of tile t, a lane holds 16 consecutive outputs of one token after four tiles.
 // Rows without an adapter take pseudo tiles behind the plan's (16 consecutive pairs, those with an
 // adapter masked) and only copy, or finish, their base result.
+#include "linear_device.hpp"
 #include "nvfp4_device.hpp"
 #include "ops.hpp"
+#include "plan_device.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -80,30 +82,194 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(TileRows tr, 
     }
 }
 
+// ---- batches of many rows per adapter -------------------------------------------------------------
+// The unit is a run: up to 64 consecutive bucket rows of one adapter. Block b of an axis takes the b-th run,
+// which every wave finds from the plan's counts (256 adapters per step, two prefix sums over the wave).
+constexpr int RUN_ROWS = 64;
+
+struct RunRows {
+    const int32_t *counts, *sorted_pair;
+    int adapters, bucket;
+};
+
+struct Run {
+    int e, first, rows;  // adapter, first bucket row, rows (0: no such run)
+};
+
+__device__ __forceinline__ Run find_run(const RunRows &rr, int b)
+{
+    const int lane = threadIdx.x & 63;
+    int row0 = 0;
+    for (int e0 = 0; e0 < rr.adapters; e0 += 256) {
+        const int e = e0 + 4 * lane;
+        int c[4];
+        // the counts are followed by the plan's other arrays, so the last piece may be read whole
+        const int4 v = e < rr.adapters ? *reinterpret_cast<const int4 *>(rr.counts + e) : int4{0, 0, 0, 0};
+        c[0] = v.x, c[1] = e + 1 < rr.adapters ? v.y : 0, c[2] = e + 2 < rr.adapters ? v.z : 0,
+        c[3] = e + 3 < rr.adapters ? v.w : 0;
+        int runs = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) runs += (c[i] + RUN_ROWS - 1) / RUN_ROWS;
+        const int incl = wave_incl_scan(runs), rows_incl = wave_incl_scan(c[0] + c[1] + c[2] + c[3]);
+        const int total = __shfl(incl, 63, 64);
+        if (b < total) {
+            const int l = __ffsll(__ballot(incl > b)) - 1;
+            int left = b - __shfl(incl - runs, l, 64);
+            int first = row0 + __shfl(rows_incl - (c[0] + c[1] + c[2] + c[3]), l, 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ci = __shfl(c[i], l, 64), ri = (ci + RUN_ROWS - 1) / RUN_ROWS;
+                if (left < ri)
+                    return Run{__builtin_amdgcn_readfirstlane(e0 + 4 * l + i),
+                               __builtin_amdgcn_readfirstlane(first + left * RUN_ROWS),
+                               __builtin_amdgcn_readfirstlane(min(RUN_ROWS, ci - left * RUN_ROWS))};
+                left -= ri;
+                first += ci;
+            }
+        }
+        b -= total;
+        row0 += __shfl(rows_incl, 63, 64);
+    }
+    return Run{0, 0, 0};
+}
+
+__device__ __forceinline__ int run_row(const RunRows &rr, int bucket_row)
+{
+    return rr.bucket ? bucket_row : rr.sorted_pair[bucket_row];
+}
+
+// Shrink with A's chunk staged in LDS: one block per (run, chunk, group of RT 16-rank tiles), one wave per
+// 16 rows. A wave's rows of x go straight to registers, all 16 fragments in flight while A arrives by
+// direct-to-LDS loads.
+template <int RT>
+__global__ __launch_bounds__(256) void shrink_run_kernel(RunRows rr, const f16 *__restrict__ x, int64_t P, int K, int rank,
+                                                         const f16 *__restrict__ a, float *__restrict__ vp)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char as[RT * 16 * XS_PITCH];
+    const Run run = find_run(rr, blockIdx.x);
+    if (run.rows == 0) return;  // the whole block
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const int c = blockIdx.y, r0 = blockIdx.z * RT * 16;
+    const int kb = c * KCHUNK, steps = min(KCHUNK, K - kb) >> 5;
+    const int k = kb + 8 * lane;
+    for (int r = wave; r < RT * 16 && r0 + r < rank; r += 4) {
+        const f16 *src = a + ((size_t)run.e * rank + r0 + r) * K + (k < K ? k : 0);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                         (__attribute__((address_space(3))) void *)(as + r * XS_PITCH), 16, 0, 0);
+    }
+    const int rows = min(16, run.rows - 16 * wave);  // this wave's, none below 1
+    const bool mine = rows > 0;
+    const int row = mine ? run_row(rr, run.first + 16 * wave + (i < rows ? i : 0)) : 0;
+    f16x8 xf[16];
+    if (mine) {
+        const f16 *xp = x + (size_t)row * K + kb + 8 * q;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) xf[j] = *reinterpret_cast<const f16x8 *>(xp + 32 * (j < steps ? j : 0));
+    }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's direct-to-LDS loads have landed
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    lds_barrier();                       // and every other wave's
+    if (!mine) return;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int u = 0; u < RT; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    typedef const __attribute__((address_space(3))) f16x8 lds_f16x8;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if ((j & ~3) < steps) {  // K % 128 == 0: whole groups of four steps
+#pragma unroll
+            for (int u = 0; u < RT; ++u)
+                acc[u] = mfma_step(xf[j], *(lds_f16x8 *)(as + (16 * u + i) * XS_PITCH + 64 * j + 16 * q), acc[u]);
+        }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int src = 4 * q + n;
+        const int orow = __shfl(row, src, 64);
+        if (src < rows) {
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                const int r = r0 + 16 * u + i;
+                if (r < rank) vp[((size_t)c * P + orow) * rank + r] = acc[u][n];
+            }
+        }
+    }
+}
+
 // ---- expand ---------------------------------------------------------------------------------------
+// One wave per (row tile, range of column groups), no barriers: a lane folds the 8 ranks of its token that it
+// feeds (lane groups 0 and 2 the same ones, hi and lo), keeps the fragments of v in registers and streams B
+// and the base result past them.
 constexpr int EXPAND_WAVES = 4;
 constexpr int GROUP_COLS = 64;  // outputs of one token per wave and step
 
-// The 16 consecutive outputs n0 + 16q .. + 15 of the lane's token: d (scaled back), from hi and lo rows in
-// LDS.
-__device__ __forceinline__ void expand16(float (&d)[16], const f16 *be, int n0, int N, int rank, const f16 *hi,
-                                         const f16 *lo, int pitch, int i, int q)
+// The lane's 8 ranks of step s of its token's v: chunk partials added in ascending order.
+__device__ __forceinline__ void fold_v(float (&v)[8], const float *p, size_t plane, int S, bool valid)
 {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (!valid) return;
+    constexpr int CB = 8;  // chunks whose loads are issued before their adds
+    for (int c0 = 0; c0 < S; c0 += CB) {
+        f32x4 l[CB][2];
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+            if (c0 + c < S) {
+                l[c][0] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
+                l[c][1] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane + 4);
+            }
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+            if (c0 + c < S) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = c0 + c ? v[e] + l[c][0][e] : l[c][0][e];
+                    v[4 + e] = c0 + c ? v[4 + e] + l[c][1][e] : l[c][1][e];
+                }
+            }
+    }
+}
+
+// The power of two that brings a row's largest finite |v| to [2^12, 2^13), and the two fp16 terms of a
+// value scaled by it. Infinities and NaN stay in hi alone.
+__device__ __forceinline__ int shift_of(float big)
+{
+    return big > 0.f ? 13 - __builtin_amdgcn_frexp_expf(big) : 0;  // frexp: big = f 2^e, f in [1/2, 1)
+}
+__device__ __forceinline__ void split(float v, int sh, f16 &hi, f16 &lo)
+{
+    const float f = __builtin_amdgcn_ldexpf(v, sh);
+    hi = (f16)f;
+    lo = fabsf(f) < __builtin_inff() ? (f16)(f - (float)hi) : (f16)0.f;
+}
+
+// The 16 consecutive outputs n0 + 16q .. + 15 of the lane's token, still scaled.
+template <int RS>
+__device__ __forceinline__ void expand16(float (&d)[16], const f16x8 (&vf)[RS], const f16 *be, int n0, int N, int rank, int i,
+                                         int q)
+{
+    constexpr int SB = RS < 4 ? RS : 4;  // steps whose loads are issued together
     f32x4 acc[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const f16 *vrow = (q < 2 ? hi : lo) + i * pitch + 8 * (q & 1);
     const bool bv = n0 + 16 * (i >> 2) < N;
-    for (int r = 0; r < rank; r += 16) {
-        const bool rv = r + 8 * (q & 1) < rank;
-        const f16x8 vf = *reinterpret_cast<const f16x8 *>(vrow + r);
+    const f16 *bp = be + (size_t)(n0 + 16 * (i >> 2) + (i & 3)) * rank + 8 * (q & 1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int n = n0 + 16 * (i >> 2) + 4 * t + (i & 3);
-            f16x8 bf = zero8();
-            if (bv && rv) bf = *reinterpret_cast<const f16x8 *>(be + (size_t)n * rank + r + 8 * (q & 1));
-            acc[t] = mfma_step(bf, vf, acc[t]);
+    for (int s0 = 0; s0 < RS; s0 += SB) {
+        f16x8 bf[SB][4];
+#pragma unroll
+        for (int s = 0; s < SB; ++s) {
+            const bool v = bv && 16 * (s0 + s) + 8 * (q & 1) < rank;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                bf[s][t] = zero8();
+                if (v) bf[s][t] = *reinterpret_cast<const f16x8 *>(bp + (size_t)(4 * t) * rank + 16 * (s0 + s));
+            }
         }
+#pragma unroll
+        for (int s = 0; s < SB; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = mfma_step(bf[s][t], vf[s0 + s], acc[t]);
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -143,85 +309,72 @@ __device__ __forceinline__ void store_half(f16 *out, const float *v)
     }
 }
 
-// GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i.
-template <typename BASE, int GATE>
-__global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, int t_max, int64_t P, int S, int N,
+// GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i. The waves of a
+// block take consecutive column ranges of one tile.
+template <typename BASE, int GATE, int RS>
+__global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, int t_max, int t_all, int64_t P, int S, int N,
                                                                    int rank, const f16 *__restrict__ b,
                                                                    const float *__restrict__ scale,
                                                                    const float *__restrict__ vp, const BASE *base,
                                                                    f16 *out, int groups_per_wave)
 {
-    extern __shared__ unsigned char smem[];
-    __shared__ int s_row[TILE];
-    __shared__ int s_exp[TILE];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const int t = blockIdx.x;
+    const int t = blockIdx.x, g0 = (blockIdx.y * EXPAND_WAVES + wave) * groups_per_wave;
+    if (t >= t_all) return;
     const bool plain_rows = t >= t_max;  // rows without an adapter
-    const int pitch = ((rank + 15) & ~15) + 8;
-    float *v32 = reinterpret_cast<float *>(smem);                       // [16][pitch]
-    f16 *hi = reinterpret_cast<f16 *>(v32 + TILE * pitch), *lo = hi + TILE * pitch;
+    int row = -1, back = 0;
     float sc = 0.f;
     const f16 *be = b;
+    f16x8 vf[RS];
     if (plain_rows) {
-        if (threadIdx.x < TILE) {
-            const int64_t p = (int64_t)(t - t_max) * TILE + threadIdx.x;
-            s_row[threadIdx.x] = p < P && tr.pair_expert[p] < 0 ? (int)p : -1;
-        }
-        __syncthreads();
+        const int64_t p = (int64_t)(t - t_max) * TILE + i;
+        if (p < P && tr.pair_expert[p] < 0) row = (int)p;
     } else {
-        if (t >= tr.hdr[3]) return;  // the whole block
+        if (t >= tr.hdr[3]) return;
         const int rows = tr.tile_rows[t], e = tr.tile_expert[t];
+        if (i < rows) row = tile_row(tr, t, i);
         be = b + (size_t)e * N * rank;
         sc = scale[e];
-        if (threadIdx.x < TILE) s_row[threadIdx.x] = (int)threadIdx.x < rows ? tile_row(tr, t, threadIdx.x) : -1;
-        __syncthreads();
-        for (int o = threadIdx.x; o < TILE * pitch; o += blockDim.x) {
-            const int m = o / pitch, r = o - m * pitch;
-            float v = 0.f;
-            if (s_row[m] >= 0 && r < rank) {
-                const float *p = vp + (size_t)s_row[m] * rank + r;
-                v = p[0];
-                for (int c = 1; c < S; ++c) v += p[(size_t)c * P * rank];
-            }
-            v32[o] = v;
-        }
-        __syncthreads();
-        // 16 threads per row: the row's largest finite magnitude, then the split of the scaled row.
-        const int m = threadIdx.x >> 4, l = threadIdx.x & 15;
-        float big = 0.f;
-        for (int r = l; r < rank; r += 16) {
-            const float f = fabsf(v32[m * pitch + r]);
-            if (f < __builtin_inff()) big = fmaxf(big, f);
+        float v[RS][8], big = 0.f;
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+            const int r = 16 * s + 8 * (q & 1);
+            fold_v(v[s], vp + (size_t)(row < 0 ? 0 : row) * rank + r, (size_t)P * rank, S, row >= 0 && r < rank);
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 16));
-        const int sh = big > 0.f ? 13 - __builtin_amdgcn_frexp_expf(big) : 0;  // frexp: big = f 2^e, f in [1/2, 1)
-        if (l == 0) s_exp[m] = -sh;
-        for (int r = l; r < pitch; r += 16) {
-            const float f = __builtin_amdgcn_ldexpf(v32[m * pitch + r], sh);
-            const f16 h = (f16)f;
-            const float rest = f - (float)h;
-            hi[m * pitch + r] = h;
-            lo[m * pitch + r] = fabsf(f) < __builtin_inff() ? (f16)rest : (f16)0.f;  // infinities and NaN stay in hi
-        }
-        __syncthreads();
+        for (int s = 0; s < RS; ++s)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = fabsf(v[s][k]);
+                if (f < __builtin_inff()) big = fmaxf(big, f);
+            }
+        big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
+        const int sh = shift_of(big);
+        back = -sh;
+#pragma unroll
+        for (int s = 0; s < RS; ++s)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                f16 hi, lo;
+                split(v[s][k], sh, hi, lo);
+                vf[s][k] = q < 2 ? hi : lo;
+            }
     }
-    const int row = s_row[i];
-    const int back = plain_rows ? 0 : s_exp[i];
     const int I = N >> 1;
     const int cols = GATE == 1 ? I : N;  // columns that the groups cover
-    const int g0 = (blockIdx.y * EXPAND_WAVES + wave) * groups_per_wave;
     for (int g = g0; g < g0 + groups_per_wave && g * GROUP_COLS < cols; ++g) {
         const int n0 = g * GROUP_COLS, n = n0 + 16 * q;
-        float d[16], d2[16];
-        if (!plain_rows) {
-            expand16(d, be, n0, cols, rank, hi, lo, pitch, i, q);
-            if (GATE == 1) expand16(d2, be + (size_t)I * rank, n0, cols, rank, hi, lo, pitch, i, q);
+        const bool live = row >= 0 && n < cols;
+        float y[16], y2[16], d[16], d2[16];
+        if (live) {
+            load_base(y, base + (size_t)row * N + n);
+            if (GATE == 1) load_base(y2, base + (size_t)row * N + I + n);
         }
-        if (row < 0 || n >= cols) continue;
-        float y[16], y2[16];
-        load_base(y, base + (size_t)row * N + n);
-        if (GATE == 1) load_base(y2, base + (size_t)row * N + I + n);
+        if (!plain_rows) {
+            expand16<RS>(d, vf, be, n0, cols, rank, i, q);
+            if (GATE == 1) expand16<RS>(d2, vf, be + (size_t)I * rank, n0, cols, rank, i, q);
+        }
+        if (!live) continue;
         if (!plain_rows) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -243,6 +396,164 @@ __global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, 
     }
 }
 
+// ---- expand of runs (lora_add) --------------------------------------------------------------------
+// v folded and split once per row, in the order of the expand kernel's fragments: vs[row][r / 8] holds 8 hi
+// then 8 lo terms, shifts[row] the row's power of two. Rows without an adapter are folded too (whatever the
+// workspace holds) and never read. The blocks behind the folding ones copy those rows of y to out.
+constexpr int FOLD_THREADS = 256;
+
+__global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *__restrict__ vp, int64_t P, int S, int rank,
+                                                                  int lg, f16 *__restrict__ vs, int *__restrict__ shifts,
+                                                                  int64_t fold_blocks, const int32_t *__restrict__ pair_expert,
+                                                                  const f16 *y, int N, f16 *out)
+{
+    if ((int64_t)blockIdx.x >= fold_blocks) {  // one wave per row
+        const int64_t p = ((int64_t)blockIdx.x - fold_blocks) * (FOLD_THREADS / 64) + (threadIdx.x >> 6);
+        if (p >= P || pair_expert[p] >= 0) return;
+        for (int n = 8 * (threadIdx.x & 63); n < N; n += 512)
+            *reinterpret_cast<f16x8 *>(out + p * N + n) = *reinterpret_cast<const f16x8 *>(y + p * N + n);
+        return;
+    }
+    const int64_t row = (int64_t)blockIdx.x * (FOLD_THREADS >> lg) + (threadIdx.x >> lg);  // 2^lg lanes per row
+    const int r = 8 * (threadIdx.x & ((1 << lg) - 1));
+    const bool valid = row < P && r < rank;
+    float v[8], big = 0.f;
+    fold_v(v, vp + (valid ? row * rank + r : 0), (size_t)P * rank, S, valid);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float f = fabsf(v[e]);
+        if (f < __builtin_inff()) big = fmaxf(big, f);
+    }
+    for (int o = 1 << lg >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
+    if (!valid) return;
+    const int sh = shift_of(big);
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f16 h, l;
+        split(v[e], sh, h, l);
+        hi[e] = h, lo[e] = l;
+    }
+    f16 *o = vs + (row * rank + r) * 2;
+    *reinterpret_cast<f16x8 *>(o) = hi;
+    *reinterpret_cast<f16x8 *>(o + 8) = lo;
+    if (r == 0) shifts[row] = sh;
+}
+
+// out = y + d for a run's rows and a range of columns: a wave takes every fourth 64-column group of the
+// block's range, reads the group's B once for all of the run's tiles (their fragments of v stay in
+// registers), and has the next group's y in flight while it computes this one's.
+template <int RS>
+__global__ __launch_bounds__(256, RS > 4 ? 1 : 2) void expand_run_kernel(RunRows rr, int N, int rank, const f16 *__restrict__ b,
+                                                                         const float *__restrict__ scale,
+                                                                         const f16 *__restrict__ vs,
+                                                                         const int *__restrict__ shifts, const f16 *y, f16 *out,
+                                                                         int groups_per_wave)
+{
+    constexpr int TT = RS <= 4 ? 4 : RS <= 8 ? 2 : 1;  // row tiles whose v is held at once
+    constexpr int BATCH = RS <= 4 ? 1 : TT;              // tiles whose accumulators are live at once
+    const Run run = find_run(rr, blockIdx.x);
+    if (run.rows == 0) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const float sc = scale[run.e];
+    const f16 *be = b + (size_t)run.e * N * rank;
+    const int g0 = blockIdx.y * EXPAND_WAVES * groups_per_wave + wave;
+    const int g_end = min((int)(blockIdx.y + 1) * EXPAND_WAVES * groups_per_wave, (N + GROUP_COLS - 1) / GROUP_COLS);
+    for (int m0 = 0; m0 < run.rows; m0 += 16 * TT) {
+        int row[TT], back[TT];
+        f16x8 vf[TT][RS];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const int m = m0 + 16 * t + i;
+            row[t] = m < run.rows ? run_row(rr, run.first + m) : -1;
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            back[t] = row[t] >= 0 ? -shifts[row[t]] : 0;
+#pragma unroll
+            for (int s = 0; s < RS; ++s) {
+                const int r = 16 * s + 8 * (q & 1);
+                vf[t][s] = zero8();
+                if (row[t] >= 0 && r < rank)
+                    vf[t][s] = *reinterpret_cast<const f16x8 *>(vs + ((size_t)row[t] * rank + r) * 2 + 8 * (q >> 1));
+            }
+        }
+        f16x8 yt[TT][2];
+        auto load_y = [&](int t, int g) {
+            const int n = g * GROUP_COLS + 16 * q;
+            if (row[t] >= 0 && g < g_end && n < N) {
+                const f16 *p = y + (size_t)row[t] * N + n;
+                yt[t][0] = *reinterpret_cast<const f16x8 *>(p);
+                yt[t][1] = *reinterpret_cast<const f16x8 *>(p + 8);
+            }
+        };
+#pragma unroll
+        for (int t = 0; t < TT; ++t) load_y(t, g0);
+        for (int g = g0; g < g_end; g += EXPAND_WAVES) {
+            const int n0 = g * GROUP_COLS, n = n0 + 16 * q;
+            const bool bv = n0 + 16 * (i >> 2) < N;
+            const f16 *bp = be + (size_t)(n0 + 16 * (i >> 2) + (i & 3)) * rank + 8 * (q & 1);
+            auto load_b = [&](f16x8 (&bf)[4], int s) {
+                const bool v = bv && 16 * s + 8 * (q & 1) < rank;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    bf[u] = zero8();
+                    if (v) bf[u] = *reinterpret_cast<const f16x8 *>(bp + (size_t)(4 * u) * rank + 16 * s);
+                }
+            };
+            f32x4 acc[BATCH][4];
+            auto clear = [&]() {
+#pragma unroll
+                for (int t = 0; t < BATCH; ++t)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            };
+            // finishes tile t from its accumulators and takes up the next group's y in its place
+            auto finish = [&](int t, const f32x4 (&a)[4]) {
+                if (row[t] >= 0 && n < N) {
+                    f16 *o = out + (size_t)row[t] * N + n;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f16x8 v;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = f16_of_f32(fmaf(sc, __builtin_amdgcn_ldexpf(a[2 * h + (k >> 2)][k & 3], back[t]), (float)yt[t][h][k]));
+                        *reinterpret_cast<f16x8 *>(o + 8 * h) = v;
+                    }
+                }
+                load_y(t, g + EXPAND_WAVES);
+            };
+            if constexpr (RS <= 4) {  // the group's B in registers, tile after tile
+                f16x8 bf[RS][4];
+#pragma unroll
+                for (int s = 0; s < RS; ++s) load_b(bf[s], s);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    clear();
+#pragma unroll
+                    for (int s = 0; s < RS; ++s)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) acc[0][u] = mfma_step(bf[s][u], vf[t][s], acc[0][u]);
+                    finish(t, acc[0]);
+                }
+            } else {  // B step by step past the tiles' accumulators
+                clear();
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    f16x8 bf[4];
+                    load_b(bf, s);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) acc[t][u] = mfma_step(bf[u], vf[t][s], acc[t][u]);
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t) finish(t, acc[t]);
+            }
+        }
+    }
+}
+
 TileRows tile_rows(const PlanView &pv, int bucket)
 {
     return TileRows{pv.hdr, pv.tile_expert, pv.tile_base, pv.tile_rows, pv.tile_pair, pv.pair_expert, bucket};
@@ -250,40 +561,98 @@ TileRows tile_rows(const PlanView &pv, int bucket)
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// The run kernels, once adapters average at least 16 rows and the batch is not small.
+bool use_runs(int64_t P, int adapters) { return P >= 512 && P >= 16 * (int64_t)adapters; }
+
+template <int RT>
 int launch_shrink(const TileRows &tr, int64_t t_max, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp,
                   hipStream_t s)
 {
-    const int rt = (lora.rank + 15) / 16;
-    const dim3 block(SHRINK_WAVES * 64);
-    const unsigned gx = (unsigned)((t_max + SHRINK_WAVES - 1) / SHRINK_WAVES), gy = (unsigned)num_chunks(lora.k);
-    const f16 *a = reinterpret_cast<const f16 *>(lora.a);
-    if (rt == 1) return launch(shrink_kernel<1>, dim3(gx, gy), block, 0, s, tr, x, P, lora.k, lora.rank, a, vp);
-    if (rt == 2) return launch(shrink_kernel<2>, dim3(gx, gy), block, 0, s, tr, x, P, lora.k, lora.rank, a, vp);
-    return launch(shrink_kernel<4>, dim3(gx, gy, (unsigned)((rt + 3) / 4)), block, 0, s, tr, x, P, lora.k, lora.rank, a, vp);
+    const unsigned gy = (unsigned)num_chunks(lora.k), gz = (unsigned)((lora.rank + 16 * RT - 1) / (16 * RT));
+    return launch(shrink_kernel<RT>, dim3((unsigned)((t_max + SHRINK_WAVES - 1) / SHRINK_WAVES), gy, gz),
+                  dim3(SHRINK_WAVES * 64), 0, s, tr, x, P, lora.k, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp);
+}
+
+int launch_shrink(const TileRows &tr, int64_t t_max, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp,
+                  hipStream_t s)
+{
+    if (lora.rank <= 16) return launch_shrink<1>(tr, t_max, P, x, lora, vp, s);
+    if (lora.rank <= 32) return launch_shrink<2>(tr, t_max, P, x, lora, vp, s);
+    return launch_shrink<4>(tr, t_max, P, x, lora, vp, s);
+}
+
+template <typename BASE, int GATE, int RS>
+int launch_expand_rs(const TileRows &tr, int64_t t_max, int64_t P, bool others, const nvfp4_lora &lora, const float *vp,
+                     const BASE *base, f16 *out, hipStream_t s)
+{
+    const int N = lora.rows, cols = GATE == 1 ? N / 2 : N;
+    const int groups = (cols + GROUP_COLS - 1) / GROUP_COLS;
+    const int64_t tiles = t_max + (others ? (P + TILE - 1) / TILE : 0);
+    // about sixteen waves per CU of the device, at most 17 column groups each
+    int per_wave = (int)(tiles * groups / (16 * (int64_t)device_cus()));
+    per_wave = per_wave < 1 ? 1 : per_wave > 17 ? 17 : per_wave;
+    const int per_block = per_wave * EXPAND_WAVES;
+    return launch(expand_kernel<BASE, GATE, RS>, dim3((unsigned)tiles, (unsigned)((groups + per_block - 1) / per_block)),
+                  dim3(EXPAND_WAVES * 64), 0, s, tr, (int)t_max, (int)tiles, P, num_chunks(lora.k), N, lora.rank,
+                  reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base, out, per_wave);
 }
 
 template <typename BASE, int GATE>
 int launch_expand(const TileRows &tr, int64_t t_max, int64_t P, bool others, const nvfp4_lora &lora, const float *vp,
                   const BASE *base, f16 *out, hipStream_t s)
 {
-    const int N = lora.rows, cols = GATE == 1 ? N / 2 : N;
-    const int pitch = ((lora.rank + 15) & ~15) + 8;
-    const int groups = (cols + GROUP_COLS - 1) / GROUP_COLS;
-    const int64_t tiles = t_max + (others ? (P + TILE - 1) / TILE : 0);
-    int per_wave = (int)(tiles * groups / (16 * device_cus()));
-    if (per_wave < 1) per_wave = 1;
-    if (per_wave > 16) per_wave = 16;
-    const unsigned gy = (unsigned)((groups + EXPAND_WAVES * per_wave - 1) / (EXPAND_WAVES * per_wave));
-    return launch(expand_kernel<BASE, GATE>, dim3((unsigned)tiles, gy), dim3(EXPAND_WAVES * 64),
-                  (size_t)TILE * pitch * (sizeof(float) + 2 * sizeof(f16)), s, tr, (int)t_max, P, num_chunks(lora.k), N, lora.rank,
-                  reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base, out, per_wave);
+    const int rs = (lora.rank + 15) / 16;
+    if (rs <= 1) return launch_expand_rs<BASE, GATE, 1>(tr, t_max, P, others, lora, vp, base, out, s);
+    if (rs <= 2) return launch_expand_rs<BASE, GATE, 2>(tr, t_max, P, others, lora, vp, base, out, s);
+    if (rs <= 4) return launch_expand_rs<BASE, GATE, 4>(tr, t_max, P, others, lora, vp, base, out, s);
+    if (rs <= 8) return launch_expand_rs<BASE, GATE, 8>(tr, t_max, P, others, lora, vp, base, out, s);
+    return launch_expand_rs<BASE, GATE, 16>(tr, t_max, P, others, lora, vp, base, out, s);
+}
+
+// lora_add of a batch of runs: shrink, fold + split (and the rows without an adapter), expand.
+int add_runs(const PlanView &pv, int64_t P, int order, const f16 *x, const nvfp4_lora &lora, const f16 *y, f16 *out,
+             uint8_t *ws, hipStream_t s)
+{
+    const RunRows rr{pv.counts, pv.sorted_pair, lora.adapters, order};
+    const int N = lora.rows, rank = lora.rank, S = num_chunks(lora.k);
+    const size_t vp_bytes = round256((size_t)S * P * rank * sizeof(float));
+    float *vp = reinterpret_cast<float *>(ws);
+    f16 *vs = reinterpret_cast<f16 *>(ws + vp_bytes);
+    int *shifts = reinterpret_cast<int *>(ws + vp_bytes + round256((size_t)P * rank * 4));
+    const unsigned runs = (unsigned)((P < lora.adapters ? P : lora.adapters) + P / RUN_ROWS);
+    const f16 *a = reinterpret_cast<const f16 *>(lora.a), *b = reinterpret_cast<const f16 *>(lora.b);
+    int st;
+    if (rank <= 16) st = launch(shrink_run_kernel<1>, dim3(runs, S), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
+    else if (rank <= 32) st = launch(shrink_run_kernel<2>, dim3(runs, S), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
+    else st = launch(shrink_run_kernel<4>, dim3(runs, S, (rank + 63) / 64), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
+    if (st != NVFP4_OK) return st;
+    int lg = 0;
+    while ((8 << lg) < rank) ++lg;
+    const int64_t fold_blocks = (P + (FOLD_THREADS >> lg) - 1) / (FOLD_THREADS >> lg);
+    const int64_t copy_blocks = order == 0 && out != y ? (P + FOLD_THREADS / 64 - 1) / (FOLD_THREADS / 64) : 0;
+    st = launch(fold_split_kernel, dim3((unsigned)(fold_blocks + copy_blocks)), dim3(FOLD_THREADS), 0, s, vp, P, S, rank, lg,
+                vs, shifts, fold_blocks, pv.pair_expert, y, N, out);
+    if (st != NVFP4_OK) return st;
+    const int groups = (N + GROUP_COLS - 1) / GROUP_COLS;
+    // about two blocks per CU
+    int per_wave = (int)((int64_t)runs * groups / (EXPAND_WAVES * 2 * (int64_t)device_cus()));
+    per_wave = per_wave < 1 ? 1 : per_wave;
+    const dim3 grid(runs, (unsigned)((groups + EXPAND_WAVES * per_wave - 1) / (EXPAND_WAVES * per_wave)));
+    auto go = [&](auto *kernel) {
+        return launch(kernel, grid, dim3(256), 0, s, rr, N, rank, b, lora.scale, vs, shifts, y, out, per_wave);
+    };
+    const int rs = (rank + 15) / 16;
+    return rs <= 1 ? go(expand_run_kernel<1>) : rs <= 2 ? go(expand_run_kernel<2>) : rs <= 4 ? go(expand_run_kernel<4>)
+         : rs <= 8 ? go(expand_run_kernel<8>) : go(expand_run_kernel<16>);
 }
 
 }  // namespace
 
 size_t lora_add_ws_bytes(int64_t P, int32_t K, int32_t rank)
 {
-    return round256((size_t)num_chunks(K) * (size_t)P * rank * sizeof(float));
+    // chunk partials of v; v folded and split; its shifts
+    return round256((size_t)num_chunks(K) * (size_t)P * rank * sizeof(float)) + round256((size_t)P * rank * 4) +
+           round256((size_t)P * 4);
 }
 
 size_t linear_lora_ws_bytes(int32_t M, int32_t rows, int32_t K, int32_t rank)
@@ -294,6 +663,9 @@ size_t linear_lora_ws_bytes(int32_t M, int32_t rows, int32_t K, int32_t rank)
 int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const uint16_t *x, const nvfp4_lora &lora,
                  const uint16_t *y, uint16_t *out, void *ws, hipStream_t s)
 {
+    if (use_runs(L.P, lora.adapters))
+        return add_runs(pv, L.P, order, reinterpret_cast<const f16 *>(x), lora, reinterpret_cast<const f16 *>(y),
+                        reinterpret_cast<f16 *>(out), static_cast<uint8_t *>(ws), s);
     const TileRows tr = tile_rows(pv, order);
     float *vp = static_cast<float *>(ws);
     const int st = launch_shrink(tr, L.T, L.P, reinterpret_cast<const f16 *>(x), lora, vp, s);
