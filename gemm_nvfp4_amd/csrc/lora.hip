@@ -18,7 +18,6 @@
 #include "linear_device.hpp"
 #include "nvfp4_device.hpp"
 #include "ops.hpp"
-#include "plan_device.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -28,7 +27,7 @@ constexpr int TILE = PLAN_TILE_ROWS;  // 16 rows
 // Where the rows of a plan tile lie: pair order (row = pair index) or bucket order.
 struct TileRows {
     const int32_t *hdr, *tile_expert, *tile_base, *tile_rows, *tile_pair, *pair_expert;
-    int bucket;
+    int t_max, bucket;  // t_max: bound of the number of tiles
 };
 
 __device__ __forceinline__ int tile_row(const TileRows &tr, int t, int i)
@@ -83,114 +82,122 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(TileRows tr, 
 }
 
 // ---- batches of many rows per adapter -------------------------------------------------------------
-// The unit is a run: up to 64 consecutive bucket rows of one adapter. Block b of an axis takes the b-th run,
-// which every wave finds from the plan's counts (256 adapters per step, two prefix sums over the wave).
-constexpr int RUN_ROWS = 64;
+// A block takes a quad: four consecutive row tiles, one per wave. Tiles lie in adapter order, so a quad holds
+// one adapter or a few, and goes through them one after the other (nearly always one), staging that
+// adapter's matrix in LDS for the waves whose tile it is.
+constexpr int QUAD = 4;
 
-struct RunRows {
-    const int32_t *counts, *sorted_pair;
-    int adapters, bucket;
-};
-
-struct Run {
-    int e, first, rows;  // adapter, first bucket row, rows (0: no such run)
-};
-
-__device__ __forceinline__ Run find_run(const RunRows &rr, int b)
-{
-    const int lane = threadIdx.x & 63;
-    int row0 = 0;
-    for (int e0 = 0; e0 < rr.adapters; e0 += 256) {
-        const int e = e0 + 4 * lane;
-        int c[4];
-        // the counts are followed by the plan's other arrays, so the last piece may be read whole
-        const int4 v = e < rr.adapters ? *reinterpret_cast<const int4 *>(rr.counts + e) : int4{0, 0, 0, 0};
-        c[0] = v.x, c[1] = e + 1 < rr.adapters ? v.y : 0, c[2] = e + 2 < rr.adapters ? v.z : 0,
-        c[3] = e + 3 < rr.adapters ? v.w : 0;
-        int runs = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) runs += (c[i] + RUN_ROWS - 1) / RUN_ROWS;
-        const int incl = wave_incl_scan(runs), rows_incl = wave_incl_scan(c[0] + c[1] + c[2] + c[3]);
-        const int total = __shfl(incl, 63, 64);
-        if (b < total) {
-            const int l = __ffsll(__ballot(incl > b)) - 1;
-            int left = b - __shfl(incl - runs, l, 64);
-            int first = row0 + __shfl(rows_incl - (c[0] + c[1] + c[2] + c[3]), l, 64);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ci = __shfl(c[i], l, 64), ri = (ci + RUN_ROWS - 1) / RUN_ROWS;
-                if (left < ri)
-                    return Run{__builtin_amdgcn_readfirstlane(e0 + 4 * l + i),
-                               __builtin_amdgcn_readfirstlane(first + left * RUN_ROWS),
-                               __builtin_amdgcn_readfirstlane(min(RUN_ROWS, ci - left * RUN_ROWS))};
-                left -= ri;
-                first += ci;
-            }
-        }
-        b -= total;
-        row0 += __shfl(rows_incl, 63, 64);
+struct Quad {
+    int e0, e1, e2, e3;  // adapters of its tiles; -1 behind the last tile
+    __device__ __forceinline__ int adapter(int p) const { return p == 0 ? e0 : p == 1 ? e1 : p == 2 ? e2 : e3; }
+    // whether tile p is the first one of its adapter
+    __device__ __forceinline__ bool starts(int p) const
+    {
+        return adapter(p) >= 0 && (p == 0 || adapter(p) != adapter(p - 1));
     }
-    return Run{0, 0, 0};
-}
+};
 
-__device__ __forceinline__ int run_row(const RunRows &rr, int bucket_row)
+// The quad's adapters and, for this lane, row i of the wave's tile (-1 past its rows). All loads are issued
+// together: what the plan holds behind its last tile is some word, and is dropped.
+__device__ __forceinline__ Quad load_quad(const TileRows &tr, int quad, int &te, int &row)
 {
-    return rr.bucket ? bucket_row : rr.sorted_pair[bucket_row];
+    const int wave = threadIdx.x >> 6, i = threadIdx.x & 15, t0 = QUAD * quad, last = tr.t_max - 1;
+    const int n = tr.hdr[3], t = min(t0 + wave, last);
+    const int rows = tr.tile_rows[t], base = tr.bucket ? tr.tile_base[t] + i : tr.tile_pair[t * TILE + i];
+    Quad r{tr.tile_expert[t0], tr.tile_expert[min(t0 + 1, last)], tr.tile_expert[min(t0 + 2, last)],
+           tr.tile_expert[min(t0 + 3, last)]};
+    if (t0 >= n) r.e0 = -1;
+    if (t0 + 1 >= n) r.e1 = -1;
+    if (t0 + 2 >= n) r.e2 = -1;
+    if (t0 + 3 >= n) r.e3 = -1;
+    te = __builtin_amdgcn_readfirstlane(r.adapter(wave));
+    row = te >= 0 && i < rows ? base : -1;
+    return r;
 }
 
-// Shrink with A's chunk staged in LDS: one block per (run, chunk, group of RT 16-rank tiles), one wave per
-// 16 rows. A wave's rows of x go straight to registers, all 16 fragments in flight while A arrives by
-// direct-to-LDS loads.
+// Waits until at most `newest` of this wave's memory operations (the last ones issued) are outstanding.
+__device__ __forceinline__ void wait_all_but(int newest)
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if (newest == 2) __builtin_amdgcn_s_waitcnt(0x0F72);       // vmcnt(2); expcnt and lgkmcnt at their maxima
+    else if (newest == 1) __builtin_amdgcn_s_waitcnt(0x0F71);
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Shrink: one block per (quad, chunk, group of RT 16-rank tiles). A wave's rows of x go straight to
+// registers, all 16 fragments in flight while A arrives by direct-to-LDS loads in two halves of the chunk (a
+// whole chunk of 64 ranks would leave two blocks per CU). Half rows are 512 bytes without padding; the
+// 16-byte piece at place p of rank r is piece p ^ (r & 15), so that the fragment reads of 16 ranks fall into
+// distinct banks.
+constexpr int HALF = KCHUNK / 2;
+
 template <int RT>
-__global__ __launch_bounds__(256) void shrink_run_kernel(RunRows rr, const f16 *__restrict__ x, int64_t P, int K, int rank,
-                                                         const f16 *__restrict__ a, float *__restrict__ vp)
+__global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const f16 *__restrict__ x, int64_t P, int K, int rank,
+                                                          const f16 *__restrict__ a, float *__restrict__ vp)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char as[RT * 16 * XS_PITCH];
-    const Run run = find_run(rr, blockIdx.x);
-    if (run.rows == 0) return;  // the whole block
+    __shared__ __attribute__((aligned(16))) unsigned char as[RT * 16 * HALF * 2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    int te, row;
+    const Quad quad = load_quad(tr, blockIdx.x, te, row);
+    if (quad.e0 < 0) return;  // the whole block
     const int c = blockIdx.y, r0 = blockIdx.z * RT * 16;
     const int kb = c * KCHUNK, steps = min(KCHUNK, K - kb) >> 5;
-    const int k = kb + 8 * lane;
-    for (int r = wave; r < RT * 16 && r0 + r < rank; r += 4) {
-        const f16 *src = a + ((size_t)run.e * rank + r0 + r) * K + (k < K ? k : 0);
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                         (__attribute__((address_space(3))) void *)(as + r * XS_PITCH), 16, 0, 0);
-    }
-    const int rows = min(16, run.rows - 16 * wave);  // this wave's, none below 1
-    const bool mine = rows > 0;
-    const int row = mine ? run_row(rr, run.first + 16 * wave + (i < rows ? i : 0)) : 0;
     f16x8 xf[16];
-    if (mine) {
+    if (row >= 0) {  // lanes past the tile's rows feed whatever their registers hold into rows that are not stored
         const f16 *xp = x + (size_t)row * K + kb + 8 * q;
 #pragma unroll
         for (int j = 0; j < 16; ++j) xf[j] = *reinterpret_cast<const f16x8 *>(xp + 32 * (j < steps ? j : 0));
     }
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's direct-to-LDS loads have landed
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    lds_barrier();                       // and every other wave's
-    if (!mine) return;
-    f32x4 acc[RT];
-#pragma unroll
-    for (int u = 0; u < RT; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     typedef const __attribute__((address_space(3))) f16x8 lds_f16x8;
+#pragma unroll 1
+    for (int p = 0; p < QUAD; ++p) {
+        if (!quad.starts(p)) continue;  // the whole block
+        const unsigned char *ae = reinterpret_cast<const unsigned char *>(a + (size_t)quad.adapter(p) * rank * K);
+        // Two half rows per instruction: lanes 0-31 rank 2v, lanes 32-63 rank 2v + 1 of pair v. Pieces past K
+        // and ranks past the last one load their neighbours' bytes, which no result reads.
+        auto stage = [&](int half) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if ((j & ~3) < steps) {  // K % 128 == 0: whole groups of four steps
+            for (int v = 0; v < RT * 2; ++v) {
+                const int r = 2 * (wave + 4 * v) + (lane >> 5);
+                const int k = kb + half * HALF + 8 * ((lane & 31) ^ (r & 15));
+                const uint32_t off = 2u * ((uint32_t)min(r0 + r, rank - 1) * (uint32_t)K + (uint32_t)(k < K ? k : 0));
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(ae + off),
+                                                 (__attribute__((address_space(3))) void *)(as + (wave + 4 * v) * 1024), 16, 0, 0);
+            }
+        };
+        f32x4 acc[RT];
 #pragma unroll
-            for (int u = 0; u < RT; ++u)
-                acc[u] = mfma_step(xf[j], *(lds_f16x8 *)(as + (16 * u + i) * XS_PITCH + 64 * j + 16 * q), acc[u]);
+        for (int u = 0; u < RT; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool mine = te == quad.adapter(p);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half == 1 && steps <= 8) break;
+            if (p + half > 0) lds_barrier();  // the staged fragments have been read
+            stage(half);
+            wait_all_but(0);  // this wave's direct-to-LDS loads have landed
+            lds_barrier();    // and every other wave's
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * half + (j & ~3) < steps) {  // K % 128 == 0: whole groups of four steps
+#pragma unroll
+                        for (int u = 0; u < RT; ++u)
+                            acc[u] = mfma_step(xf[8 * half + j],
+                                               *(lds_f16x8 *)(as + (16 * u + i) * HALF * 2 + 16 * ((4 * j + q) ^ i)), acc[u]);
+                    }
+            }
         }
+        if (!mine) continue;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int src = 4 * q + n;
-        const int orow = __shfl(row, src, 64);
-        if (src < rows) {
+        for (int n = 0; n < 4; ++n) {
+            const int orow = __shfl(row, 4 * q + n, 64);
+            if (orow >= 0) {
 #pragma unroll
-            for (int u = 0; u < RT; ++u) {
-                const int r = r0 + 16 * u + i;
-                if (r < rank) vp[((size_t)c * P + orow) * rank + r] = acc[u][n];
+                for (int u = 0; u < RT; ++u) {
+                    const int r = r0 + 16 * u + i;
+                    if (r < rank) vp[((size_t)c * P + orow) * rank + r] = acc[u][n];
+                }
             }
         }
     }
@@ -396,8 +403,8 @@ __global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, 
     }
 }
 
-// ---- expand of runs (lora_add) --------------------------------------------------------------------
-// v folded and split once per row, in the order of the expand kernel's fragments: vs[row][r / 8] holds 8 hi
+// ---- expand of quads (lora_add) -------------------------------------------------------------------
+// v folded and split once per row, in the order of the expand kernels' fragments: vs[row][r / 8] holds 8 hi
 // then 8 lo terms, shifts[row] the row's power of two. Rows without an adapter are folded too (whatever the
 // workspace holds) and never read. The blocks behind the folding ones copy those rows of y to out.
 constexpr int FOLD_THREADS = 256;
@@ -405,13 +412,15 @@ constexpr int FOLD_THREADS = 256;
 __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *__restrict__ vp, int64_t P, int S, int rank,
                                                                   int lg, f16 *__restrict__ vs, int *__restrict__ shifts,
                                                                   int64_t fold_blocks, const int32_t *__restrict__ pair_expert,
-                                                                  const f16 *y, int N, f16 *out)
+                                                                  const f16 *__restrict__ y, int N, f16 *__restrict__ out)
 {
-    if ((int64_t)blockIdx.x >= fold_blocks) {  // one wave per row
-        const int64_t p = ((int64_t)blockIdx.x - fold_blocks) * (FOLD_THREADS / 64) + (threadIdx.x >> 6);
-        if (p >= P || pair_expert[p] >= 0) return;
-        for (int n = 8 * (threadIdx.x & 63); n < N; n += 512)
-            *reinterpret_cast<f16x8 *>(out + p * N + n) = *reinterpret_cast<const f16x8 *>(y + p * N + n);
+    if ((int64_t)blockIdx.x >= fold_blocks) {  // one block per row to copy (y and out are different buffers)
+        const int64_t p = (int64_t)blockIdx.x - fold_blocks;
+        if (pair_expert[p] >= 0) return;
+        const f16x8 *src = reinterpret_cast<const f16x8 *>(y + p * N);
+        f16x8 *dst = reinterpret_cast<f16x8 *>(out + p * N);
+#pragma unroll 4
+        for (int n = threadIdx.x; n < N / 8; n += FOLD_THREADS) dst[n] = src[n];
         return;
     }
     const int64_t row = (int64_t)blockIdx.x * (FOLD_THREADS >> lg) + (threadIdx.x >> lg);  // 2^lg lanes per row
@@ -440,129 +449,159 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
     if (r == 0) shifts[row] = sh;
 }
 
-// out = y + d for a run's rows and a range of columns: a wave takes every fourth 64-column group of the
-// block's range, reads the group's B once for all of the run's tiles (their fragments of v stay in
-// registers), and has the next group's y in flight while it computes this one's.
+// out = y + d for a quad's rows and a range of column groups. A group's B (64 rows of `rank` elements, one
+// contiguous piece of memory) is staged in LDS by direct-to-LDS loads, the next group's while this one is
+// computed; the accumulators go through LDS, so that y and out are read and written in whole 128-byte lines.
+// Fragments of v stay in registers. The MFMA's row operand is B (rows 16u + i of the group in tile u), so a
+// lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y; fragment loads of B and y straight
+// from memory (a lane a row: one 16-byte piece per cycle and CU) took twice the time.
+// LDS: B pieces of 8 ranks, piece p of row n at place p ^ swizzle(n); then 16 x D_PITCH floats per wave.
+constexpr int D_PITCH = GROUP_COLS + 4;
+
 template <int RS>
-__global__ __launch_bounds__(256, RS > 4 ? 1 : 2) void expand_run_kernel(RunRows rr, int N, int rank, const f16 *__restrict__ b,
-                                                                         const float *__restrict__ scale,
-                                                                         const f16 *__restrict__ vs,
-                                                                         const int *__restrict__ shifts, const f16 *y, f16 *out,
-                                                                         int groups_per_wave)
+struct BStage {
+    static constexpr int PIECES = 2 * RS;                 // 16-byte pieces per row, rank padded to 16 RS
+    static constexpr int BYTES = GROUP_COLS * PIECES * 16;
+    static constexpr int BUFFERS = RS <= 8 ? 2 : 1;
+    static constexpr size_t LDS = (size_t)BUFFERS * BYTES + (size_t)QUAD * TILE * D_PITCH * sizeof(float);
+    // rows of fewer than 16 pieces: row n of the 16 that a fragment read takes, by the bank slots they share
+    __device__ static __forceinline__ int place(int n, int p)
+    {
+        return PIECES >= 16 ? (p & ~15) | ((p ^ n) & 15) : p ^ ((n / (16 / PIECES)) & (PIECES - 1));
+    }
+};
+
+template <int RS>
+__global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, int rank, const f16 *__restrict__ b,
+                                                          const float *__restrict__ scale, const f16 *__restrict__ vs,
+                                                          const int *__restrict__ shifts, const f16 *y, f16 *out,
+                                                          int groups_per_block)
 {
-    constexpr int TT = RS <= 4 ? 4 : RS <= 8 ? 2 : 1;  // row tiles whose v is held at once
-    constexpr int BATCH = RS <= 4 ? 1 : TT;              // tiles whose accumulators are live at once
-    const Run run = find_run(rr, blockIdx.x);
-    if (run.rows == 0) return;
+    typedef BStage<RS> B;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const float sc = scale[run.e];
-    const f16 *be = b + (size_t)run.e * N * rank;
-    const int g0 = blockIdx.y * EXPAND_WAVES * groups_per_wave + wave;
-    const int g_end = min((int)(blockIdx.y + 1) * EXPAND_WAVES * groups_per_wave, (N + GROUP_COLS - 1) / GROUP_COLS);
-    for (int m0 = 0; m0 < run.rows; m0 += 16 * TT) {
-        int row[TT], back[TT];
-        f16x8 vf[TT][RS];
+    int te, row;
+    const Quad quad = load_quad(tr, blockIdx.x, te, row);
+    if (quad.e0 < 0) return;  // the whole block
+    const int g0 = blockIdx.y * groups_per_block, g_end = min(g0 + groups_per_block, (N + GROUP_COLS - 1) / GROUP_COLS);
+    // This lane's two pieces of a group's y and out: rows 8h + lane / 8, columns 8 (lane % 8) .. + 7.
+    const int c8 = 8 * (lane & 7);
+    int yrow[2];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int m = m0 + 16 * t + i;
-            row[t] = m < run.rows ? run_row(rr, run.first + m) : -1;
-        }
+    for (int h = 0; h < 2; ++h) yrow[h] = __shfl(row, 8 * h + (lane >> 3), 64);
+    float *dw = reinterpret_cast<float *>(smem + B::BUFFERS * B::BYTES) + wave * TILE * D_PITCH;
+    typedef __attribute__((address_space(3))) unsigned char lds_byte;
+    typedef const __attribute__((address_space(3))) f16x8 lds_f16x8;
+    f16x8 yv[2];
+    auto load_y = [&](int g) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            back[t] = row[t] >= 0 ? -shifts[row[t]] : 0;
+        for (int h = 0; h < 2; ++h)
+            if (yrow[h] >= 0 && g < g_end && g * GROUP_COLS + c8 < N)
+                yv[h] = *reinterpret_cast<const f16x8 *>(y + (size_t)yrow[h] * N + g * GROUP_COLS + c8);
+    };
+    f16x8 vf[RS];
+    float sc = 0.f;
+    int back = 0;
+#pragma unroll 1
+    for (int p = 0; p < QUAD; ++p) {
+        if (!quad.starts(p)) continue;  // the whole block
+        const bool mine = te == quad.adapter(p);
+        const unsigned char *be = reinterpret_cast<const unsigned char *>(b + (size_t)quad.adapter(p) * N * rank);
+        // Place l of the group's pieces (row n = l / PIECES) is filled with the piece that belongs there; pieces
+        // past the rank and rows past N are read as some other piece, and only ever meet zeros of v or columns
+        // that are not stored.
+        auto stage = [&](int g) {
+            const unsigned char *bg = be + (size_t)g * GROUP_COLS * rank * 2;
+            const int cols = N - g * GROUP_COLS;
+#pragma unroll
+            for (int v = 0; v < GROUP_COLS * B::PIECES / 256 || v == 0; ++v) {
+                const int first = (wave + QUAD * v) * 64, l = first + lane, n = l / B::PIECES;
+                if (B::PIECES == 2 && wave >= 2) break;  // 64 rows of two pieces: two waves' loads
+                const int piece = B::place(n, l % B::PIECES);  // its own inverse
+                const uint32_t off = 2u * ((uint32_t)min(n, cols - 1) * (uint32_t)rank + (uint32_t)(8 * piece < rank ? 8 * piece : 0));
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(bg + off),
+                                                 (__attribute__((address_space(3))) void *)(smem + (B::BUFFERS == 2 ? (g & 1) * B::BYTES : 0) +
+                                                                                            first * 16),
+                                                 16, 0, 0);
+            }
+        };
+        if (p > 0) lds_barrier();  // the staged fragments have been read
+        stage(g0);
+        if (mine) {
+            load_y(g0);
+            sc = scale[te];
+            back = row >= 0 ? -shifts[row] : 0;
 #pragma unroll
             for (int s = 0; s < RS; ++s) {
                 const int r = 16 * s + 8 * (q & 1);
-                vf[t][s] = zero8();
-                if (row[t] >= 0 && r < rank)
-                    vf[t][s] = *reinterpret_cast<const f16x8 *>(vs + ((size_t)row[t] * rank + r) * 2 + 8 * (q >> 1));
+                vf[s] = zero8();
+                if (row >= 0 && r < rank) vf[s] = *reinterpret_cast<const f16x8 *>(vs + ((size_t)row * rank + r) * 2 + 8 * (q >> 1));
             }
         }
-        f16x8 yt[TT][2];
-        auto load_y = [&](int t, int g) {
-            const int n = g * GROUP_COLS + 16 * q;
-            if (row[t] >= 0 && g < g_end && n < N) {
-                const f16 *p = y + (size_t)row[t] * N + n;
-                yt[t][0] = *reinterpret_cast<const f16x8 *>(p);
-                yt[t][1] = *reinterpret_cast<const f16x8 *>(p + 8);
-            }
-        };
+        int stores = 0;  // this wave's newest memory operations, wave-uniform
+        for (int g = g0; g < g_end; ++g) {
+            const int n0 = g * GROUP_COLS;
+            wait_all_but(stores);  // this wave's part of the group's B has landed
+            lds_barrier();         // and every other wave's; the other buffer has been read
+            f16x8 yc[2] = {yv[0], yv[1]};
+            if (B::BUFFERS == 2 && g + 1 < g_end) stage(g + 1);
+            if (mine) {
+                load_y(g + 1);
+                __builtin_amdgcn_sched_barrier(0);  // loads before the stores below, which the next wait leaves out
+                const unsigned char *bs = smem + (B::BUFFERS == 2 ? (g & 1) * B::BYTES : 0);
+                f32x4 acc[4];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) load_y(t, g0);
-        for (int g = g0; g < g_end; g += EXPAND_WAVES) {
-            const int n0 = g * GROUP_COLS, n = n0 + 16 * q;
-            const bool bv = n0 + 16 * (i >> 2) < N;
-            const f16 *bp = be + (size_t)(n0 + 16 * (i >> 2) + (i & 3)) * rank + 8 * (q & 1);
-            auto load_b = [&](f16x8 (&bf)[4], int s) {
-                const bool v = bv && 16 * s + 8 * (q & 1) < rank;
+                for (int u = 0; u < 4; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int n = 16 * u + i;
+                        acc[u] = mfma_step(*(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16), vf[s],
+                                           acc[u]);
+                    }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    bf[u] = zero8();
-                    if (v) bf[u] = *reinterpret_cast<const f16x8 *>(bp + (size_t)(4 * u) * rank + 16 * s);
+                    f32x4 d;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_ldexpf(acc[u][e], back);
+                    *reinterpret_cast<f32x4 *>(dw + i * D_PITCH + 16 * u + 4 * q) = d;
                 }
-            };
-            f32x4 acc[BATCH][4];
-            auto clear = [&]() {
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+                stores = 0;
 #pragma unroll
-                for (int t = 0; t < BATCH; ++t)
+                for (int h = 0; h < 2; ++h) {
+                    const float *sp = dw + (8 * h + (lane >> 3)) * D_PITCH + c8;
+                    const f32x4 lo = *reinterpret_cast<const f32x4 *>(sp), hi = *reinterpret_cast<const f32x4 *>(sp + 4);
+                    f16x8 o;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-            };
-            // finishes tile t from its accumulators and takes up the next group's y in its place
-            auto finish = [&](int t, const f32x4 (&a)[4]) {
-                if (row[t] >= 0 && n < N) {
-                    f16 *o = out + (size_t)row[t] * N + n;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f16x8 v;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[k] = f16_of_f32(fmaf(sc, __builtin_amdgcn_ldexpf(a[2 * h + (k >> 2)][k & 3], back[t]), (float)yt[t][h][k]));
-                        *reinterpret_cast<f16x8 *>(o + 8 * h) = v;
-                    }
+                    for (int e = 0; e < 8; ++e) o[e] = f16_of_f32(fmaf(sc, e < 4 ? lo[e & 3] : hi[e & 3], (float)yc[h][e]));
+                    const bool live = yrow[h] >= 0 && n0 + c8 < N;
+                    if (live) *reinterpret_cast<f16x8 *>(out + (size_t)yrow[h] * N + n0 + c8) = o;
+                    stores += __ballot(live) != 0;
                 }
-                load_y(t, g + EXPAND_WAVES);
-            };
-            if constexpr (RS <= 4) {  // the group's B in registers, tile after tile
-                f16x8 bf[RS][4];
-#pragma unroll
-                for (int s = 0; s < RS; ++s) load_b(bf[s], s);
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    clear();
-#pragma unroll
-                    for (int s = 0; s < RS; ++s)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) acc[0][u] = mfma_step(bf[s][u], vf[t][s], acc[0][u]);
-                    finish(t, acc[0]);
-                }
-            } else {  // B step by step past the tiles' accumulators
-                clear();
-#pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    f16x8 bf[4];
-                    load_b(bf, s);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) acc[t][u] = mfma_step(bf[u], vf[t][s], acc[t][u]);
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t) finish(t, acc[t]);
+                __builtin_amdgcn_wave_barrier();
+            }
+            if (B::BUFFERS == 1 && g + 1 < g_end) {
+                lds_barrier();  // the staged fragments have been read
+                stage(g + 1);
+                stores = 0;     // the staging loads are newer than the stores
             }
         }
     }
 }
 
-TileRows tile_rows(const PlanView &pv, int bucket)
+TileRows tile_rows(const PlanView &pv, const PlanLayout &L, int bucket)
 {
-    return TileRows{pv.hdr, pv.tile_expert, pv.tile_base, pv.tile_rows, pv.tile_pair, pv.pair_expert, bucket};
+    return TileRows{pv.hdr, pv.tile_expert, pv.tile_base, pv.tile_rows, pv.tile_pair, pv.pair_expert, (int)L.T, bucket};
 }
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// The run kernels, once adapters average at least 16 rows and the batch is not small.
-bool use_runs(int64_t P, int adapters) { return P >= 512 && P >= 16 * (int64_t)adapters; }
+// The quad kernels, once adapters average at least 16 rows and the batch is not small.
+bool use_quads(int64_t P, int adapters) { return P >= 512 && P >= 16 * (int64_t)adapters; }
 
 template <int RT>
 int launch_shrink(const TileRows &tr, int64_t t_max, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp,
@@ -609,41 +648,50 @@ int launch_expand(const TileRows &tr, int64_t t_max, int64_t P, bool others, con
     return launch_expand_rs<BASE, GATE, 16>(tr, t_max, P, others, lora, vp, base, out, s);
 }
 
-// lora_add of a batch of runs: shrink, fold + split (and the rows without an adapter), expand.
-int add_runs(const PlanView &pv, int64_t P, int order, const f16 *x, const nvfp4_lora &lora, const f16 *y, f16 *out,
-             uint8_t *ws, hipStream_t s)
+constexpr int QUAD_BLOCKS_PER_CU = 3;
+
+template <int RS>
+int launch_expand_quad(const TileRows &tr, const nvfp4_lora &lora, const f16 *vs, const int *shifts, const f16 *y, f16 *out,
+                       hipStream_t s)
 {
-    const RunRows rr{pv.counts, pv.sorted_pair, lora.adapters, order};
-    const int N = lora.rows, rank = lora.rank, S = num_chunks(lora.k);
+    const int groups = (lora.rows + GROUP_COLS - 1) / GROUP_COLS, quads = (tr.t_max + QUAD - 1) / QUAD;
+    int per_block = (int)((int64_t)quads * groups / (QUAD_BLOCKS_PER_CU * (int64_t)device_cus()));
+    per_block = per_block < 1 ? 1 : per_block;
+    const size_t lds = BStage<RS>::LDS;
+    static_assert(BStage<RS>::LDS <= 64 * 1024, "within the LDS that a launch may use without an opt-in");
+    return launch(expand_quad_kernel<RS>, dim3((unsigned)quads, (unsigned)((groups + per_block - 1) / per_block)), dim3(256), lds,
+                  s, tr, lora.rows, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vs, shifts, y, out, per_block);
+}
+
+// lora_add of a batch of quads: shrink, fold + split (and the rows without an adapter), expand.
+int add_quads(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lora, const f16 *y, f16 *out, uint8_t *ws,
+              hipStream_t s)
+{
+    const int rank = lora.rank, S = num_chunks(lora.k);
     const size_t vp_bytes = round256((size_t)S * P * rank * sizeof(float));
     float *vp = reinterpret_cast<float *>(ws);
     f16 *vs = reinterpret_cast<f16 *>(ws + vp_bytes);
     int *shifts = reinterpret_cast<int *>(ws + vp_bytes + round256((size_t)P * rank * 4));
-    const unsigned runs = (unsigned)((P < lora.adapters ? P : lora.adapters) + P / RUN_ROWS);
-    const f16 *a = reinterpret_cast<const f16 *>(lora.a), *b = reinterpret_cast<const f16 *>(lora.b);
+    const unsigned quads = (unsigned)((tr.t_max + QUAD - 1) / QUAD);
+    const f16 *a = reinterpret_cast<const f16 *>(lora.a);
     int st;
-    if (rank <= 16) st = launch(shrink_run_kernel<1>, dim3(runs, S), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
-    else if (rank <= 32) st = launch(shrink_run_kernel<2>, dim3(runs, S), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
-    else st = launch(shrink_run_kernel<4>, dim3(runs, S, (rank + 63) / 64), dim3(256), 0, s, rr, x, P, lora.k, rank, a, vp);
+    if (rank <= 16) st = launch(shrink_quad_kernel<1>, dim3(quads, S), dim3(256), 0, s, tr, x, P, lora.k, rank, a, vp);
+    else if (rank <= 32) st = launch(shrink_quad_kernel<2>, dim3(quads, S), dim3(256), 0, s, tr, x, P, lora.k, rank, a, vp);
+    else st = launch(shrink_quad_kernel<4>, dim3(quads, S, (rank + 63) / 64), dim3(256), 0, s, tr, x, P, lora.k, rank, a, vp);
     if (st != NVFP4_OK) return st;
     int lg = 0;
     while ((8 << lg) < rank) ++lg;
     const int64_t fold_blocks = (P + (FOLD_THREADS >> lg) - 1) / (FOLD_THREADS >> lg);
-    const int64_t copy_blocks = order == 0 && out != y ? (P + FOLD_THREADS / 64 - 1) / (FOLD_THREADS / 64) : 0;
+    const int64_t copy_blocks = !tr.bucket && out != y ? P : 0;
     st = launch(fold_split_kernel, dim3((unsigned)(fold_blocks + copy_blocks)), dim3(FOLD_THREADS), 0, s, vp, P, S, rank, lg,
-                vs, shifts, fold_blocks, pv.pair_expert, y, N, out);
+                vs, shifts, fold_blocks, tr.pair_expert, y, lora.rows, out);
     if (st != NVFP4_OK) return st;
-    const int groups = (N + GROUP_COLS - 1) / GROUP_COLS;
-    // about two blocks per CU
-    int per_wave = (int)((int64_t)runs * groups / (EXPAND_WAVES * 2 * (int64_t)device_cus()));
-    per_wave = per_wave < 1 ? 1 : per_wave;
-    const dim3 grid(runs, (unsigned)((groups + EXPAND_WAVES * per_wave - 1) / (EXPAND_WAVES * per_wave)));
-    auto go = [&](auto *kernel) {
-        return launch(kernel, grid, dim3(256), 0, s, rr, N, rank, b, lora.scale, vs, shifts, y, out, per_wave);
-    };
     const int rs = (rank + 15) / 16;
-    return rs <= 1 ? go(expand_run_kernel<1>) : rs <= 2 ? go(expand_run_kernel<2>) : rs <= 4 ? go(expand_run_kernel<4>)
-         : rs <= 8 ? go(expand_run_kernel<8>) : go(expand_run_kernel<16>);
+    return rs <= 1 ? launch_expand_quad<1>(tr, lora, vs, shifts, y, out, s)
+         : rs <= 2 ? launch_expand_quad<2>(tr, lora, vs, shifts, y, out, s)
+         : rs <= 4 ? launch_expand_quad<4>(tr, lora, vs, shifts, y, out, s)
+         : rs <= 8 ? launch_expand_quad<8>(tr, lora, vs, shifts, y, out, s)
+                   : launch_expand_quad<16>(tr, lora, vs, shifts, y, out, s);
 }
 
 }  // namespace
@@ -663,10 +711,10 @@ size_t linear_lora_ws_bytes(int32_t M, int32_t rows, int32_t K, int32_t rank)
 int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const uint16_t *x, const nvfp4_lora &lora,
                  const uint16_t *y, uint16_t *out, void *ws, hipStream_t s)
 {
-    if (use_runs(L.P, lora.adapters))
-        return add_runs(pv, L.P, order, reinterpret_cast<const f16 *>(x), lora, reinterpret_cast<const f16 *>(y),
-                        reinterpret_cast<f16 *>(out), static_cast<uint8_t *>(ws), s);
-    const TileRows tr = tile_rows(pv, order);
+    const TileRows tr = tile_rows(pv, L, order);
+    if (use_quads(L.P, lora.adapters))
+        return add_quads(tr, L.P, reinterpret_cast<const f16 *>(x), lora, reinterpret_cast<const f16 *>(y),
+                         reinterpret_cast<f16 *>(out), static_cast<uint8_t *>(ws), s);
     float *vp = static_cast<float *>(ws);
     const int st = launch_shrink(tr, L.T, L.P, reinterpret_cast<const f16 *>(x), lora, vp, s);
     if (st != NVFP4_OK) return st;
@@ -677,7 +725,7 @@ int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const u
 int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, int32_t M, const nvfp4_weights &w,
                     const nvfp4_lora &lora, bool gated, int32_t layout, uint16_t *y, void *ws, hipStream_t s)
 {
-    const TileRows tr = tile_rows(pv, 0);
+    const TileRows tr = tile_rows(pv, L, 0);
     float *base = static_cast<float *>(ws);
     float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256((size_t)M * w.rows * sizeof(float)));
     int st = run_linear_f32(x, M, w, base, s);
