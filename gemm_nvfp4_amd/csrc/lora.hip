@@ -30,52 +30,130 @@ struct TileRows {
     int t_max, bucket;  // t_max: bound of the number of tiles
 };
 
-__device__ __forceinline__ int tile_row(const TileRows &tr, int t, int i)
+// Waits until at most `newest` of this wave's memory operations (the last ones issued) are outstanding.
+__device__ __forceinline__ void wait_all_but(int newest)
 {
-    return tr.bucket ? tr.tile_base[t] + i : tr.tile_pair[t * TILE + i];
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if (newest == 2) __builtin_amdgcn_s_waitcnt(0x0F72);       // vmcnt(2); expcnt and lgkmcnt at their maxima
+    else if (newest == 1) __builtin_amdgcn_s_waitcnt(0x0F71);
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 // ---- shrink ---------------------------------------------------------------------------------------
-// One wave per (row tile, chunk, group of RT 16-rank tiles): vp[c][row][r] = the chunk's part of v.
-constexpr int SHRINK_WAVES = 4;  // consecutive row tiles of one chunk: tiles of one adapter share A in L1
-
-template <int RT>
-__global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(TileRows tr, const f16 *__restrict__ x, int64_t P,
-                                                                   int K, int rank, const f16 *__restrict__ a,
-                                                                   float *__restrict__ vp)
+// One wave per unit: (row tile t, 16-rank tile u, chunk c), chunks fastest; vp[c][row][r] = the chunk's
+// part of v. Lanes of rows past the tile's load nothing (a tile of a decode batch is often one row).
+__device__ __forceinline__ void shrink_unit(const TileRows &tr, int64_t unit, const f16 *x, int64_t P, int K, int rank,
+                                            const f16 *a, float *vp)
 {
     const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-    const int t = blockIdx.x * SHRINK_WAVES + (threadIdx.x >> 6);
-    const int c = blockIdx.y, r0 = blockIdx.z * RT * 16;
-    if (t >= tr.hdr[3]) return;  // wave-uniform
-    const int rows = tr.tile_rows[t];
-    const int row = tile_row(tr, t, i < rows ? i : 0);
-    const f16 *ae = a + (size_t)tr.tile_expert[t] * rank * K;
+    const int S = num_chunks(K), U = (rank + 15) >> 4;
+    const int c = (int)(unit % S), tu = (int)(unit / S), r0 = 16 * (tu % U), t = tu / U;
+    if (t >= tr.t_max) return;  // wave-uniform, as all below but the row
+    const int n = tr.hdr[3], e = tr.tile_expert[t], rows = tr.tile_rows[t];
+    const int at = tr.bucket ? tr.tile_base[t] + i : tr.tile_pair[t * TILE + i];
+    if (t >= n) return;
+    const int row = i < rows ? at : -1;
     const int kb = c * KCHUNK, steps = min(KCHUNK, K - kb) >> 5;
-    const f16 *xp = x + (size_t)row * K + kb + 8 * q;
-    const f16 *ap[RT];
+    const f16 *ap = a + ((size_t)e * rank + min(r0 + i, rank - 1)) * K + kb + 8 * q;
+    const f16 *xp = x + (size_t)(row < 0 ? 0 : row) * K + kb + 8 * q;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < RT; ++u) ap[u] = ae + (size_t)min(r0 + 16 * u + i, rank - 1) * K + kb + 8 * q;
-    f32x4 acc[RT];
+    for (int h = 0; h < 16; h += 8) {  // eight steps' loads in flight at once
+        f16x8 af[8], xf[8];
 #pragma unroll
-    for (int u = 0; u < RT; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < steps; j0 += 4)  // K % 128 == 0: whole groups of four steps
-#pragma unroll
-        for (int j = j0; j < j0 + 4; ++j) {
-            const f16x8 xf = *reinterpret_cast<const f16x8 *>(xp + 32 * j);
-#pragma unroll
-            for (int u = 0; u < RT; ++u)
-                acc[u] = mfma_step(xf, *reinterpret_cast<const f16x8 *>(ap[u] + 32 * j), acc[u]);
+        for (int j = 0; j < 8; ++j) {  // K % 128 == 0: whole groups of four steps
+            af[j] = xf[j] = zero8();
+            if (((h + j) & ~3) < steps) {
+                af[j] = *reinterpret_cast<const f16x8 *>(ap + 32 * (h + j));
+                if (row >= 0) xf[j] = *reinterpret_cast<const f16x8 *>(xp + 32 * (h + j));
+            }
         }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int src = 4 * q + e;
-        const int orow = __shfl(row, src, 64);
-        if (src < rows) {
+        for (int j = 0; j < 8; ++j)
+            if (((h + j) & ~3) < steps) acc = mfma_step(xf[j], af[j], acc);
+    }
 #pragma unroll
-            for (int u = 0; u < RT; ++u) {
-                const int r = r0 + 16 * u + i;
-                if (r < rank) vp[((size_t)c * P + orow) * rank + r] = acc[u][e];
+    for (int k = 0; k < 4; ++k) {
+        const int orow = __shfl(row, 4 * q + k, 64);
+        if (orow >= 0 && r0 + i < rank) vp[((size_t)c * P + orow) * rank + r0 + i] = acc[k];
+    }
+}
+
+constexpr int SHRINK_WAVES = 4;
+__global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(TileRows tr, const f16 *__restrict__ x, int64_t P, int K,
+                                                                   int rank, const f16 *__restrict__ a,
+                                                                   float *__restrict__ vp)
+{
+    shrink_unit(tr, (int64_t)blockIdx.x * SHRINK_WAVES + (threadIdx.x >> 6), x, P, K, rank, a, vp);
+}
+
+int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
+{
+    return (int64_t)tr.t_max * ((lora.rank + 15) / 16) * num_chunks(lora.k);
+}
+
+// ---- the projection's chunk products and the shrink in one launch ---------------------------------
+// Blocks [0, shrink_blocks) take shrink units. Each of the others takes one chunk and one 16-row weight tile
+// per wave, as the split-K form of the projection (linear.hip): part[c][m][n] is the library's chunk result,
+// so the sum over c is bitwise nvfp4_linear's. The weights decode anew for every 16 rows of x, which keeps a
+// wave within 128 registers and two blocks on a CU: the shrink's blocks, whose first loads wait for the
+// plan, then run beside the weight stream instead of behind it.
+constexpr int FUSED_ROWS = 32;   // activation rows staged in LDS per pass
+constexpr int FUSED_WAVES = 8;   // most waves per block
+
+__global__ __launch_bounds__(FUSED_WAVES * 64, 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
+                                                                            const uint8_t *__restrict__ codes,
+                                                                            const uint8_t *__restrict__ scales, int N, int K,
+                                                                            float *__restrict__ part, TileRows tr, int rank,
+                                                                            const f16 *__restrict__ a, float *__restrict__ vp,
+                                                                            int shrink_blocks)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char xs[FUSED_ROWS * XS_PITCH];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
+    if ((int)blockIdx.x < shrink_blocks) {
+        shrink_unit(tr, (int64_t)blockIdx.x * nwaves + wave, x, M, K, rank, a, vp);
+        return;
+    }
+    const int S = num_chunks(K), blk = (int)blockIdx.x - shrink_blocks, c = blk % S;
+    const int n = lane & 15, q = lane >> 4;
+    const int t = (blk / S) * nwaves + wave;  // this wave's weight tile
+    const bool tv = t < (N >> 4);             // wave-uniform
+    const int kb = c * KCHUNK;
+    const bool qv = q < (min(KCHUNK, K - kb) >> 7);
+    RawChunk w = RawChunk{};
+    if (tv && qv) {
+        const size_t row = (size_t)t * 16 + n;
+        w = load_chunk(codes + row * ((size_t)K >> 1), scales + row * ((size_t)K >> 4), kb, q);
+    }
+    const int k = kb + 8 * lane;
+    for (int m0 = 0; m0 < M; m0 += FUSED_ROWS) {
+        const int gm = min(M - m0, FUSED_ROWS);
+        if (m0 > 0) lds_barrier();  // the previous pass's fragment reads are done
+        for (int r = wave; r < gm; r += nwaves) {
+            const f16 *src = x + (size_t)(m0 + r) * K + (k < K ? k : 0);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                             (__attribute__((address_space(3))) void *)(xs + r * XS_PITCH), 16, 0, 0);
+        }
+        wait_all_but(0);  // this wave's direct-to-LDS loads (and weights) are done
+        lds_barrier();    // and every other wave's
+        if (!tv) continue;
+#pragma unroll 1
+        for (int rt = 0; rt * 16 < gm; ++rt) {
+            f16x8 af[4][4];
+            load_a_tile<A_STAGED>(af, x, make_rsrc(x, 0), xs, rt * 16 + n, gm, K, kb, q, qv);
+            keep_in_loop(w);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f16x2 sc = chunk_scales(w, b);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) acc = mfma_step(af[b][s], decode8(w.codes[b][s], sc[s >> 1]), acc);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int m = m0 + rt * 16 + 4 * q + j;
+                if (m < M) part[((size_t)c * M + m) * N + (size_t)t * 16 + n] = acc[j];
             }
         }
     }
@@ -113,16 +191,6 @@ __device__ __forceinline__ Quad load_quad(const TileRows &tr, int quad, int &te,
     te = __builtin_amdgcn_readfirstlane(r.adapter(wave));
     row = te >= 0 && i < rows ? base : -1;
     return r;
-}
-
-// Waits until at most `newest` of this wave's memory operations (the last ones issued) are outstanding.
-__device__ __forceinline__ void wait_all_but(int newest)
-{
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    if (newest == 2) __builtin_amdgcn_s_waitcnt(0x0F72);       // vmcnt(2); expcnt and lgkmcnt at their maxima
-    else if (newest == 1) __builtin_amdgcn_s_waitcnt(0x0F71);
-    else __builtin_amdgcn_s_waitcnt(0x0F70);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 // Shrink: one block per (quad, chunk, group of RT 16-rank tiles). A wave's rows of x go straight to
@@ -203,12 +271,12 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
     }
 }
 
-// ---- expand ---------------------------------------------------------------------------------------
-// One wave per (row tile, range of column groups), no barriers: a lane folds the 8 ranks of its token that it
-// feeds (lane groups 0 and 2 the same ones, hi and lo), keeps the fragments of v in registers and streams B
-// and the base result past them.
-constexpr int EXPAND_WAVES = 4;
-constexpr int GROUP_COLS = 64;  // outputs of one token per wave and step
+// ---- expand of tiles ------------------------------------------------------------------------------
+// One wave per (row tile, 64 columns): after the plan's words, one round of loads brings B, the base result and
+// the chunk partials of v, which a lane folds for the 8 ranks that it feeds (lane groups 0 and 2 the same ones,
+// hi and lo). Behind the plan's tiles lie pseudo tiles of 16 consecutive rows each, for the rows without an
+// adapter.
+constexpr int GROUP_COLS = 64;  // outputs of one token per wave
 
 // The lane's 8 ranks of step s of its token's v: chunk partials added in ascending order.
 __device__ __forceinline__ void fold_v(float (&v)[8], const float *p, size_t plane, int S, bool valid)
@@ -250,98 +318,114 @@ __device__ __forceinline__ void split(float v, int sh, f16 &hi, f16 &lo)
     lo = fabsf(f) < __builtin_inff() ? (f16)(f - (float)hi) : (f16)0.f;
 }
 
-// The 16 consecutive outputs n0 + 16q .. + 15 of the lane's token, still scaled.
-template <int RS>
-__device__ __forceinline__ void expand16(float (&d)[16], const f16x8 (&vf)[RS], const f16 *be, int n0, int N, int rank, int i,
-                                         int q)
+// The fragments of B for ranks 16s0 .. + 16SB - 1 of a group of 64 outputs: rows n0 + 16u + i in MFMA tile u, so
+// that a lane ends with the outputs n0 + 16u + 4q .. + 3 of token i.
+template <int SB>
+__device__ __forceinline__ void load_b(f16x8 (&bf)[SB][4], const f16 *be, int n0, int N, int rank, int s0, int i, int q)
 {
-    constexpr int SB = RS < 4 ? RS : 4;  // steps whose loads are issued together
-    f32x4 acc[4];
+    const f16 *bp = be + (size_t)(n0 + i) * rank + 8 * (q & 1);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const bool bv = n0 + 16 * (i >> 2) < N;
-    const f16 *bp = be + (size_t)(n0 + 16 * (i >> 2) + (i & 3)) * rank + 8 * (q & 1);
+    for (int s = 0; s < SB; ++s)
 #pragma unroll
-    for (int s0 = 0; s0 < RS; s0 += SB) {
-        f16x8 bf[SB][4];
+        for (int u = 0; u < 4; ++u) {
+            bf[s][u] = zero8();
+            if (n0 + 16 * u < N && 16 * (s0 + s) + 8 * (q & 1) < rank)  // N % 16 == 0
+                bf[s][u] = *reinterpret_cast<const f16x8 *>(bp + (size_t)(16 * u) * rank + 16 * (s0 + s));
+        }
+}
+
+// The base result of four consecutive outputs, in two steps: start() issues its loads (of the first chunks, for
+// chunk partials), finish() returns it in FP32.
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct BaseLoads;
+
+template <>
+struct BaseLoads<f16> {
+    f16x4 v;
+    __device__ __forceinline__ void start(const f16 *p, size_t, int) { v = *reinterpret_cast<const f16x4 *>(p); }
+    __device__ __forceinline__ f32x4 finish(const f16 *, size_t, int, float)
+    {
+        return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+    }
+};
+
+template <>
+struct BaseLoads<float> {
+    static constexpr int CB = 10;  // chunk planes whose loads are issued together
+    f32x4 v[CB];
+    __device__ __forceinline__ void load(const float *p, size_t plane, int c0, int S)
+    {
 #pragma unroll
-        for (int s = 0; s < SB; ++s) {
-            const bool v = bv && 16 * (s0 + s) + 8 * (q & 1) < rank;
+        for (int c = 0; c < CB; ++c)
+            if (c0 + c < S) v[c] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
+    }
+    __device__ __forceinline__ void start(const float *p, size_t plane, int S) { load(p, plane, 0, S); }
+    __device__ __forceinline__ f32x4 finish(const float *p, size_t plane, int S, float gs)
+    {
+        f32x4 y = v[0];
+        for (int c0 = 0; c0 < S; c0 += CB) {
+            if (c0 > 0) load(p, plane, c0, S);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                bf[s][t] = zero8();
-                if (v) bf[s][t] = *reinterpret_cast<const f16x8 *>(bp + (size_t)(4 * t) * rank + 16 * (s0 + s));
-            }
+            for (int c = 0; c < CB; ++c)
+                if (c0 + c < S && c0 + c > 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] += v[c][e];
+                }
         }
 #pragma unroll
-        for (int s = 0; s < SB; ++s)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t] = mfma_step(bf[s][t], vf[s0 + s], acc[t]);
+        for (int e = 0; e < 4; ++e) y[e] *= gs;
+        return y;
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[4 * t + e] = acc[t][e];
-}
+};
 
-__device__ __forceinline__ void load_base(float (&b)[16], const f16 *y)
-{
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const f16x8 v = *reinterpret_cast<const f16x8 *>(y + 8 * h);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) b[8 * h + e] = (float)v[e];
-    }
-}
+// Base: y fp16 [P][N] (T = f16), or Sb planes of FP32 [P][N] that are added in order and scaled by gscale[0]
+// (NULL: 1). GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i.
+// The accumulators go through LDS, so that the base result is read and the output written in whole row
+// segments: lane l finishes columns 4 (l % 16) .. + 3 of rows l / 16, l / 16 + 4, ... of the tile.
+constexpr int D_PITCH = GROUP_COLS + 4;
 
-__device__ __forceinline__ void load_base(float (&b)[16], const float *y)
+template <typename T, int GATE, int RS>
+__global__ __launch_bounds__(64) void expand_tile_kernel(TileRows tr, int64_t P, int S, int N, int rank,
+                                                         const f16 *__restrict__ b, const float *__restrict__ scale,
+                                                         const float *__restrict__ vp, const T *base, int Sb,
+                                                         const float *__restrict__ gscale, f16 *out)
 {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(y + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[4 * h + e] = v[e];
-    }
-}
-
-template <int N8>
-__device__ __forceinline__ void store_half(f16 *out, const float *v)
-{
-#pragma unroll
-    for (int h = 0; h < N8; ++h) {
-        f16x8 o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = f16_of_f32(v[8 * h + e]);
-        *reinterpret_cast<f16x8 *>(out + 8 * h) = o;
-    }
-}
-
-// GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i. The waves of a
-// block take consecutive column ranges of one tile.
-template <typename BASE, int GATE, int RS>
-__global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, int t_max, int t_all, int64_t P, int S, int N,
-                                                                   int rank, const f16 *__restrict__ b,
-                                                                   const float *__restrict__ scale,
-                                                                   const float *__restrict__ vp, const BASE *base,
-                                                                   f16 *out, int groups_per_wave)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const int t = blockIdx.x, g0 = (blockIdx.y * EXPAND_WAVES + wave) * groups_per_wave;
-    if (t >= t_all) return;
-    const bool plain_rows = t >= t_max;  // rows without an adapter
-    int row = -1, back = 0;
-    float sc = 0.f;
-    const f16 *be = b;
-    f16x8 vf[RS];
+    constexpr int SETS = GATE == 1 ? 2 : 1;      // column sets: gate and up rows apart
+    constexpr int SB = RS < 4 ? RS : 4;          // steps of B whose loads are issued together
+    __shared__ float dw[SETS][TILE][D_PITCH];
+    const int lane = threadIdx.x, i = lane & 15, q = lane >> 4;
+    const int t = blockIdx.x, n0 = blockIdx.y * GROUP_COLS, n = n0 + 4 * i;
+    const bool plain_rows = t >= tr.t_max;  // rows without an adapter
+    int row = -1, e = 0, rows = TILE;
     if (plain_rows) {
-        const int64_t p = (int64_t)(t - t_max) * TILE + i;
+        const int64_t p = (int64_t)(t - tr.t_max) * TILE + i;
         if (p < P && tr.pair_expert[p] < 0) row = (int)p;
     } else {
-        if (t >= tr.hdr[3]) return;
-        const int rows = tr.tile_rows[t], e = tr.tile_expert[t];
-        if (i < rows) row = tile_row(tr, t, i);
-        be = b + (size_t)e * N * rank;
-        sc = scale[e];
+        const int nt = tr.hdr[3], at = tr.bucket ? tr.tile_base[t] + i : tr.tile_pair[t * TILE + i];
+        rows = tr.tile_rows[t];
+        e = tr.tile_expert[t];
+        if (t >= nt) return;
+        if (i < rows) row = at;
+    }
+    const int I = N >> 1, cols = GATE == 1 ? I : N;
+    const size_t plane = (size_t)P * N;
+    const float gs = gscale ? gscale[0] : 1.0f;
+    auto start = [&](BaseLoads<T> (&bl)[SETS], int r) {
+        if (r < 0 || n >= cols) return;
+#pragma unroll
+        for (int z = 0; z < SETS; ++z) bl[z].start(base + (size_t)r * N + z * I + n, plane, Sb);
+    };
+    BaseLoads<T> bl[SETS];
+    const int first = __shfl(row, q, 64);  // this lane's row of the first round
+    float sc = 0.f;
+    if (!plain_rows) {
+        const f16 *be = b + (size_t)e * N * rank;
+        f16x8 bf[SETS][SB][4];
+#pragma unroll
+        for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
+        start(bl, first);
         float v[RS][8], big = 0.f;
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
@@ -357,48 +441,67 @@ __global__ __launch_bounds__(EXPAND_WAVES * 64) void expand_kernel(TileRows tr, 
             }
         big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
         const int sh = shift_of(big);
-        back = -sh;
+        f32x4 acc[SETS][4];
 #pragma unroll
-        for (int s = 0; s < RS; ++s)
+        for (int z = 0; z < SETS; ++z)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[z][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+            if (s > 0 && s % SB == 0) {
+#pragma unroll
+                for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, s, i, q);
+            }
+            f16x8 vf;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 f16 hi, lo;
                 split(v[s][k], sh, hi, lo);
-                vf[s][k] = q < 2 ? hi : lo;
+                vf[k] = q < 2 ? hi : lo;
             }
+#pragma unroll
+            for (int z = 0; z < SETS; ++z)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[z][u] = mfma_step(bf[z][s % SB][u], vf, acc[z][u]);
+        }
+#pragma unroll
+        for (int z = 0; z < SETS; ++z)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                f32x4 d;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_ldexpf(acc[z][u][k], -sh);
+                *reinterpret_cast<f32x4 *>(&dw[z][i][16 * u + 4 * q]) = d;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+        sc = scale[e];
+    } else {
+        start(bl, first);
     }
-    const int I = N >> 1;
-    const int cols = GATE == 1 ? I : N;  // columns that the groups cover
-    for (int g = g0; g < g0 + groups_per_wave && g * GROUP_COLS < cols; ++g) {
-        const int n0 = g * GROUP_COLS, n = n0 + 16 * q;
-        const bool live = row >= 0 && n < cols;
-        float y[16], y2[16], d[16], d2[16];
-        if (live) {
-            load_base(y, base + (size_t)row * N + n);
-            if (GATE == 1) load_base(y2, base + (size_t)row * N + I + n);
-        }
-        if (!plain_rows) {
-            expand16<RS>(d, vf, be, n0, cols, rank, i, q);
-            if (GATE == 1) expand16<RS>(d2, vf, be + (size_t)I * rank, n0, cols, rank, i, q);
-        }
-        if (!live) continue;
-        if (!plain_rows) {
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+        const int m = r0 + q, r = __shfl(row, m, 64);
+        if (r0 > 0) start(bl, r);
+        if (r < 0 || n >= cols) continue;
+        f32x4 y[SETS];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                y[e] = fmaf(sc, __builtin_amdgcn_ldexpf(d[e], back), y[e]);
-                if (GATE == 1) y2[e] = fmaf(sc, __builtin_amdgcn_ldexpf(d2[e], back), y2[e]);
+        for (int z = 0; z < SETS; ++z) {
+            y[z] = bl[z].finish(base + (size_t)r * N + z * I + n, plane, Sb, gs);
+            if (!plain_rows) {
+                const f32x4 d = *reinterpret_cast<const f32x4 *>(&dw[z][m][4 * i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[z][k] = fmaf(sc, d[k], y[z][k]);
             }
         }
-        if constexpr (GATE == 0) {
-            store_half<2>(out + (size_t)row * N + n, y);
-        } else if constexpr (GATE == 1) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = swiglu(y[e], y2[e]);
-            store_half<2>(out + (size_t)row * I + n, y);
+        if constexpr (GATE == 2) {
+            *reinterpret_cast<f16x2 *>(out + (size_t)r * I + (n >> 1)) =
+                f16x2{f16_of_f32(swiglu(y[0][0], y[0][1])), f16_of_f32(swiglu(y[0][2], y[0][3]))};
         } else {
+            f16x4 o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = swiglu(y[2 * e], y[2 * e + 1]);
-            store_half<1>(out + (size_t)row * I + (n >> 1), y);
+            for (int k = 0; k < 4; ++k) o[k] = f16_of_f32(GATE == 1 ? swiglu(y[0][k], y[SETS - 1][k]) : y[0][k]);
+            *reinterpret_cast<f16x4 *>(out + (size_t)r * cols + n) = o;
         }
     }
 }
@@ -456,8 +559,6 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
 // lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y; fragment loads of B and y straight
 // from memory (a lane a row: one 16-byte piece per cycle and CU) took twice the time.
 // LDS: B pieces of 8 ranks, piece p of row n at place p ^ swizzle(n); then 16 x D_PITCH floats per wave.
-constexpr int D_PITCH = GROUP_COLS + 4;
-
 template <int RS>
 struct BStage {
     static constexpr int PIECES = 2 * RS;                 // 16-byte pieces per row, rank padded to 16 RS
@@ -603,49 +704,36 @@ size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 // The quad kernels, once adapters average at least 16 rows and the batch is not small.
 bool use_quads(int64_t P, int adapters) { return P >= 512 && P >= 16 * (int64_t)adapters; }
 
-template <int RT>
-int launch_shrink(const TileRows &tr, int64_t t_max, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp,
+int launch_shrink(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp, hipStream_t s)
+{
+    const int64_t blocks = (shrink_units(tr, lora) + SHRINK_WAVES - 1) / SHRINK_WAVES;
+    return launch(shrink_kernel, dim3((unsigned)blocks), dim3(SHRINK_WAVES * 64), 0, s, tr, x, P, lora.k, lora.rank,
+                  reinterpret_cast<const f16 *>(lora.a), vp);
+}
+
+// Base result of the expand kernels: a finished y, or Sb planes with their scale.
+template <typename T>
+struct BaseOf {
+    const T *y;
+    int Sb;
+    const float *gscale;
+    bool others;  // rows without an adapter are written too
+};
+
+template <typename T, int GATE>
+int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const float *vp, const BaseOf<T> &base, f16 *out,
                   hipStream_t s)
 {
-    const unsigned gy = (unsigned)num_chunks(lora.k), gz = (unsigned)((lora.rank + 16 * RT - 1) / (16 * RT));
-    return launch(shrink_kernel<RT>, dim3((unsigned)((t_max + SHRINK_WAVES - 1) / SHRINK_WAVES), gy, gz),
-                  dim3(SHRINK_WAVES * 64), 0, s, tr, x, P, lora.k, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp);
-}
-
-int launch_shrink(const TileRows &tr, int64_t t_max, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp,
-                  hipStream_t s)
-{
-    if (lora.rank <= 16) return launch_shrink<1>(tr, t_max, P, x, lora, vp, s);
-    if (lora.rank <= 32) return launch_shrink<2>(tr, t_max, P, x, lora, vp, s);
-    return launch_shrink<4>(tr, t_max, P, x, lora, vp, s);
-}
-
-template <typename BASE, int GATE, int RS>
-int launch_expand_rs(const TileRows &tr, int64_t t_max, int64_t P, bool others, const nvfp4_lora &lora, const float *vp,
-                     const BASE *base, f16 *out, hipStream_t s)
-{
-    const int N = lora.rows, cols = GATE == 1 ? N / 2 : N;
-    const int groups = (cols + GROUP_COLS - 1) / GROUP_COLS;
-    const int64_t tiles = t_max + (others ? (P + TILE - 1) / TILE : 0);
-    // about sixteen waves per CU of the device, at most 17 column groups each
-    int per_wave = (int)(tiles * groups / (16 * (int64_t)device_cus()));
-    per_wave = per_wave < 1 ? 1 : per_wave > 17 ? 17 : per_wave;
-    const int per_block = per_wave * EXPAND_WAVES;
-    return launch(expand_kernel<BASE, GATE, RS>, dim3((unsigned)tiles, (unsigned)((groups + per_block - 1) / per_block)),
-                  dim3(EXPAND_WAVES * 64), 0, s, tr, (int)t_max, (int)tiles, P, num_chunks(lora.k), N, lora.rank,
-                  reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base, out, per_wave);
-}
-
-template <typename BASE, int GATE>
-int launch_expand(const TileRows &tr, int64_t t_max, int64_t P, bool others, const nvfp4_lora &lora, const float *vp,
-                  const BASE *base, f16 *out, hipStream_t s)
-{
-    const int rs = (lora.rank + 15) / 16;
-    if (rs <= 1) return launch_expand_rs<BASE, GATE, 1>(tr, t_max, P, others, lora, vp, base, out, s);
-    if (rs <= 2) return launch_expand_rs<BASE, GATE, 2>(tr, t_max, P, others, lora, vp, base, out, s);
-    if (rs <= 4) return launch_expand_rs<BASE, GATE, 4>(tr, t_max, P, others, lora, vp, base, out, s);
-    if (rs <= 8) return launch_expand_rs<BASE, GATE, 8>(tr, t_max, P, others, lora, vp, base, out, s);
-    return launch_expand_rs<BASE, GATE, 16>(tr, t_max, P, others, lora, vp, base, out, s);
+    const int N = lora.rows, cols = GATE == 1 ? N / 2 : N, rs = (lora.rank + 15) / 16;
+    const int64_t tiles = tr.t_max + (base.others ? (P + TILE - 1) / TILE : 0);
+    auto go = [&](auto *kernel) {
+        return launch(kernel, dim3((unsigned)tiles, (unsigned)((cols + GROUP_COLS - 1) / GROUP_COLS)), dim3(64), 0, s, tr, P,
+                      num_chunks(lora.k), N, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb,
+                      base.gscale, out);
+    };
+    return rs <= 1 ? go(expand_tile_kernel<T, GATE, 1>) : rs <= 2 ? go(expand_tile_kernel<T, GATE, 2>)
+         : rs <= 4 ? go(expand_tile_kernel<T, GATE, 4>) : rs <= 8 ? go(expand_tile_kernel<T, GATE, 8>)
+                   : go(expand_tile_kernel<T, GATE, 16>);
 }
 
 constexpr int QUAD_BLOCKS_PER_CU = 3;
@@ -703,38 +791,58 @@ size_t lora_add_ws_bytes(int64_t P, int32_t K, int32_t rank)
            round256((size_t)P * 4);
 }
 
+// Batches whose projection runs as chunk products beside the shrink; larger ones take the one-launch
+// projection into one FP32 plane.
+constexpr int FUSED_MAX_ROWS = 64;
+static int base_planes(int32_t M, int32_t K) { return M <= FUSED_MAX_ROWS ? num_chunks(K) : 1; }
+
 size_t linear_lora_ws_bytes(int32_t M, int32_t rows, int32_t K, int32_t rank)
 {
-    return round256((size_t)M * rows * sizeof(float)) + lora_add_ws_bytes(M, K, rank);
+    return round256((size_t)base_planes(M, K) * M * rows * sizeof(float)) +
+           round256((size_t)num_chunks(K) * (size_t)M * rank * sizeof(float));
 }
 
 int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const uint16_t *x, const nvfp4_lora &lora,
                  const uint16_t *y, uint16_t *out, void *ws, hipStream_t s)
 {
     const TileRows tr = tile_rows(pv, L, order);
-    if (use_quads(L.P, lora.adapters))
-        return add_quads(tr, L.P, reinterpret_cast<const f16 *>(x), lora, reinterpret_cast<const f16 *>(y),
-                         reinterpret_cast<f16 *>(out), static_cast<uint8_t *>(ws), s);
+    const f16 *xh = reinterpret_cast<const f16 *>(x), *yh = reinterpret_cast<const f16 *>(y);
+    f16 *oh = reinterpret_cast<f16 *>(out);
+    if (use_quads(L.P, lora.adapters)) return add_quads(tr, L.P, xh, lora, yh, oh, static_cast<uint8_t *>(ws), s);
     float *vp = static_cast<float *>(ws);
-    const int st = launch_shrink(tr, L.T, L.P, reinterpret_cast<const f16 *>(x), lora, vp, s);
+    const int st = launch_shrink(tr, L.P, xh, lora, vp, s);
     if (st != NVFP4_OK) return st;
-    return launch_expand<f16, 0>(tr, L.T, L.P, order == 0 && out != y, lora, vp, reinterpret_cast<const f16 *>(y),
-                                 reinterpret_cast<f16 *>(out), s);
+    return launch_expand<f16, 0>(tr, L.P, lora, vp, BaseOf<f16>{yh, 1, nullptr, order == 0 && out != y}, oh, s);
 }
 
 int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, int32_t M, const nvfp4_weights &w,
                     const nvfp4_lora &lora, bool gated, int32_t layout, uint16_t *y, void *ws, hipStream_t s)
 {
     const TileRows tr = tile_rows(pv, L, 0);
-    float *base = static_cast<float *>(ws);
-    float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256((size_t)M * w.rows * sizeof(float)));
-    int st = run_linear_f32(x, M, w, base, s);
-    if (st == NVFP4_OK) st = launch_shrink(tr, L.T, L.P, reinterpret_cast<const f16 *>(x), lora, vp, s);
+    const f16 *xh = reinterpret_cast<const f16 *>(x);
+    const int N = w.rows, K = w.k, S = num_chunks(K), planes = base_planes(M, K);
+    float *part = static_cast<float *>(ws);
+    float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256((size_t)planes * M * N * sizeof(float)));
+    int st;
+    if (M <= FUSED_MAX_ROWS) {
+        // about two blocks per CU, one unit (weight tile and chunk, or shrink unit) per wave
+        const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora), slots = 2 * (int64_t)device_cus();
+        int T = (int)((units + slots - 1) / slots);
+        T = T < 1 ? 1 : T > FUSED_WAVES ? FUSED_WAVES : T;
+        const int64_t shrink_blocks = (shrink_units(tr, lora) + T - 1) / T;
+        const int64_t blocks = shrink_blocks + (int64_t)S * ((N / 16 + T - 1) / T);
+        st = launch(linear_shrink_kernel, dim3((unsigned)blocks), dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K,
+                    part, tr, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp, (int)shrink_blocks);
+    } else {
+        st = run_linear_f32(x, M, w, part, s);
+        if (st == NVFP4_OK) st = launch_shrink(tr, L.P, xh, lora, vp, s);
+    }
     if (st != NVFP4_OK) return st;
+    const BaseOf<float> base{part, planes, M <= FUSED_MAX_ROWS ? w.global_scale : nullptr, true};
     f16 *o = reinterpret_cast<f16 *>(y);
-    if (!gated) return launch_expand<float, 0>(tr, L.T, L.P, true, lora, vp, base, o, s);
-    if (layout == 0) return launch_expand<float, 1>(tr, L.T, L.P, true, lora, vp, base, o, s);
-    return launch_expand<float, 2>(tr, L.T, L.P, true, lora, vp, base, o, s);
+    if (!gated) return launch_expand<float, 0>(tr, L.P, lora, vp, base, o, s);
+    if (layout == 0) return launch_expand<float, 1>(tr, L.P, lora, vp, base, o, s);
+    return launch_expand<float, 2>(tr, L.P, lora, vp, base, o, s);
 }
 
 }  // namespace nvfp4
