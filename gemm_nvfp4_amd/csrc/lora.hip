@@ -272,38 +272,34 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
 }
 
 // ---- expand of tiles ------------------------------------------------------------------------------
-// One wave per (row tile, 64 columns): after the plan's words, one round of loads brings B, the base result and
-// the chunk partials of v, which a lane folds for the 8 ranks that it feeds (lane groups 0 and 2 the same ones,
-// hi and lo). Behind the plan's tiles lie pseudo tiles of 16 consecutive rows each, for the rows without an
-// adapter.
-constexpr int GROUP_COLS = 64;  // outputs of one token per wave
+// One block per (row tile, 256 columns), one wave per 64 columns. After the plan's words, one round of loads
+// brings the chunk partials of v (folded by the block into LDS), B and the base result. Behind the plan's tiles
+// lie pseudo tiles of 16 consecutive rows each, for the rows without an adapter.
+constexpr int GROUP_COLS = 64;   // outputs of one token per wave
+constexpr int TILE_WAVES = 4;
 
-// The lane's 8 ranks of step s of its token's v: chunk partials added in ascending order.
-__device__ __forceinline__ void fold_v(float (&v)[8], const float *p, size_t plane, int S, bool valid)
-{
+// Four ranks of a row's v: its chunk partials added in ascending order, the loads of ten chunks in flight at
+// once.
+struct Fold4 {
+    f32x4 v;
+    __device__ __forceinline__ void run(const float *p, size_t plane, int S)
+    {
+        constexpr int CB = 10;
+        v = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c0 = 0; c0 < S; c0 += CB) {
+            f32x4 l[CB];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (!valid) return;
-    constexpr int CB = 8;  // chunks whose loads are issued before their adds
-    for (int c0 = 0; c0 < S; c0 += CB) {
-        f32x4 l[CB][2];
+            for (int c = 0; c < CB; ++c)
+                if (c0 + c < S) l[c] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
-            if (c0 + c < S) {
-                l[c][0] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
-                l[c][1] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane + 4);
-            }
+            for (int c = 0; c < CB; ++c)
+                if (c0 + c < S) {
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
-            if (c0 + c < S) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = c0 + c ? v[e] + l[c][0][e] : l[c][0][e];
-                    v[4 + e] = c0 + c ? v[4 + e] + l[c][1][e] : l[c][1][e];
+                    for (int e = 0; e < 4; ++e) v[e] = c0 + c ? v[e] + l[c][e] : l[c][e];
                 }
-            }
+        }
     }
-}
+};
 
 // The power of two that brings a row's largest finite |v| to [2^12, 2^13), and the two fp16 terms of a
 // value scaled by it. Infinities and NaN stay in hi alone.
@@ -334,69 +330,72 @@ __device__ __forceinline__ void load_b(f16x8 (&bf)[SB][4], const f16 *be, int n0
         }
 }
 
-// The base result of four consecutive outputs, in two steps: start() issues its loads (of the first chunks, for
-// chunk partials), finish() returns it in FP32.
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-
-template <typename T>
+// The base result of eight consecutive outputs, in two steps: start() issues its loads (of the first CB chunks,
+// for chunk partials), finish() returns it in FP32.
+template <typename T, int CB>
 struct BaseLoads;
 
-template <>
-struct BaseLoads<f16> {
-    f16x4 v;
-    __device__ __forceinline__ void start(const f16 *p, size_t, int) { v = *reinterpret_cast<const f16x4 *>(p); }
-    __device__ __forceinline__ f32x4 finish(const f16 *, size_t, int, float)
+template <int CB>
+struct BaseLoads<f16, CB> {
+    f16x8 v;
+    __device__ __forceinline__ void start(const f16 *p, size_t, int) { v = *reinterpret_cast<const f16x8 *>(p); }
+    __device__ __forceinline__ void finish(float (&y)[8], const f16 *, size_t, int, float)
     {
-        return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (float)v[e];
     }
 };
 
-template <>
-struct BaseLoads<float> {
-    static constexpr int CB = 10;  // chunk planes whose loads are issued together
-    f32x4 v[CB];
+template <int CB>
+struct BaseLoads<float, CB> {
+    f32x4 v[CB][2];
     __device__ __forceinline__ void load(const float *p, size_t plane, int c0, int S)
     {
 #pragma unroll
         for (int c = 0; c < CB; ++c)
-            if (c0 + c < S) v[c] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
+            if (c0 + c < S) {
+                v[c][0] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane);
+                v[c][1] = *reinterpret_cast<const f32x4 *>(p + (c0 + c) * plane + 4);
+            }
     }
     __device__ __forceinline__ void start(const float *p, size_t plane, int S) { load(p, plane, 0, S); }
-    __device__ __forceinline__ f32x4 finish(const float *p, size_t plane, int S, float gs)
+    __device__ __forceinline__ void finish(float (&y)[8], const float *p, size_t plane, int S, float gs)
     {
-        f32x4 y = v[0];
         for (int c0 = 0; c0 < S; c0 += CB) {
             if (c0 > 0) load(p, plane, c0, S);
 #pragma unroll
             for (int c = 0; c < CB; ++c)
-                if (c0 + c < S && c0 + c > 0) {
+                if (c0 + c < S) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] += v[c][e];
+                    for (int e = 0; e < 8; ++e) y[e] = c0 + c ? y[e] + v[c][e >> 2][e & 3] : v[c][e >> 2][e & 3];
                 }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] *= gs;
-        return y;
+        for (int e = 0; e < 8; ++e) y[e] *= gs;
     }
 };
 
 // Base: y fp16 [P][N] (T = f16), or Sb planes of FP32 [P][N] that are added in order and scaled by gscale[0]
 // (NULL: 1). GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i.
-// The accumulators go through LDS, so that the base result is read and the output written in whole row
-// segments: lane l finishes columns 4 (l % 16) .. + 3 of rows l / 16, l / 16 + 4, ... of the tile.
+// The accumulators go through LDS, so that the base result is read and the output written in row segments: lane
+// l finishes columns 8 (l % 8) .. + 7 of the wave's 64, of rows l / 8 and l / 8 + 8 of the tile.
 constexpr int D_PITCH = GROUP_COLS + 4;
 
 template <typename T, int GATE, int RS>
-__global__ __launch_bounds__(64) void expand_tile_kernel(TileRows tr, int64_t P, int S, int N, int rank,
-                                                         const f16 *__restrict__ b, const float *__restrict__ scale,
-                                                         const float *__restrict__ vp, const T *base, int Sb,
-                                                         const float *__restrict__ gscale, f16 *out)
+__global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows tr, int64_t P, int S, int N, int rank,
+                                                                      const f16 *__restrict__ b,
+                                                                      const float *__restrict__ scale,
+                                                                      const float *__restrict__ vp, const T *base, int Sb,
+                                                                      const float *__restrict__ gscale, f16 *out)
 {
     constexpr int SETS = GATE == 1 ? 2 : 1;      // column sets: gate and up rows apart
     constexpr int SB = RS < 4 ? RS : 4;          // steps of B whose loads are issued together
-    __shared__ float dw[SETS][TILE][D_PITCH];
-    const int lane = threadIdx.x, i = lane & 15, q = lane >> 4;
-    const int t = blockIdx.x, n0 = blockIdx.y * GROUP_COLS, n = n0 + 4 * i;
+    constexpr int CB = 10 / SETS;                // chunk planes whose loads are issued together
+    constexpr int V_PITCH = 16 * RS + 4;
+    __shared__ float v32[TILE * V_PITCH];
+    __shared__ float dw[TILE_WAVES][SETS][TILE][D_PITCH];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const int t = blockIdx.x, n0 = (blockIdx.y * TILE_WAVES + wave) * GROUP_COLS, n = n0 + 8 * (lane & 7);
     const bool plain_rows = t >= tr.t_max;  // rows without an adapter
     int row = -1, e = 0, rows = TILE;
     if (plain_rows) {
@@ -406,103 +405,126 @@ __global__ __launch_bounds__(64) void expand_tile_kernel(TileRows tr, int64_t P,
         const int nt = tr.hdr[3], at = tr.bucket ? tr.tile_base[t] + i : tr.tile_pair[t * TILE + i];
         rows = tr.tile_rows[t];
         e = tr.tile_expert[t];
-        if (t >= nt) return;
+        if (t >= nt) return;  // the whole block
         if (i < rows) row = at;
     }
     const int I = N >> 1, cols = GATE == 1 ? I : N;
     const size_t plane = (size_t)P * N;
     const float gs = gscale ? gscale[0] : 1.0f;
-    auto start = [&](BaseLoads<T> (&bl)[SETS], int r) {
+    BaseLoads<T, CB> bl[SETS];
+    auto start = [&](int r) {
         if (r < 0 || n >= cols) return;
 #pragma unroll
         for (int z = 0; z < SETS; ++z) bl[z].start(base + (size_t)r * N + z * I + n, plane, Sb);
     };
-    BaseLoads<T> bl[SETS];
-    const int first = __shfl(row, q, 64);  // this lane's row of the first round
-    float sc = 0.f;
-    if (!plain_rows) {
-        const f16 *be = b + (size_t)e * N * rank;
-        f16x8 bf[SETS][SB][4];
-#pragma unroll
-        for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
-        start(bl, first);
-        float v[RS][8], big = 0.f;
-#pragma unroll
-        for (int s = 0; s < RS; ++s) {
-            const int r = 16 * s + 8 * (q & 1);
-            fold_v(v[s], vp + (size_t)(row < 0 ? 0 : row) * rank + r, (size_t)P * rank, S, row >= 0 && r < rank);
-        }
-#pragma unroll
-        for (int s = 0; s < RS; ++s)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float f = fabsf(v[s][k]);
-                if (f < __builtin_inff()) big = fmaxf(big, f);
-            }
-        big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
-        const int sh = shift_of(big);
-        f32x4 acc[SETS][4];
-#pragma unroll
-        for (int z = 0; z < SETS; ++z)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) acc[z][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < RS; ++s) {
-            if (s > 0 && s % SB == 0) {
-#pragma unroll
-                for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, s, i, q);
-            }
-            f16x8 vf;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                f16 hi, lo;
-                split(v[s][k], sh, hi, lo);
-                vf[k] = q < 2 ? hi : lo;
-            }
-#pragma unroll
-            for (int z = 0; z < SETS; ++z)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[z][u] = mfma_step(bf[z][s % SB][u], vf, acc[z][u]);
-        }
-#pragma unroll
-        for (int z = 0; z < SETS; ++z)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                f32x4 d;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_ldexpf(acc[z][u][k], -sh);
-                *reinterpret_cast<f32x4 *>(&dw[z][i][16 * u + 4 * q]) = d;
-            }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-        sc = scale[e];
-    } else {
-        start(bl, first);
-    }
-    for (int r0 = 0; r0 < rows; r0 += 4) {
-        const int m = r0 + q, r = __shfl(row, m, 64);
-        if (r0 > 0) start(bl, r);
-        if (r < 0 || n >= cols) continue;
-        f32x4 y[SETS];
+    auto finish = [&](int m, int r, float sc) {
+        if (r < 0 || n >= cols) return;
+        float y[SETS][8];
 #pragma unroll
         for (int z = 0; z < SETS; ++z) {
-            y[z] = bl[z].finish(base + (size_t)r * N + z * I + n, plane, Sb, gs);
+            bl[z].finish(y[z], base + (size_t)r * N + z * I + n, plane, Sb, gs);
             if (!plain_rows) {
-                const f32x4 d = *reinterpret_cast<const f32x4 *>(&dw[z][m][4 * i]);
+                const float *dp = &dw[wave][z][m][8 * (lane & 7)];
+                const f32x4 d0 = *reinterpret_cast<const f32x4 *>(dp), d1 = *reinterpret_cast<const f32x4 *>(dp + 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[z][k] = fmaf(sc, d[k], y[z][k]);
+                for (int k = 0; k < 4; ++k) {
+                    y[z][k] = fmaf(sc, d0[k], y[z][k]);
+                    y[z][4 + k] = fmaf(sc, d1[k], y[z][4 + k]);
+                }
             }
         }
         if constexpr (GATE == 2) {
-            *reinterpret_cast<f16x2 *>(out + (size_t)r * I + (n >> 1)) =
-                f16x2{f16_of_f32(swiglu(y[0][0], y[0][1])), f16_of_f32(swiglu(y[0][2], y[0][3]))};
-        } else {
+            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
             f16x4 o;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = f16_of_f32(GATE == 1 ? swiglu(y[0][k], y[SETS - 1][k]) : y[0][k]);
-            *reinterpret_cast<f16x4 *>(out + (size_t)r * cols + n) = o;
+            for (int k = 0; k < 4; ++k) o[k] = f16_of_f32(swiglu(y[0][2 * k], y[0][2 * k + 1]));
+            *reinterpret_cast<f16x4 *>(out + (size_t)r * I + (n >> 1)) = o;
+        } else {
+            f16x8 o;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = f16_of_f32(GATE == 1 ? swiglu(y[0][k], y[SETS - 1][k]) : y[0][k]);
+            *reinterpret_cast<f16x8 *>(out + (size_t)r * cols + n) = o;
         }
+    };
+    const int m0 = lane >> 3, r_first = __shfl(row, m0, 64), r_second = __shfl(row, m0 + 8, 64);
+    if (plain_rows) {
+        start(r_first);
+        finish(m0, r_first, 0.f);
+        start(r_second);
+        finish(m0 + 8, r_second, 0.f);
+        return;
+    }
+    // v: one thread per four ranks of a row, all chunks in flight.
+    const int r4 = rank >> 2;
+    for (int task = threadIdx.x; task < rows * r4; task += TILE_WAVES * 64) {
+        const int m = task / r4, r = 4 * (task - m * r4);
+        const int vrow = tr.bucket ? tr.tile_base[t] + m : tr.tile_pair[t * TILE + m];
+        Fold4 f;
+        f.run(vp + (size_t)vrow * rank + r, (size_t)P * rank, S);
+        *reinterpret_cast<f32x4 *>(&v32[m * V_PITCH + r]) = f.v;
+    }
+    const f16 *be = b + (size_t)e * N * rank;
+    f16x8 bf[SETS][SB][4];
+#pragma unroll
+    for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
+    start(r_first);
+    lds_barrier();
+    float v[RS][8], big = 0.f;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        const int r = 16 * s + 8 * (q & 1);
+        const bool valid = row >= 0 && r < rank;
+        const f32x4 v0 = *reinterpret_cast<const f32x4 *>(&v32[i * V_PITCH + r]);
+        const f32x4 v1 = *reinterpret_cast<const f32x4 *>(&v32[i * V_PITCH + r + 4]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[s][k] = valid ? (k < 4 ? v0[k & 3] : v1[k & 3]) : 0.f;
+            const float f = fabsf(v[s][k]);
+            if (f < __builtin_inff()) big = fmaxf(big, f);
+        }
+    }
+    big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
+    const int sh = shift_of(big);
+    f32x4 acc[SETS][4];
+#pragma unroll
+    for (int z = 0; z < SETS; ++z)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[z][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        if (s > 0 && s % SB == 0) {
+#pragma unroll
+            for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, s, i, q);
+        }
+        f16x8 vf;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            f16 hi, lo;
+            split(v[s][k], sh, hi, lo);
+            vf[k] = q < 2 ? hi : lo;
+        }
+#pragma unroll
+        for (int z = 0; z < SETS; ++z)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[z][u] = mfma_step(bf[z][s % SB][u], vf, acc[z][u]);
+    }
+#pragma unroll
+    for (int z = 0; z < SETS; ++z)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            f32x4 d;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_ldexpf(acc[z][u][k], -sh);
+            *reinterpret_cast<f32x4 *>(&dw[wave][z][i][16 * u + 4 * q]) = d;
+        }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    const float sc = scale[e];
+    finish(m0, r_first, sc);
+    if (rows > 8) {  // wave-uniform
+        start(r_second);
+        finish(m0 + 8, r_second, sc);
     }
 }
 
@@ -529,11 +551,16 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
     const int64_t row = (int64_t)blockIdx.x * (FOLD_THREADS >> lg) + (threadIdx.x >> lg);  // 2^lg lanes per row
     const int r = 8 * (threadIdx.x & ((1 << lg) - 1));
     const bool valid = row < P && r < rank;
-    float v[8], big = 0.f;
-    fold_v(v, vp + (valid ? row * rank + r : 0), (size_t)P * rank, S, valid);
+    Fold4 v[2];
+    v[0].v = v[1].v = f32x4{0.f, 0.f, 0.f, 0.f};
+    float big = 0.f;
+    if (valid) {
+        v[0].run(vp + row * rank + r, (size_t)P * rank, S);
+        v[1].run(vp + row * rank + r + 4, (size_t)P * rank, S);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float f = fabsf(v[e]);
+        const float f = fabsf(v[e >> 2].v[e & 3]);
         if (f < __builtin_inff()) big = fmaxf(big, f);
     }
     for (int o = 1 << lg >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
@@ -543,7 +570,7 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         f16 h, l;
-        split(v[e], sh, h, l);
+        split(v[e >> 2].v[e & 3], sh, h, l);
         hi[e] = h, lo[e] = l;
     }
     f16 *o = vs + (row * rank + r) * 2;
@@ -727,7 +754,8 @@ int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f
     const int N = lora.rows, cols = GATE == 1 ? N / 2 : N, rs = (lora.rank + 15) / 16;
     const int64_t tiles = tr.t_max + (base.others ? (P + TILE - 1) / TILE : 0);
     auto go = [&](auto *kernel) {
-        return launch(kernel, dim3((unsigned)tiles, (unsigned)((cols + GROUP_COLS - 1) / GROUP_COLS)), dim3(64), 0, s, tr, P,
+        return launch(kernel, dim3((unsigned)tiles, (unsigned)((cols + TILE_WAVES * GROUP_COLS - 1) / (TILE_WAVES * GROUP_COLS))),
+                      dim3(TILE_WAVES * 64), 0, s, tr, P,
                       num_chunks(lora.k), N, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb,
                       base.gscale, out);
     };
