@@ -690,21 +690,33 @@ def _alloc(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _one_device(*tensors):
-    """Raise unless every tensor lies on the current device, where the launch goes."""
-    for t in tensors:
-        if t is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _opt(t, name: str, dtype: torch.dtype):
-    return None if t is None else _dev(t, name, dtype)
+def _current_device(t: torch.Tensor) -> int:
+    """The current device's index, or -1 for a tensor that is not on a GPU (which is then refused)."""
+    return _DEVICE() if t.is_cuda else -1
 
 
-def _row_plan(plan: torch.Tensor, M: int, topk: int, E: int):
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
+    """Device pointer of a contiguous tensor of this type on the current device, where the launch goes. The
+    checks of _dev in few steps, since a small call's host time is most of its time."""
+    if dev >= 0 and isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} lies on {t.device}, the current device is cuda:{dev}")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return stream.cuda_stream if stream is not None else _stream(None, dev)
+
+
+def _rows_plan(plan: torch.Tensor, M: int, topk: int, E: int, dev: int) -> int:
+    """Device pointer of a plan that is large enough (the calls take no plan size)."""
     need = _plan_bytes(M, topk, E)
-    if plan.numel() * plan.element_size() < need or need == 0:
+    if plan.numel() * plan.element_size() < need:
         _bytes(plan, "plan", need)
+    return _ptr(plan, "plan", torch.int32, dev)
 
 
 def nvfp4_moe_permute(plan: torch.Tensor, M: int, topk: int, E: int, x: torch.Tensor,
@@ -715,16 +727,16 @@ def nvfp4_moe_permute(plan: torch.Tensor, M: int, topk: int, E: int, x: torch.Te
     if x.dim() != 2 or x.shape[0] != M:
         raise ValueError(f"x must have shape ({M}, K), got {tuple(x.shape)}")
     K = x.shape[1]
-    _row_plan(plan, M, topk, E)
     if topk_weights is not None:
         _shape(topk_weights, "topk_weights", (M, topk))
     if xs is None:
         xs = _alloc((M * topk, K), torch.float16, x.device, stream)
     _rows(xs, "xs", M * topk, K)
-    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(x, "x", torch.float16),
-            _opt(topk_weights, "topk_weights", torch.float32), K, _dev(xs, "xs", torch.float16), _stream(stream))
-    _one_device(plan, x, topk_weights, xs)
-    _check("nvfp4_moe_permute", lib().nvfp4_moe_permute(*args))
+    dev = _current_device(plan)
+    _check("nvfp4_moe_permute", lib().nvfp4_moe_permute(
+        _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(x, "x", torch.float16, dev),
+        None if topk_weights is None else _ptr(topk_weights, "topk_weights", torch.float32, dev), K,
+        _ptr(xs, "xs", torch.float16, dev), _raw_stream(stream, dev)))
     return xs
 
 
@@ -737,16 +749,16 @@ def nvfp4_moe_unpermute(plan: torch.Tensor, M: int, topk: int, E: int, ys: torch
     if ys.dim() != 2 or ys.shape[0] < M * topk:
         raise ValueError(f"ys must have shape [>= {M * topk}, K], got {tuple(ys.shape)}")
     K = ys.shape[1]
-    _row_plan(plan, M, topk, E)
     if topk_weights is not None:
         _shape(topk_weights, "topk_weights", (M, topk))
     if out is None:
         out = _alloc((M, K), torch.float16, ys.device, stream)
     _shape(out, "out", (M, K))
-    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(ys, "ys", torch.float16),
-            _opt(topk_weights, "topk_weights", torch.float32), K, _dev(out, "out", torch.float16), _stream(stream))
-    _one_device(plan, ys, topk_weights, out)
-    _check("nvfp4_moe_unpermute", lib().nvfp4_moe_unpermute(*args))
+    dev = _current_device(plan)
+    _check("nvfp4_moe_unpermute", lib().nvfp4_moe_unpermute(
+        _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(ys, "ys", torch.float16, dev),
+        None if topk_weights is None else _ptr(topk_weights, "topk_weights", torch.float32, dev), K,
+        _ptr(out, "out", torch.float16, dev), _raw_stream(stream, dev)))
     return out
 
 
@@ -758,7 +770,6 @@ def nvfp4_moe_unpermute_grad(plan: torch.Tensor, M: int, topk: int, E: int, dout
     if dout.dim() != 2 or dout.shape[0] != M:
         raise ValueError(f"dout must have shape ({M}, K), got {tuple(dout.shape)}")
     K = dout.shape[1]
-    _row_plan(plan, M, topk, E)
     _rows(ys, "ys", M * topk, K)
     if topk_weights is not None:
         _shape(topk_weights, "topk_weights", (M, topk))
@@ -771,11 +782,13 @@ def nvfp4_moe_unpermute_grad(plan: torch.Tensor, M: int, topk: int, E: int, dout
     if dweights is None:
         dweights = _alloc((M, topk), torch.float32, dout.device, stream)
     _shape(dweights, "dweights", (M, topk))
-    args = (_dev(plan, "plan", torch.int32), M, topk, E, _dev(dout, "dout", torch.float16), _dev(ys, "ys", torch.float16),
-            _opt(topk_weights, "topk_weights", torch.float32), K, _opt(dys, "dys", torch.float16),
-            _dev(dweights, "dweights", torch.float32), _stream(stream))
-    _one_device(plan, dout, ys, topk_weights, dys, dweights)
-    _check("nvfp4_moe_unpermute_grad", lib().nvfp4_moe_unpermute_grad(*args))
+    dev = _current_device(plan)
+    _check("nvfp4_moe_unpermute_grad", lib().nvfp4_moe_unpermute_grad(
+        _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(dout, "dout", torch.float16, dev),
+        _ptr(ys, "ys", torch.float16, dev),
+        None if topk_weights is None else _ptr(topk_weights, "topk_weights", torch.float32, dev), K,
+        None if dys is None else _ptr(dys, "dys", torch.float16, dev), _ptr(dweights, "dweights", torch.float32, dev),
+        _raw_stream(stream, dev)))
     return dys, dweights
 
 
@@ -798,8 +811,9 @@ class LoRATensor:
         c = self.__dict__.get("_desc")
         if c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale:
             return c[3]
-        d = nvfp4_lora(_dev(self.a, "a", torch.float16), _dev(self.b, "b", torch.float16),
-                       _dev(self.scale, "scale", torch.float32), self.adapters, self.rows, self.k, self.rank)
+        dev = _current_device(self.a)
+        d = nvfp4_lora(_ptr(self.a, "a", torch.float16, dev), _ptr(self.b, "b", torch.float16, dev),
+                       _ptr(self.scale, "scale", torch.float32, dev), self.adapters, self.rows, self.k, self.rank)
         self._desc = (self.a, self.b, self.scale, d)
         return d
 
@@ -810,6 +824,11 @@ def nvfp4_lora_add_ws_bytes(P: int, K: int, rank: int) -> int:
 
 def nvfp4_linear_lora_ws_bytes(M: int, rows: int, K: int, rank: int) -> int:
     return int(lib().nvfp4_linear_lora_ws_bytes(M, rows, K, rank))
+
+
+# The sizes of the calls' workspaces, remembered per shape (pure functions of their arguments).
+_add_ws_bytes = functools.lru_cache(maxsize=256)(nvfp4_lora_add_ws_bytes)
+_linear_ws_bytes = functools.lru_cache(maxsize=256)(nvfp4_linear_lora_ws_bytes)
 
 
 def _lora_ws(ws, need: int, device, stream) -> torch.Tensor:
@@ -828,16 +847,16 @@ def nvfp4_lora_add(plan: torch.Tensor, M: int, topk: int, x: torch.Tensor, lora:
     P = M * topk
     _shape(x, "x", (P, lora.k))
     _shape(y, "y", (P, lora.rows))
-    _row_plan(plan, M, topk, lora.adapters)
     if out is None:
         out = _alloc((P, lora.rows), torch.float16, x.device, stream)
     _shape(out, "out", (P, lora.rows))
-    ws = _lora_ws(ws, nvfp4_lora_add_ws_bytes(P, lora.k, lora.rank), x.device, stream)
-    args = (_dev(plan, "plan", torch.int32), M, topk, order, _dev(x, "x", torch.float16), C.byref(lora.desc()),
-            _dev(y, "y", torch.float16), _dev(out, "out", torch.float16), _dev(ws, "ws", ws.dtype),
-            ws.numel() * ws.element_size(), _stream(stream))
-    _one_device(plan, x, lora.a, y, out, ws)
-    _check("nvfp4_lora_add", lib().nvfp4_lora_add(*args))
+    ws = _lora_ws(ws, _add_ws_bytes(P, lora.k, lora.rank), x.device, stream)
+    dev = _current_device(plan)
+    _ptr(lora.a, "lora.a", torch.float16, dev)  # the descriptor may have been built under another current device
+    _check("nvfp4_lora_add", lib().nvfp4_lora_add(
+        _rows_plan(plan, M, topk, lora.adapters, dev), M, topk, order, _ptr(x, "x", torch.float16, dev),
+        C.byref(lora.desc()), _ptr(y, "y", torch.float16, dev), _ptr(out, "out", torch.float16, dev),
+        _ptr(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
     return out
 
 
@@ -845,17 +864,18 @@ def _linear_lora(fn: str, plan, x, w: NVFP4Tensor, lora: LoRATensor, layout, out
     if x.dim() != 2 or x.shape[1] != w.k:
         raise ValueError(f"x must have shape (M, {w.k}), got {tuple(x.shape)}")
     M = x.shape[0]
-    if (lora.rows, lora.k) != (w.rows, w.k):
+    if lora.rows != w.rows or lora.k != w.k:
         raise ValueError(f"the adapters are for a {lora.rows} x {lora.k} weight, not {w.rows} x {w.k}")
-    _row_plan(plan, M, 1, lora.adapters)
     if out is None:
         out = _alloc((M, cols), torch.float16, x.device, stream)
     _shape(out, name, (M, cols))
-    ws = _lora_ws(ws, nvfp4_linear_lora_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
-    head = (_dev(plan, "plan", torch.int32), _dev(x, "x", torch.float16), M, C.byref(w.desc()))
-    tail = (C.byref(lora.desc()), _dev(out, name, torch.float16), _dev(ws, "ws", ws.dtype),
-            ws.numel() * ws.element_size(), _stream(stream))
-    _one_device(plan, x, w.codes, lora.a, out, ws)
+    ws = _lora_ws(ws, _linear_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
+    dev = _current_device(plan)
+    head = (_rows_plan(plan, M, 1, lora.adapters, dev), _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc()))
+    tail = (C.byref(lora.desc()), _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    # the descriptors may have been built under another current device
+    _ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(lora.a, "lora.a", torch.float16, dev)
     _check(fn, getattr(lib(), fn)(*head, *(() if layout is None else (layout,)), *tail))
     return out
 

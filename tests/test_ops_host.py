@@ -94,7 +94,7 @@ def test_linear_lora_refuses(L, gated):
     rows, k, rank, m = 64, 256, 16, 4
     w0 = lambda codes=fake, groups=1, rows=rows, k=k: C.byref(nvfp4_weights(codes, fake, fake, groups, rows, k))  # noqa: E731
     need = L.nvfp4_linear_lora_ws_bytes(m, rows, k, rank)
-    assert need >= m * rows * 4 + L.nvfp4_lora_add_ws_bytes(m, k, rank)
+    assert need >= m * rows * 4 + m * rank * 4 and need % 256 == 0
     assert L.nvfp4_linear_lora_ws_bytes(-1, rows, k, rank) == 0 and L.nvfp4_linear_lora_ws_bytes(m, 0, k, rank) == 0
 
     def call(plan=fake, x=fake, M=m, w=w0(), layout=0, lora=_lora(), y=fake, ws=fake, n=need):
