@@ -96,9 +96,10 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // ---- the projection's chunk products and the shrink in one launch ---------------------------------
 // Blocks [0, shrink_blocks) take shrink units. Each of the others takes one chunk and one 16-row weight tile
 // per wave, as the split-K form of the projection (linear.hip): part[c][m][n] is the library's chunk result,
-// so the sum over c is bitwise nvfp4_linear's. The weights decode anew for every 16 rows of x, which keeps a
-// wave within 128 registers and two blocks on a CU: the shrink's blocks, whose first loads wait for the
-// plan, then run beside the weight stream instead of behind it.
+// so the sum over c is bitwise nvfp4_linear's. The weights decode anew for every 16 rows of x: the 100
+// registers of a wave then let all blocks of a launch be resident at once, several to a CU, so that the
+// shrink's, whose first loads wait for the plan, run beside the weight stream (decoded weights kept for all
+// rows: 12.0 instead of 10.8 us at 32 rows of 4352 x 5120, 15.0 instead of 14.8 at 64).
 constexpr int FUSED_ROWS = 32;   // activation rows staged in LDS per pass
 constexpr int FUSED_WAVES = 8;   // most waves per block
 
@@ -194,17 +195,18 @@ __device__ __forceinline__ Quad load_quad(const TileRows &tr, int quad, int &te,
 }
 
 // Shrink: one block per (quad, chunk, group of RT 16-rank tiles). A wave's rows of x go straight to
-// registers, all 16 fragments in flight while A arrives by direct-to-LDS loads in two halves of the chunk (a
-// whole chunk of 64 ranks would leave two blocks per CU). Half rows are 512 bytes without padding; the
-// 16-byte piece at place p of rank r is piece p ^ (r & 15), so that the fragment reads of 16 ranks fall into
-// distinct banks.
-constexpr int HALF = KCHUNK / 2;
+// registers, all 16 fragments in flight while A arrives by direct-to-LDS loads: for 64 ranks in two halves of
+// the chunk (a whole one would leave two blocks per CU: 22.4 instead of 18.6 us at 4096 rows, rank 64, K =
+// 5120), else at once. Staged rows have no padding; the 16-byte piece at place p of rank r is piece
+// p ^ (r & 15), so that the fragment reads of 16 ranks fall into distinct banks.
 
 template <int RT>
 __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const f16 *__restrict__ x, int64_t P, int K, int rank,
                                                           const f16 *__restrict__ a, float *__restrict__ vp)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char as[RT * 16 * HALF * 2];
+    constexpr int PHASES = RT == 4 ? 2 : 1, PART = KCHUNK / PHASES;  // elements of a rank staged at once
+    constexpr int RPI = 512 / PART;                                  // ranks per 1 KB instruction
+    __shared__ __attribute__((aligned(16))) unsigned char as[RT * 16 * PART * 2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
     int te, row;
     const Quad quad = load_quad(tr, blockIdx.x, te, row);
@@ -222,16 +224,15 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
     for (int p = 0; p < QUAD; ++p) {
         if (!quad.starts(p)) continue;  // the whole block
         const unsigned char *ae = reinterpret_cast<const unsigned char *>(a + (size_t)quad.adapter(p) * rank * K);
-        // Two half rows per instruction: lanes 0-31 rank 2v, lanes 32-63 rank 2v + 1 of pair v. Pieces past K
-        // and ranks past the last one load their neighbours' bytes, which no result reads.
-        auto stage = [&](int half) {
+        // Pieces past K and ranks past the last one load other bytes of the matrix, which no result reads.
+        auto stage = [&](int phase) {
 #pragma unroll
-            for (int v = 0; v < RT * 2; ++v) {
-                const int r = 2 * (wave + 4 * v) + (lane >> 5);
-                const int k = kb + half * HALF + 8 * ((lane & 31) ^ (r & 15));
+            for (int v = 0; v < RT * 4 / RPI; ++v) {
+                const int r = RPI * (wave + QUAD * v) + lane / (64 / RPI);
+                const int k = kb + phase * PART + 8 * ((lane % (64 / RPI)) ^ (r & 15));
                 const uint32_t off = 2u * ((uint32_t)min(r0 + r, rank - 1) * (uint32_t)K + (uint32_t)(k < K ? k : 0));
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(ae + off),
-                                                 (__attribute__((address_space(3))) void *)(as + (wave + 4 * v) * 1024), 16, 0, 0);
+                                                 (__attribute__((address_space(3))) void *)(as + (wave + QUAD * v) * 1024), 16, 0, 0);
             }
         };
         f32x4 acc[RT];
@@ -239,20 +240,21 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
         for (int u = 0; u < RT; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
         const bool mine = te == quad.adapter(p);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half == 1 && steps <= 8) break;
-            if (p + half > 0) lds_barrier();  // the staged fragments have been read
-            stage(half);
+        for (int ph = 0; ph < PHASES; ++ph) {
+            constexpr int STEPS = 16 / PHASES;
+            if (ph > 0 && steps <= STEPS) break;
+            if (p + ph > 0) lds_barrier();  // the staged fragments have been read
+            stage(ph);
             wait_all_but(0);  // this wave's direct-to-LDS loads have landed
             lds_barrier();    // and every other wave's
             if (mine) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * half + (j & ~3) < steps) {  // K % 128 == 0: whole groups of four steps
+                for (int j = 0; j < STEPS; ++j)
+                    if (STEPS * ph + (j & ~3) < steps) {  // K % 128 == 0: whole groups of four steps
 #pragma unroll
                         for (int u = 0; u < RT; ++u)
-                            acc[u] = mfma_step(xf[8 * half + j],
-                                               *(lds_f16x8 *)(as + (16 * u + i) * HALF * 2 + 16 * ((4 * j + q) ^ i)), acc[u]);
+                            acc[u] = mfma_step(xf[STEPS * ph + j],
+                                               *(lds_f16x8 *)(as + (16 * u + i) * PART * 2 + 16 * ((4 * j + q) ^ i)), acc[u]);
                     }
             }
         }
@@ -312,6 +314,36 @@ __device__ __forceinline__ void split(float v, int sh, f16 &hi, f16 &lo)
     const float f = __builtin_amdgcn_ldexpf(v, sh);
     hi = (f16)f;
     lo = fabsf(f) < __builtin_inff() ? (f16)(f - (float)hi) : (f16)0.f;
+}
+
+// The fragments of a token's v from its row in LDS: the lane's 8 ranks of each step, scaled and split (hi in lane
+// groups 0 and 1, lo in 2 and 3); zeros past `rank`. Returns the power of two.
+template <int RS>
+__device__ __forceinline__ int split_row(f16x8 (&vf)[RS], const float *v32, int rank, int q)
+{
+    float v[RS][8], big = 0.f;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        const int r = 16 * s + 8 * (q & 1);
+        const f32x4 v0 = *reinterpret_cast<const f32x4 *>(v32 + r), v1 = *reinterpret_cast<const f32x4 *>(v32 + r + 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[s][k] = r < rank ? (k < 4 ? v0[k & 3] : v1[k & 3]) : 0.f;
+            const float f = fabsf(v[s][k]);
+            if (f < __builtin_inff()) big = fmaxf(big, f);
+        }
+    }
+    big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
+    const int sh = shift_of(big);
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            f16 hi, lo;
+            split(v[s][k], sh, hi, lo);
+            vf[s][k] = q < 2 ? hi : lo;
+        }
+    return sh;
 }
 
 // The fragments of B for ranks 16s0 .. + 16SB - 1 of a group of 64 outputs: rows n0 + 16u + i in MFMA tile u, so
@@ -469,22 +501,8 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
     for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
     start(r_first);
     lds_barrier();
-    float v[RS][8], big = 0.f;
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-        const int r = 16 * s + 8 * (q & 1);
-        const bool valid = row >= 0 && r < rank;
-        const f32x4 v0 = *reinterpret_cast<const f32x4 *>(&v32[i * V_PITCH + r]);
-        const f32x4 v1 = *reinterpret_cast<const f32x4 *>(&v32[i * V_PITCH + r + 4]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[s][k] = valid ? (k < 4 ? v0[k & 3] : v1[k & 3]) : 0.f;
-            const float f = fabsf(v[s][k]);
-            if (f < __builtin_inff()) big = fmaxf(big, f);
-        }
-    }
-    big = fmaxf(big, __shfl_xor(big, 16, 64));  // the token's other eight ranks of each step
-    const int sh = shift_of(big);
+    f16x8 vf[RS];
+    const int sh = split_row<RS>(vf, &v32[i * V_PITCH], row >= 0 ? rank : 0, q);
     f32x4 acc[SETS][4];
 #pragma unroll
     for (int z = 0; z < SETS; ++z)
@@ -496,17 +514,10 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
 #pragma unroll
             for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, s, i, q);
         }
-        f16x8 vf;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            f16 hi, lo;
-            split(v[s][k], sh, hi, lo);
-            vf[k] = q < 2 ? hi : lo;
-        }
 #pragma unroll
         for (int z = 0; z < SETS; ++z)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[z][u] = mfma_step(bf[z][s % SB][u], vf, acc[z][u]);
+            for (int u = 0; u < 4; ++u) acc[z][u] = mfma_step(bf[z][s % SB][u], vf[s], acc[z][u]);
     }
 #pragma unroll
     for (int z = 0; z < SETS; ++z)
@@ -529,9 +540,11 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
 }
 
 // ---- expand of quads (lora_add) -------------------------------------------------------------------
-// v folded and split once per row, in the order of the expand kernels' fragments: vs[row][r / 8] holds 8 hi
+// v folded and split once per row, in the order of the expand kernel's fragments: vs[row][r / 8] holds 8 hi
 // then 8 lo terms, shifts[row] the row's power of two. Rows without an adapter are folded too (whatever the
 // workspace holds) and never read. The blocks behind the folding ones copy those rows of y to out.
+// (Folding in the expand blocks instead, once per column range, saves this launch but was slower: 25.0 instead
+// of 23.0 us at 6000 rows, rank 16, four chunks; copying there too: 51 instead of 46 us at 4096 rows, rank 64.)
 constexpr int FOLD_THREADS = 256;
 
 __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *__restrict__ vp, int64_t P, int S, int rank,
@@ -595,7 +608,8 @@ struct BStage {
     // rows of fewer than 16 pieces: row n of the 16 that a fragment read takes, by the bank slots they share
     __device__ static __forceinline__ int place(int n, int p)
     {
-        return PIECES >= 16 ? (p & ~15) | ((p ^ n) & 15) : p ^ ((n / (16 / PIECES)) & (PIECES - 1));
+        if constexpr (PIECES >= 16) return (p & ~15) | ((p ^ n) & 15);
+        else return p ^ ((n / (16 / PIECES)) & (PIECES - 1));
     }
 };
 
@@ -608,10 +622,10 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
     typedef BStage<RS> B;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const int g0 = blockIdx.y * groups_per_block, g_end = min(g0 + groups_per_block, (N + GROUP_COLS - 1) / GROUP_COLS);
     int te, row;
     const Quad quad = load_quad(tr, blockIdx.x, te, row);
     if (quad.e0 < 0) return;  // the whole block
-    const int g0 = blockIdx.y * groups_per_block, g_end = min(g0 + groups_per_block, (N + GROUP_COLS - 1) / GROUP_COLS);
     // This lane's two pieces of a group's y and out: rows 8h + lane / 8, columns 8 (lane % 8) .. + 7.
     const int c8 = 8 * (lane & 7);
     int yrow[2];
@@ -764,19 +778,19 @@ int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f
                    : go(expand_tile_kernel<T, GATE, 16>);
 }
 
-constexpr int QUAD_BLOCKS_PER_CU = 3;
-
 template <int RS>
 int launch_expand_quad(const TileRows &tr, const nvfp4_lora &lora, const f16 *vs, const int *shifts, const f16 *y, f16 *out,
                        hipStream_t s)
 {
     const int groups = (lora.rows + GROUP_COLS - 1) / GROUP_COLS, quads = (tr.t_max + QUAD - 1) / QUAD;
-    int per_block = (int)((int64_t)quads * groups / (QUAD_BLOCKS_PER_CU * (int64_t)device_cus()));
-    per_block = per_block < 1 ? 1 : per_block;
-    const size_t lds = BStage<RS>::LDS;
+    // About four blocks per CU, of two column groups at least. Measured with 1, 2, 3, 4 and 6 per CU: 24.9, 21.2,
+    // 21.6, 20.1 and 23.3 us at 4096 rows, rank 64, N = 4352.
+    const int per_cu = (int)((int64_t)quads * groups / (4 * (int64_t)device_cus()));
+    const int per_block = per_cu < 2 ? 2 : per_cu;
     static_assert(BStage<RS>::LDS <= 64 * 1024, "within the LDS that a launch may use without an opt-in");
-    return launch(expand_quad_kernel<RS>, dim3((unsigned)quads, (unsigned)((groups + per_block - 1) / per_block)), dim3(256), lds,
-                  s, tr, lora.rows, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vs, shifts, y, out, per_block);
+    return launch(expand_quad_kernel<RS>, dim3((unsigned)quads, (unsigned)((groups + per_block - 1) / per_block)), dim3(256),
+                  BStage<RS>::LDS, s, tr, lora.rows, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vs, shifts, y,
+                  out, per_block);
 }
 
 // lora_add of a batch of quads: shrink, fold + split (and the rows without an adapter), expand.
@@ -853,8 +867,11 @@ int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, 
     float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256((size_t)planes * M * N * sizeof(float)));
     int st;
     if (M <= FUSED_MAX_ROWS) {
-        // about two blocks per CU, one unit (weight tile and chunk, or shrink unit) per wave
-        const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora), slots = 2 * (int64_t)device_cus();
+        // One unit (weight tile and chunk, or shrink unit) per wave; four blocks per CU up to 16 rows, three
+        // above. Measured (4352 x 5120) with 1, 2, 3, 4 and 6 per CU: 8.8, 6.9, 6.8, 6.6 and 7.6 us at one row,
+        // 12.2, 12.0, 10.8, 11.1 and 13.9 at 32.
+        const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora);
+        const int64_t slots = (M > 16 ? 3 : 4) * (int64_t)device_cus();
         int T = (int)((units + slots - 1) / slots);
         T = T < 1 ? 1 : T > FUSED_WAVES ? FUSED_WAVES : T;
         const int64_t shrink_blocks = (shrink_units(tr, lora) + T - 1) / T;

@@ -100,7 +100,8 @@ def _tensor(a, b, scale):
 ADD = [(1, 16, 128, 8, 1, "one"), (1, 4352, 5120, 16, 4, "one"), (5, 80, 640, 24, 3, "mixed"), (16, 64, 512, 16, 16, "own"),
        (17, 272, 1152, 40, 5, "mixed"), (40, 128, 2176, 64, 2, "mixed"), (100, 1040, 256, 72, 64, "mixed"),
        (260, 96, 384, 128, 7, "runs"), (33, 48, 896, 256, 3, "mixed"), (700, 512, 1024, 16, 9, "mixed"),
-       (2100, 208, 640, 32, 4, "runs"), (50, 64, 128, 8, 4096, "own"), (21, 112, 512, 200, 4, "none")]
+       (2100, 208, 640, 32, 4, "runs"), (600, 144, 768, 128, 3, "mixed"), (530, 80, 1536, 200, 2, "mixed"),
+       (900, 336, 5120, 8, 11, "mixed"), (640, 160, 384, 40, 40, "own"), (1300, 96, 128, 256, 5, "runs"), (50, 64, 128, 8, 4096, "own"), (21, 112, 512, 200, 4, "none")]
 
 
 @pytest.mark.parametrize("whole", [True, False])
