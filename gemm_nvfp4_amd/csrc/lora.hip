@@ -742,8 +742,14 @@ TileRows tile_rows(const PlanView &pv, const PlanLayout &L, int bucket)
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// The quad kernels, once adapters average at least 16 rows and the batch is not small.
-bool use_quads(int64_t P, int adapters) { return P >= 512 && P >= 16 * (int64_t)adapters; }
+// The quad kernels take batches of enough work, with two row tiles per adapter on average. Measured, tile against
+// quad kernels (us): rank 16, K = 5120, N = 4352, one adapter: 18.4 / 17.9 at 1536 rows, 36.1 / 29.6 at 4096; rank
+// 16, K = 2048, N = 1024: 12.1 / 13.5 at 2048, 22.3 / 23.7 at 8192; rank 64, K = 5120, N = 4352: 15.5 / 15.9 at 256,
+// 32.7 / 21.7 at 1024; 64 adapters there: 35.5 / 50.1 at 1024, 58.4 / 34.6 at 2048.
+bool use_quads(int64_t P, const nvfp4_lora &lora)
+{
+    return P * lora.rank * ((int64_t)lora.k + lora.rows) >= 250000000 && P >= 32 * (int64_t)lora.adapters;
+}
 
 int launch_shrink(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lora, float *vp, hipStream_t s)
 {
@@ -850,7 +856,7 @@ int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const u
     const TileRows tr = tile_rows(pv, L, order);
     const f16 *xh = reinterpret_cast<const f16 *>(x), *yh = reinterpret_cast<const f16 *>(y);
     f16 *oh = reinterpret_cast<f16 *>(out);
-    if (use_quads(L.P, lora.adapters)) return add_quads(tr, L.P, xh, lora, yh, oh, static_cast<uint8_t *>(ws), s);
+    if (use_quads(L.P, lora)) return add_quads(tr, L.P, xh, lora, yh, oh, static_cast<uint8_t *>(ws), s);
     float *vp = static_cast<float *>(ws);
     const int st = launch_shrink(tr, L.P, xh, lora, vp, s);
     if (st != NVFP4_OK) return st;

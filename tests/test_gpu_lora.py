@@ -100,8 +100,13 @@ def _tensor(a, b, scale):
 ADD = [(1, 16, 128, 8, 1, "one"), (1, 4352, 5120, 16, 4, "one"), (5, 80, 640, 24, 3, "mixed"), (16, 64, 512, 16, 16, "own"),
        (17, 272, 1152, 40, 5, "mixed"), (40, 128, 2176, 64, 2, "mixed"), (100, 1040, 256, 72, 64, "mixed"),
        (260, 96, 384, 128, 7, "runs"), (33, 48, 896, 256, 3, "mixed"), (700, 512, 1024, 16, 9, "mixed"),
-       (2100, 208, 640, 32, 4, "runs"), (600, 144, 768, 128, 3, "mixed"), (530, 80, 1536, 200, 2, "mixed"),
-       (900, 336, 5120, 8, 11, "mixed"), (640, 160, 384, 40, 40, "own"), (1300, 96, 128, 256, 5, "runs"), (50, 64, 128, 8, 4096, "own"), (21, 112, 512, 200, 4, "none")]
+       (2100, 208, 640, 32, 4, "runs"), (50, 64, 128, 8, 4096, "own"), (21, 112, 512, 200, 4, "none")]
+
+# batches whose work takes the kernels for many rows per adapter (rows * rank * (K + N) >= 2.5e8), every rank
+# step; a single adapter, several in one group of 64 rows, adapters without rows, rows without an adapter
+ADD += [(6100, 1040, 1664, 16, 7, "mixed"), (9001, 1648, 2176, 8, 180, "mixed"), (3500, 1056, 2048, 24, 3, "runs"),
+        (2050, 1104, 2176, 40, 60, "own"), (1200, 2000, 1408, 64, 1, "one"), (1030, 912, 1152, 120, 5, "mixed"),
+        (515, 1232, 1280, 200, 16, "mixed"), (700, 1424, 128, 256, 2, "runs"), (2100, 1040, 1152, 64, 4, "none")]
 
 
 @pytest.mark.parametrize("whole", [True, False])
@@ -127,7 +132,8 @@ def test_add(rows, n, k, rank, adapters, how, whole):
 
 
 @pytest.mark.parametrize("m,topk,n,k,rank,experts", [(1, 1, 64, 128, 8, 4), (9, 3, 144, 640, 16, 8), (200, 4, 256, 512, 48, 32),
-                                                     (300, 8, 1024, 2048, 16, 64)])
+                                                     (300, 8, 1024, 2048, 16, 64), (750, 8, 1040, 1664, 16, 64),
+                                                     (421, 5, 592, 896, 88, 50)])
 def test_add_in_bucket_order(m, topk, n, k, rank, experts):
     """The experts' adapters on rows that the plan sorted; rows behind the last valid one stay as they were."""
     rng = np.random.default_rng([2, m, n, k])
@@ -270,8 +276,8 @@ def test_swiglu(m, rows, k, rank, adapters, how, layout):
 
 
 def test_a_rows_result_does_not_depend_on_the_batch():
-    """lora_add of 2100 rows (many tiles) against single rows and against the same rows in another order."""
-    rows, n, k, rank, adapters = 2100, 144, 1152, 24, 5
+    """lora_add of 2100 rows (in groups of 64) against single rows and against the same rows in another order."""
+    rows, n, k, rank, adapters = 2100, 1104, 1152, 56, 5
     rng = np.random.default_rng(8)
     a, b, scale = _adapters(rng, adapters, n, k, rank, False)
     x, y, ids = _x(rng, rows, k, False), _x(rng, rows, n, False), _ids(rng, rows, adapters, "mixed")
