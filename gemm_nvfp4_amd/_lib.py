@@ -834,7 +834,8 @@ _linear_ws_bytes = functools.lru_cache(maxsize=256)(nvfp4_linear_lora_ws_bytes)
 def _lora_ws(ws, need: int, device, stream) -> torch.Tensor:
     if ws is None:
         return _alloc((max(need, 16),), torch.uint8, device, stream)
-    _bytes(ws, "ws", need)
+    if ws.numel() * ws.element_size() < need:
+        _bytes(ws, "ws", need)
     return ws
 
 
@@ -860,31 +861,36 @@ def nvfp4_lora_add(plan: torch.Tensor, M: int, topk: int, x: torch.Tensor, lora:
     return out
 
 
-def _linear_lora(fn: str, plan, x, w: NVFP4Tensor, lora: LoRATensor, layout, out, name: str, cols: int, ws, stream):
-    if x.dim() != 2 or x.shape[1] != w.k:
-        raise ValueError(f"x must have shape (M, {w.k}), got {tuple(x.shape)}")
-    M = x.shape[0]
+def _linear_lora(plan, x, w: NVFP4Tensor, lora: LoRATensor, out, name: str, cols: int, ws, stream):
+    """The checks of the projections with adapters. Returns the output tensor and the C arguments: those before
+    the adapters' descriptor and those behind it."""
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != w.k:
+        raise ValueError(f"x must have shape (M, {w.k}), got {tuple(shape)}")
+    M = shape[0]
     if lora.rows != w.rows or lora.k != w.k:
         raise ValueError(f"the adapters are for a {lora.rows} x {lora.k} weight, not {w.rows} x {w.k}")
     if out is None:
         out = _alloc((M, cols), torch.float16, x.device, stream)
-    _shape(out, name, (M, cols))
+    elif out.shape != (M, cols):
+        _shape(out, name, (M, cols))
     ws = _lora_ws(ws, _linear_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
     dev = _current_device(plan)
-    head = (_rows_plan(plan, M, 1, lora.adapters, dev), _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc()))
-    tail = (C.byref(lora.desc()), _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev),
-            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    plan_ptr = _rows_plan(plan, M, 1, lora.adapters, dev)
     # the descriptors may have been built under another current device
     _ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(lora.a, "lora.a", torch.float16, dev)
-    _check(fn, getattr(lib(), fn)(*head, *(() if layout is None else (layout,)), *tail))
-    return out
+    return (out, (plan_ptr, _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc())),
+            (C.byref(lora.desc()), _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev),
+             ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
 
 
 def nvfp4_linear_lora(plan: torch.Tensor, x: torch.Tensor, w: NVFP4Tensor, lora: LoRATensor,
                       y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """nvfp4_linear with each token's low-rank adapter: y = fp16(x W^T + scale_a (x A_a^T) B_a^T). plan:
     nvfp4_moe_plan of the adapter ids [M, 1] over lora.adapters (-1: no adapter). Returns y [M, N]."""
-    return _linear_lora("nvfp4_linear_lora", plan, x, w, lora, None, y, "y", w.rows, ws, stream)
+    y, head, tail = _linear_lora(plan, x, w, lora, y, "y", w.rows, ws, stream)
+    _check("nvfp4_linear_lora", lib().nvfp4_linear_lora(*head, *tail))
+    return y
 
 
 def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tensor, lora: LoRATensor, layout: int = 0,
@@ -892,4 +898,6 @@ def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tens
                              stream=None) -> torch.Tensor:
     """nvfp4_linear_swiglu with each token's low-rank adapter on the gate and up rows (lora.rows = 2I, in
     w13's row order) before SwiGLU. Returns h fp16 [M, I]."""
-    return _linear_lora("nvfp4_linear_swiglu_lora", plan, x, w13, lora, layout, h, "h", w13.rows // 2, ws, stream)
+    h, head, tail = _linear_lora(plan, x, w13, lora, h, "h", w13.rows // 2, ws, stream)
+    _check("nvfp4_linear_swiglu_lora", lib().nvfp4_linear_swiglu_lora(*head, layout, *tail))
+    return h

@@ -48,7 +48,7 @@ int check_lora(const nvfp4_lora *lora)
     if (lora->adapters < 1 || lora->rows < 1 || lora->k < 1 || lora->rank < 1) return NVFP4_ERR_SHAPE;
     if (!aligned(lora->a, 16) || !aligned(lora->b, 16) || !aligned(lora->scale, 4)) return NVFP4_ERR_ALIGN;
     if (lora->adapters > nvfp4::MAX_EXPERTS || lora->rank % 8 != 0 || lora->rank > nvfp4::MAX_LORA_RANK ||
-        lora->k % 128 != 0 || lora->k > nvfp4::MAX_LINEAR_K || lora->rows % 16 != 0)
+        lora->k % 128 != 0 || lora->k > nvfp4::MAX_LINEAR_K || lora->rows % 16 != 0 || lora->rows > nvfp4::MAX_LORA_ROWS)
         return NVFP4_ERR_UNSUPPORTED;
     return NVFP4_OK;
 }

@@ -101,7 +101,7 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // shrink's, whose first loads wait for the plan, run beside the weight stream (decoded weights kept for all
 // rows: 12.0 instead of 10.8 us at 32 rows of 4352 x 5120, 15.0 instead of 14.8 at 64).
 constexpr int FUSED_ROWS = 32;   // activation rows staged in LDS per pass
-constexpr int FUSED_WAVES = 8;   // most waves per block
+constexpr int FUSED_WAVES = 12;  // most waves per block
 
 __global__ __launch_bounds__(FUSED_WAVES * 64, 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
                                                                             const uint8_t *__restrict__ codes,
@@ -407,8 +407,8 @@ struct BaseLoads<float, CB> {
     }
 };
 
-// Base: y fp16 [P][N] (T = f16), or Sb planes of FP32 [P][N] that are added in order and scaled by gscale[0]
-// (NULL: 1). GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i.
+// Base: y fp16 [P][N] (T = f16), or Sb planes of FP32 [P][N] that are added in order and scaled by gscale[0].
+// GATE 0: plain; 1: gate rows [0, N/2), up rows [N/2, N); 2: row 2i gate i, row 2i + 1 up i.
 // The accumulators go through LDS, so that the base result is read and the output written in row segments: lane
 // l finishes columns 8 (l % 8) .. + 7 of the wave's 64, of rows l / 8 and l / 8 + 8 of the tile.
 constexpr int D_PITCH = GROUP_COLS + 4;
@@ -552,13 +552,14 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
                                                                   int64_t fold_blocks, const int32_t *__restrict__ pair_expert,
                                                                   const f16 *__restrict__ y, int N, f16 *__restrict__ out)
 {
-    if ((int64_t)blockIdx.x >= fold_blocks) {  // one block per row to copy (y and out are different buffers)
-        const int64_t p = (int64_t)blockIdx.x - fold_blocks;
-        if (pair_expert[p] >= 0) return;
-        const f16x8 *src = reinterpret_cast<const f16x8 *>(y + p * N);
-        f16x8 *dst = reinterpret_cast<f16x8 *>(out + p * N);
+    if ((int64_t)blockIdx.x >= fold_blocks) {  // a block copies row after row (y and out are different buffers)
+        for (int64_t p = (int64_t)blockIdx.x - fold_blocks; p < P; p += (int64_t)gridDim.x - fold_blocks) {
+            if (pair_expert[p] >= 0) continue;
+            const f16x8 *src = reinterpret_cast<const f16x8 *>(y + p * N);
+            f16x8 *dst = reinterpret_cast<f16x8 *>(out + p * N);
 #pragma unroll 4
-        for (int n = threadIdx.x; n < N / 8; n += FOLD_THREADS) dst[n] = src[n];
+            for (int n = threadIdx.x; n < N / 8; n += FOLD_THREADS) dst[n] = src[n];
+        }
         return;
     }
     const int64_t row = (int64_t)blockIdx.x * (FOLD_THREADS >> lg) + (threadIdx.x >> lg);  // 2^lg lanes per row
@@ -799,6 +800,8 @@ int launch_expand_quad(const TileRows &tr, const nvfp4_lora &lora, const f16 *vs
                   out, per_block);
 }
 
+constexpr int64_t MAX_COPY_BLOCKS = 1 << 20;  // a launch holds fewer than 2^32 threads
+
 // lora_add of a batch of quads: shrink, fold + split (and the rows without an adapter), expand.
 int add_quads(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lora, const f16 *y, f16 *out, uint8_t *ws,
               hipStream_t s)
@@ -818,7 +821,7 @@ int add_quads(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lor
     int lg = 0;
     while ((8 << lg) < rank) ++lg;
     const int64_t fold_blocks = (P + (FOLD_THREADS >> lg) - 1) / (FOLD_THREADS >> lg);
-    const int64_t copy_blocks = !tr.bucket && out != y ? P : 0;
+    const int64_t copy_blocks = tr.bucket || out == y ? 0 : P < MAX_COPY_BLOCKS ? P : MAX_COPY_BLOCKS;
     st = launch(fold_split_kernel, dim3((unsigned)(fold_blocks + copy_blocks)), dim3(FOLD_THREADS), 0, s, vp, P, S, rank, lg,
                 vs, shifts, fold_blocks, tr.pair_expert, y, lora.rows, out);
     if (st != NVFP4_OK) return st;
@@ -839,15 +842,10 @@ size_t lora_add_ws_bytes(int64_t P, int32_t K, int32_t rank)
            round256((size_t)P * 4);
 }
 
-// Batches whose projection runs as chunk products beside the shrink; larger ones take the one-launch
-// projection into one FP32 plane.
-constexpr int FUSED_MAX_ROWS = 64;
-static int base_planes(int32_t M, int32_t K) { return M <= FUSED_MAX_ROWS ? num_chunks(K) : 1; }
-
+// The projection's chunk products (as many as nvfp4_linear_ws keeps), then the chunk partials of v.
 size_t linear_lora_ws_bytes(int32_t M, int32_t rows, int32_t K, int32_t rank)
 {
-    return round256((size_t)base_planes(M, K) * M * rows * sizeof(float)) +
-           round256((size_t)num_chunks(K) * (size_t)M * rank * sizeof(float));
+    return round256(linear_ws_bytes(M, rows, K)) + round256((size_t)num_chunks(K) * (size_t)M * rank * sizeof(float));
 }
 
 int run_lora_add(const PlanView &pv, const PlanLayout &L, int32_t order, const uint16_t *x, const nvfp4_lora &lora,
@@ -868,28 +866,24 @@ int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, 
 {
     const TileRows tr = tile_rows(pv, L, 0);
     const f16 *xh = reinterpret_cast<const f16 *>(x);
-    const int N = w.rows, K = w.k, S = num_chunks(K), planes = base_planes(M, K);
+    const int N = w.rows, K = w.k, S = num_chunks(K);
     float *part = static_cast<float *>(ws);
-    float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256((size_t)planes * M * N * sizeof(float)));
-    int st;
-    if (M <= FUSED_MAX_ROWS) {
-        // One unit (weight tile and chunk, or shrink unit) per wave; four blocks per CU up to 16 rows, three
-        // above. Measured (4352 x 5120) with 1, 2, 3, 4 and 6 per CU: 8.8, 6.9, 6.8, 6.6 and 7.6 us at one row,
-        // 12.2, 12.0, 10.8, 11.1 and 13.9 at 32.
-        const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora);
-        const int64_t slots = (M > 16 ? 3 : 4) * (int64_t)device_cus();
-        int T = (int)((units + slots - 1) / slots);
-        T = T < 1 ? 1 : T > FUSED_WAVES ? FUSED_WAVES : T;
-        const int64_t shrink_blocks = (shrink_units(tr, lora) + T - 1) / T;
-        const int64_t blocks = shrink_blocks + (int64_t)S * ((N / 16 + T - 1) / T);
-        st = launch(linear_shrink_kernel, dim3((unsigned)blocks), dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K,
-                    part, tr, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp, (int)shrink_blocks);
-    } else {
-        st = run_linear_f32(x, M, w, part, s);
-        if (st == NVFP4_OK) st = launch_shrink(tr, L.P, xh, lora, vp, s);
-    }
+    float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256(linear_ws_bytes(M, N, K)));
+    // One unit (weight tile and chunk, or shrink unit) per wave; four blocks per CU up to 16 rows, three up to 64,
+    // then one, which stages x least often. Measured for this launch (4352 x 5120) with 1, 2, 3, 4 and 6 per CU: 8.8,
+    // 6.9, 6.8, 6.6 and 7.6 us at one row, 12.2, 12.0, 10.8, 11.1 and 13.9 at 32; for the whole call with 3 and 1:
+    // 31.6 and 30.9 at 128 rows, 241 and 167 at 1024.
+    const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora);
+    const int64_t slots = (M > 64 ? 1 : M > 16 ? 3 : 4) * (int64_t)device_cus();
+    int T = (int)((units + slots - 1) / slots);
+    T = T < 1 ? 1 : T > FUSED_WAVES ? FUSED_WAVES : T;
+    const int64_t shrink_blocks = (shrink_units(tr, lora) + T - 1) / T;
+    const int64_t blocks = shrink_blocks + (int64_t)S * ((N / 16 + T - 1) / T);
+    if (blocks * T * 64 >= (int64_t(1) << 32)) return NVFP4_ERR_UNSUPPORTED;  // more threads than a launch holds
+    const int st = launch(linear_shrink_kernel, dim3((unsigned)blocks), dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales,
+                          N, K, part, tr, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp, (int)shrink_blocks);
     if (st != NVFP4_OK) return st;
-    const BaseOf<float> base{part, planes, M <= FUSED_MAX_ROWS ? w.global_scale : nullptr, true};
+    const BaseOf<float> base{part, S, w.global_scale, true};
     f16 *o = reinterpret_cast<f16 *>(y);
     if (!gated) return launch_expand<float, 0>(tr, L.P, lora, vp, base, o, s);
     if (layout == 0) return launch_expand<float, 1>(tr, L.P, lora, vp, base, o, s);

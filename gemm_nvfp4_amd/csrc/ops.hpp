@@ -8,6 +8,7 @@ namespace nvfp4 {
 
 constexpr int MAX_ROW_K = 65536;   // row operators: elements per row
 constexpr int MAX_LORA_RANK = 256;
+constexpr int MAX_LORA_ROWS = 1 << 22;  // N, within a launch's second axis
 
 // moe_rows.hip
 int run_permute(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *x, const float *w, int32_t K, uint16_t *xs,

@@ -92,7 +92,7 @@ typedef struct nvfp4_lora {
  *        entry, overwritten. Calls that share a ws must not run concurrently.
  * Apart from out == y, outputs and ws must not overlap inputs.
  * Requirements: rank % 8 == 0, 8 <= rank <= 256; K % 128 == 0, K <= 32768 (swiglu: 16384);
- * N % 16 == 0 (swiglu: I % 16 == 0); adapters <= 4096; those of nvfp4_moe_plan; plan, x, y, out, h,
+ * N % 16 == 0 (swiglu: I % 16 == 0), N <= 2^22; adapters <= 4096; those of nvfp4_moe_plan; plan, x, y, out, h,
  * a, b, codes 16-byte aligned, scale 4-byte. Errors as in nvfp4moe.h (SHAPE also where lora and w
  * disagree), all before anything is enqueued. The *_ws_bytes functions return 0 for sizes that the
  * calls reject as SHAPE.

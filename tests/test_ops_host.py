@@ -80,7 +80,8 @@ def test_lora_add_refuses(L):
     call = lambda plan=fake, M=4, topk=2, order=0, x=fake, lora=_lora(), y=fake, out=fake, ws=fake, n=need: L.nvfp4_lora_add(plan, M, topk, order, x, lora, y, out, ws, n, null)  # noqa: E731,E501
     assert call(M=-1) == SHAPE and call(topk=33) == SHAPE and call(order=2) == SHAPE and call(order=-1) == SHAPE
     assert call(lora=None) == NULL
-    for bad, want in BAD_LORA + [(dict(k=192), UNSUPPORTED), (dict(k=32896), UNSUPPORTED), (dict(rows=72), UNSUPPORTED)]:
+    for bad, want in BAD_LORA + [(dict(k=192), UNSUPPORTED), (dict(k=32896), UNSUPPORTED), (dict(rows=72), UNSUPPORTED),
+                            (dict(rows=(1 << 22) + 16), UNSUPPORTED)]:
         assert call(lora=_lora(**bad)) == want, bad
         assert call(M=0, lora=_lora(**bad)) == want, bad
     assert call(M=0, plan=null, x=null, y=null, out=null, ws=null, n=0) == OK
