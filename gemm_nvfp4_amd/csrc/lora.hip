@@ -96,21 +96,23 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // ---- the projection's chunk products and the shrink in one launch ---------------------------------
 // Blocks [0, shrink_blocks) take shrink units. Each of the others takes one chunk and one 16-row weight tile
 // per wave, as the split-K form of the projection (linear.hip): part[c][m][n] is the library's chunk result,
-// so the sum over c is bitwise nvfp4_linear's. The weights decode anew for every 16 rows of x: the 100
-// registers of a wave then let all blocks of a launch be resident at once, several to a CU, so that the
-// shrink's, whose first loads wait for the plan, run beside the weight stream (decoded weights kept for all
-// rows: 12.0 instead of 10.8 us at 32 rows of 4352 x 5120, 15.0 instead of 14.8 at 64).
-constexpr int FUSED_ROWS = 32;   // activation rows staged in LDS per pass
+// so the sum over c is bitwise nvfp4_linear's. Small batches decode the weights
+// anew for every 16 rows of x: the 100 registers of a wave then let all blocks of a launch be resident at once,
+// several to a CU, so that the shrink's, whose first loads wait for the plan, run beside the weight stream. KEEP,
+// for larger ones: decoded weights kept for all rows, one block per CU, 64 rows of x staged at once (whole call,
+// 4352 x 5120, KEEP off and on: 31.0 and 25.7 us at 128 rows, 167 and 116 at 1024, 684 and 508 at 4096).
 constexpr int FUSED_WAVES = 12;  // most waves per block
 
-__global__ __launch_bounds__(FUSED_WAVES * 64, 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
+template <bool KEEP>
+__global__ __launch_bounds__(FUSED_WAVES * 64, KEEP ? 3 : 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
                                                                             const uint8_t *__restrict__ codes,
                                                                             const uint8_t *__restrict__ scales, int N, int K,
                                                                             float *__restrict__ part, TileRows tr, int rank,
                                                                             const f16 *__restrict__ a, float *__restrict__ vp,
                                                                             int shrink_blocks)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char xs[FUSED_ROWS * XS_PITCH];
+    constexpr int ROWS = KEEP ? 64 : 32;  // activation rows staged in LDS per pass
+    __shared__ __attribute__((aligned(16))) unsigned char xs[ROWS * XS_PITCH];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
     if ((int)blockIdx.x < shrink_blocks) {
         shrink_unit(tr, (int64_t)blockIdx.x * nwaves + wave, x, M, K, rank, a, vp);
@@ -127,9 +129,10 @@ __global__ __launch_bounds__(FUSED_WAVES * 64, 4) void linear_shrink_kernel(cons
         const size_t row = (size_t)t * 16 + n;
         w = load_chunk(codes + row * ((size_t)K >> 1), scales + row * ((size_t)K >> 4), kb, q);
     }
+    f16x8 bf[4][4];
     const int k = kb + 8 * lane;
-    for (int m0 = 0; m0 < M; m0 += FUSED_ROWS) {
-        const int gm = min(M - m0, FUSED_ROWS);
+    for (int m0 = 0; m0 < M; m0 += ROWS) {
+        const int gm = min(M - m0, ROWS);
         if (m0 > 0) lds_barrier();  // the previous pass's fragment reads are done
         for (int r = wave; r < gm; r += nwaves) {
             const f16 *src = x + (size_t)(m0 + r) * K + (k < K ? k : 0);
@@ -139,18 +142,28 @@ __global__ __launch_bounds__(FUSED_WAVES * 64, 4) void linear_shrink_kernel(cons
         wait_all_but(0);  // this wave's direct-to-LDS loads (and weights) are done
         lds_barrier();    // and every other wave's
         if (!tv) continue;
-#pragma unroll 1
-        for (int rt = 0; rt * 16 < gm; ++rt) {
-            f16x8 af[4][4];
-            load_a_tile<A_STAGED>(af, x, make_rsrc(x, 0), xs, rt * 16 + n, gm, K, kb, q, qv);
-            keep_in_loop(w);
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        auto decode = [&]() {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const f16x2 sc = chunk_scales(w, b);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) acc = mfma_step(af[b][s], decode8(w.codes[b][s], sc[s >> 1]), acc);
+                for (int s = 0; s < 4; ++s) bf[b][s] = decode8(w.codes[b][s], sc[s >> 1]);
             }
+        };
+        if (KEEP && m0 == 0) decode();
+#pragma unroll 1
+        for (int rt = 0; rt * 16 < gm; ++rt) {
+            f16x8 af[4][4];
+            load_a_tile<A_STAGED>(af, x, make_rsrc(x, 0), xs, rt * 16 + n, gm, K, kb, q, qv);
+            if (!KEEP) {
+                keep_in_loop(w);
+                decode();
+            }
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) acc = mfma_step(af[b][s], bf[b][s], acc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int m = m0 + rt * 16 + 4 * q + j;
@@ -869,19 +882,23 @@ int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, 
     const int N = w.rows, K = w.k, S = num_chunks(K);
     float *part = static_cast<float *>(ws);
     float *vp = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round256(linear_ws_bytes(M, N, K)));
-    // One unit (weight tile and chunk, or shrink unit) per wave; four blocks per CU up to 16 rows, three up to 64,
-    // then one, which stages x least often. Measured for this launch (4352 x 5120) with 1, 2, 3, 4 and 6 per CU: 8.8,
-    // 6.9, 6.8, 6.6 and 7.6 us at one row, 12.2, 12.0, 10.8, 11.1 and 13.9 at 32; for the whole call with 3 and 1:
-    // 31.6 and 30.9 at 128 rows, 241 and 167 at 1024.
-    const int64_t units = (int64_t)(N / 16) * S + shrink_units(tr, lora);
-    const int64_t slots = (M > 64 ? 1 : M > 16 ? 3 : 4) * (int64_t)device_cus();
-    int T = (int)((units + slots - 1) / slots);
-    T = T < 1 ? 1 : T > FUSED_WAVES ? FUSED_WAVES : T;
-    const int64_t shrink_blocks = (shrink_units(tr, lora) + T - 1) / T;
-    const int64_t blocks = shrink_blocks + (int64_t)S * ((N / 16 + T - 1) / T);
+    // One unit (weight tile and chunk, or shrink unit) per wave: T waves per block for so many blocks per CU. Four
+    // up to 16 rows, three above: measured for this launch (4352 x 5120) with 1, 2, 3, 4 and 6 per CU 8.8, 6.9, 6.8,
+    // 6.6 and 7.6 us at one row, 12.2, 12.0, 10.8, 11.1 and 13.9 at 32. One, with the weights kept, beyond 64 rows,
+    // and from 33 where its blocks all fit at once (15.1 and 14.6 us at 64 rows).
+    const int64_t shrinks = shrink_units(tr, lora), units = (int64_t)(N / 16) * S + shrinks, cus = device_cus();
+    auto waves = [&](int64_t slots) {
+        const int64_t t = (units + slots - 1) / slots;
+        return (int)(t < 1 ? 1 : t > FUSED_WAVES ? FUSED_WAVES : t);
+    };
+    auto blocks_of = [&](int T) { return (shrinks + T - 1) / T + (int64_t)S * ((N / 16 + T - 1) / T); };
+    const bool keep = M > 64 || (M > 32 && blocks_of(waves(cus)) <= cus);
+    const int T = waves(keep ? cus : (M > 16 ? 3 : 4) * cus);
+    const int64_t blocks = blocks_of(T);
     if (blocks * T * 64 >= (int64_t(1) << 32)) return NVFP4_ERR_UNSUPPORTED;  // more threads than a launch holds
-    const int st = launch(linear_shrink_kernel, dim3((unsigned)blocks), dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales,
-                          N, K, part, tr, lora.rank, reinterpret_cast<const f16 *>(lora.a), vp, (int)shrink_blocks);
+    const int st = launch(keep ? linear_shrink_kernel<true> : linear_shrink_kernel<false>, dim3((unsigned)blocks),
+                          dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K, part, tr, lora.rank,
+                          reinterpret_cast<const f16 *>(lora.a), vp, (int)((shrinks + T - 1) / T));
     if (st != NVFP4_OK) return st;
     const BaseOf<float> base{part, S, w.global_scale, true};
     f16 *o = reinterpret_cast<f16 *>(y);

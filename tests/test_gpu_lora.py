@@ -207,7 +207,7 @@ def test_values_that_are_not_finite_stay_in_their_rows():
 # on both sides of every path change
 LINEAR = [(1, 4352, 5120, 16, 4, "one"), (1, 64, 128, 8, 1, "none"), (4, 256, 640, 32, 3, "mixed"), (13, 5120, 2176, 16, 13, "own"),
           (32, 544, 1024, 64, 8, "mixed"), (33, 96, 1536, 16, 5, "mixed"), (64, 1088, 2176, 24, 6, "runs"),
-          (65, 64, 512, 128, 2, "mixed"), (130, 288, 896, 16, 40, "mixed"), (3, 32, 16512, 8, 2, "mixed"),
+          (65, 64, 512, 128, 2, "mixed"), (50, 128, 640, 16, 2, "mixed"), (200, 4352, 1664, 16, 3, "mixed"), (130, 288, 896, 16, 40, "mixed"), (3, 32, 16512, 8, 2, "mixed"),
           (9, 96, 256, 256, 3, "mixed")]
 
 
