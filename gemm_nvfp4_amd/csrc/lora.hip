@@ -287,11 +287,11 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
 }
 
 // ---- expand of tiles ------------------------------------------------------------------------------
-// One block per (row tile, 256 columns), one wave per 64 columns. After the plan's words, one round of loads
+// One block per (row tile, 128 columns), one wave per 64 columns. After the plan's words, one round of loads
 // brings the chunk partials of v (folded by the block into LDS), B and the base result. Behind the plan's tiles
 // lie pseudo tiles of 16 consecutive rows each, for the rows without an adapter.
 constexpr int GROUP_COLS = 64;   // outputs of one token per wave
-constexpr int TILE_WAVES = 4;
+constexpr int TILE_WAVES = 2;   // (4: 7.3 instead of 6.4 us at 32 rows of 4352 x 5120, rank 16, an adapter each)
 
 // Four ranks of a row's v: its chunk partials added in ascending order, the loads of ten chunks in flight at
 // once.
