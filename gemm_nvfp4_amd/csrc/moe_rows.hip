@@ -16,7 +16,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int ROW_THREADS = 256;
-constexpr int SLOTS = 16;  // slots whose rows are in flight at once
+constexpr int SEG_THREADS = 256;  // most pieces of a row per block
+constexpr int SLOTS = 16;  // slots of permute and unpermute whose rows are in flight at once
 
 __device__ __forceinline__ f16x8 round8(const float (&v)[8])
 {
@@ -31,15 +32,19 @@ __device__ __forceinline__ f16x8 round8(const float (&v)[8])
 constexpr int GRID_X = 1 << 20;
 __device__ __forceinline__ int token_block() { return (int)blockIdx.z * GRID_X + (int)blockIdx.x; }
 
-// This thread's token and piece: rows of 2^lg lanes (a block holds ROW_THREADS >> lg tokens), piece
-// segments over blockIdx.y. UNI: a wave lies within one token, whose index is then made wave-uniform, so
-// that positions and weights are scalar loads.
+// This thread's token and piece. UNI: a block takes one token (and one of blockIdx.y segments of its row), whose
+// positions and weights are then scalar loads. Else rows are shorter than a wave and a block takes
+// ROW_THREADS >> lg tokens, 2^lg lanes each.
 template <bool UNI>
 __device__ __forceinline__ bool row_piece(int lg, int M, int pieces, int &t, int &pc)
 {
-    t = token_block() * (ROW_THREADS >> lg) + (int)(threadIdx.x >> lg);
-    if (UNI) t = __builtin_amdgcn_readfirstlane(t);
-    pc = (blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+    if (UNI) {
+        t = token_block();
+        pc = blockIdx.y * blockDim.x + threadIdx.x;
+    } else {
+        t = token_block() * (ROW_THREADS >> lg) + (int)(threadIdx.x >> lg);
+        pc = threadIdx.x & ((1 << lg) - 1);
+    }
     return t < M && pc < pieces;
 }
 
@@ -60,7 +65,7 @@ __device__ __forceinline__ void store_row(f16 *p, f16x8 v)
 }
 
 template <bool UNI, bool NT>
-__global__ __launch_bounds__(ROW_THREADS) void permute_kernel(const int32_t *__restrict__ pos_of_pair,
+__global__ __launch_bounds__(SEG_THREADS) void permute_kernel(const int32_t *__restrict__ pos_of_pair,
                                                               const f16 *__restrict__ x, const float *__restrict__ w,
                                                               int M, int topk, int pieces, int lg, f16 *__restrict__ xs)
 {
@@ -68,23 +73,31 @@ __global__ __launch_bounds__(ROW_THREADS) void permute_kernel(const int32_t *__r
     if (!row_piece<UNI>(lg, M, pieces, t, pc)) return;
     const f16x8 v = *reinterpret_cast<const f16x8 *>(x + ((size_t)t * pieces + pc) * 8);
     const int32_t *pos = pos_of_pair + (size_t)t * topk;
-    for (int k = 0; k < topk; ++k) {
-        const int j = pos[k];
-        if (j < 0) continue;
-        f16x8 o = v;
-        if (w) {
-            const float wk = w[(size_t)t * topk + k];
-            float f[8];
+    for (int k0 = 0; k0 < topk; k0 += SLOTS) {
+        int j[SLOTS];
+        float wk[SLOTS];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = wk * (float)v[e];
-            o = round8(f);
+        for (int i = 0; i < SLOTS; ++i) {
+            j[i] = k0 + i < topk ? pos[k0 + i] : -1;
+            wk[i] = w && k0 + i < topk ? w[(size_t)t * topk + k0 + i] : 1.0f;
         }
-        store_row<NT>(xs + ((size_t)j * pieces + pc) * 8, o);
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            if (j[i] < 0) continue;
+            f16x8 o = v;
+            if (w) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = wk[i] * (float)v[e];
+                o = round8(f);
+            }
+            store_row<NT>(xs + ((size_t)j[i] * pieces + pc) * 8, o);
+        }
     }
 }
 
 template <bool UNI, bool NT>
-__global__ __launch_bounds__(ROW_THREADS) void unpermute_kernel(const int32_t *__restrict__ pos_of_pair,
+__global__ __launch_bounds__(SEG_THREADS) void unpermute_kernel(const int32_t *__restrict__ pos_of_pair,
                                                                 const f16 *__restrict__ ys, const float *__restrict__ w,
                                                                 int M, int topk, int pieces, int lg,
                                                                 f16 *__restrict__ out)
@@ -137,10 +150,12 @@ __device__ __forceinline__ float wave_sums(float (&a)[SL])
 }
 
 // One block per token; its waves share the row's pieces, hold each slot's partial dot product in a register
-// and add them across the wave and, through LDS, across the waves in ascending order. SL: slots per round, the
-// power of two that holds topk (16 at most); a thread has SLOTS bucket-row pieces in flight, of SL slots and
-// SLOTS / SL pieces of the row.
-template <int SL, bool NT>
+// and add them across the wave and, through LDS, across the waves in ascending order. The slots go in rounds of NS
+// (at most GRAD_SLOTS: one round of up to 16 is straight-line code of 10 KB, whose fetch took longer than its loads,
+// 7.7 us for one token of 128 elements and 16 slots); a thread has about GRAD_SLOTS bucket-row pieces in flight.
+constexpr int GRAD_SLOTS = 8;
+
+template <int NS, bool NT>
 __global__ __launch_bounds__(ROW_THREADS) void unpermute_grad_kernel(const int32_t *__restrict__ pos_of_pair,
                                                                      const f16 *__restrict__ dout,
                                                                      const f16 *__restrict__ ys,
@@ -148,37 +163,39 @@ __global__ __launch_bounds__(ROW_THREADS) void unpermute_grad_kernel(const int32
                                                                      int pieces,
                                                                      f16 *__restrict__ dys, float *__restrict__ dw)
 {
-    constexpr int PB = SLOTS / SL;
+    constexpr int SL = NS <= 1 ? 1 : NS <= 2 ? 2 : NS <= 4 ? 4 : 8;  // NS as wave_sums takes it
+    constexpr int PB = GRAD_SLOTS / NS;
     __shared__ float part[ROW_THREADS / 64][SL];
     const int t = token_block(), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (t >= M) return;  // the whole block
     const int32_t *pos = pos_of_pair + (size_t)t * topk;
-    for (int k0 = 0; k0 < topk; k0 += SL) {
-        int j[SL];
-        float wk[SL], acc[SL];
+    for (int k0 = 0; k0 < topk; k0 += NS) {
+        int j[NS];
+        float wk[NS], acc[SL];
 #pragma unroll
-        for (int i = 0; i < SL; ++i) {
+        for (int i = 0; i < SL; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
             j[i] = k0 + i < topk ? pos[k0 + i] : -1;
             wk[i] = dys && k0 + i < topk ? w[(size_t)t * topk + k0 + i] : 0.f;
-            acc[i] = 0.f;
         }
         for (int p0 = threadIdx.x; p0 < pieces; p0 += PB * blockDim.x) {
-            f16x8 d[PB], v[PB][SL];
+            f16x8 d[PB], v[PB][NS];
 #pragma unroll
             for (int b = 0; b < PB; ++b) {
                 const int pc = p0 + b * blockDim.x;
                 if (pc >= pieces) continue;
                 d[b] = *reinterpret_cast<const f16x8 *>(dout + ((size_t)t * pieces + pc) * 8);
 #pragma unroll
-                for (int i = 0; i < SL; ++i)
-                    if (j[i] >= 0) v[b][i] = load_row<NT>(ys + ((size_t)j[i] * pieces + pc) * 8);
+                for (int i = 0; i < NS; ++i)  // a skipped slot reads row 0 and drops it: no branch parts the loads
+                    v[b][i] = load_row<NT>(ys + ((size_t)max(j[i], 0) * pieces + pc) * 8);
             }
 #pragma unroll
             for (int b = 0; b < PB; ++b) {
                 const int pc = p0 + b * blockDim.x;
                 if (pc >= pieces) continue;
 #pragma unroll
-                for (int i = 0; i < SL; ++i)
+                for (int i = 0; i < NS; ++i)
                     if (j[i] >= 0) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) acc[i] = fmaf((float)d[b][e], (float)v[b][i][e], acc[i]);
@@ -196,25 +213,12 @@ __global__ __launch_bounds__(ROW_THREADS) void unpermute_grad_kernel(const int32
         if (lane % (64 / SL) == 0) part[wave][lane / (64 / SL)] = sum;
         __syncthreads();
         const int i = threadIdx.x;
-        if (i < SL && k0 + i < topk) {
+        if (i < NS && k0 + i < topk) {
             float s = part[0][i];
             for (int v = 1; v < (int)(blockDim.x >> 6); ++v) s += part[v][i];
             dw[(size_t)t * topk + k0 + i] = s;  // a skipped pair's partial sums are all +0
         }
     }
-}
-
-// log2 of the lanes per row (16 to 256): the fewest idle lanes in the row's last segment, the widest
-// of equals.
-int row_lanes_log2(int pieces)
-{
-    int best = 8;
-    int64_t best_lanes = INT64_MAX;
-    for (int lg = 8; lg >= 4; --lg) {
-        const int64_t lanes = ((int64_t)(pieces + (1 << lg) - 1) >> lg) << lg;
-        if (lanes < best_lanes) best_lanes = lanes, best = lg;
-    }
-    return best;
 }
 
 dim3 token_grid(int64_t blocks, int segments)
@@ -223,15 +227,42 @@ dim3 token_grid(int64_t blocks, int segments)
                 (unsigned)((blocks + GRID_X - 1) / GRID_X));
 }
 
-dim3 row_grid(int M, int pieces, int lg)
+// How a row operator is launched. Rows of at least a wave: one block per row and segment, as many whole waves as
+// the segment needs, so that a row's lines are touched together (rows of 129 pieces in 16-lane segments spread over
+// blocks took three times the floor). Shorter rows: the power of two that holds them.
+struct RowLaunch {
+    bool uni;
+    int lg;
+    dim3 grid, block;
+};
+
+RowLaunch row_launch(int M, int pieces)
 {
-    const int rows = ROW_THREADS >> lg;
-    return token_grid(((int64_t)M + rows - 1) / rows, (pieces + (1 << lg) - 1) >> lg);
+    RowLaunch r;
+    r.uni = pieces >= 64;
+    r.lg = 0;
+    while ((1 << r.lg) < pieces && !r.uni) ++r.lg;
+    if (r.uni) {
+        int segments = 0, threads = 0;
+        for (int n = (pieces + SEG_THREADS - 1) / SEG_THREADS, end = n + 3; n <= end; ++n) {  // fewest idle lanes
+            const int waves = ((pieces + n - 1) / n + 63) / 64 * 64;
+            if (segments == 0 || (int64_t)n * waves < (int64_t)segments * threads) segments = n, threads = waves;
+        }
+        r.block = dim3((unsigned)threads);
+        r.grid = token_grid(M, segments);
+    } else {
+        const int rows = ROW_THREADS >> r.lg;
+        r.block = dim3(ROW_THREADS);
+        r.grid = token_grid(((int64_t)M + rows - 1) / rows, 1);
+    }
+    return r;
 }
 
-// Whether the bucket rows exceed what the L2s of the eight XCDs hold (4 MB each). Measured on MI355X at 81920 rows
-// of 2048 elements: permute 73.1 -> 66.4 us, unpermute 76.4 -> 69.0, unpermute_grad 166 -> 151.
-bool streams(int64_t P, int K) { return P * K * 2 > (int64_t(32) << 20); }
+// Whether the bucket rows exceed what the L2s of the eight XCDs hold (4 MB each) and are whole 128-byte lines (lines
+// shared by two rows would go to memory twice). Measured on MI355X, without and with non-temporal rows: 81920 rows of
+// 2048 elements, permute 73.1 and 66.4 us, unpermute 76.4 and 69.0, unpermute_grad 166 and 151; 131072 rows of 1032,
+// permute 49.8 and 100.2, unpermute 56.2 and 65.0.
+bool streams(int64_t P, int K) { return K % 64 == 0 && P * K * 2 > (int64_t(32) << 20); }
 
 const f16 *half(const uint16_t *p) { return reinterpret_cast<const f16 *>(p); }
 f16 *half(uint16_t *p) { return reinterpret_cast<f16 *>(p); }
@@ -241,25 +272,27 @@ f16 *half(uint16_t *p) { return reinterpret_cast<f16 *>(p); }
 int run_permute(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *x, const float *w, int32_t K, uint16_t *xs,
                 hipStream_t s)
 {
-    const int pieces = K / 8, lg = row_lanes_log2(pieces);
+    const int pieces = K / 8;
+    const RowLaunch r = row_launch(M, pieces);
     auto go = [&](auto *kernel) {
-        return launch(kernel, row_grid(M, pieces, lg), dim3(ROW_THREADS), 0, s, pv.pos_of_pair, half(x), w, M, topk, pieces, lg,
+        return launch(kernel, r.grid, r.block, 0, s, pv.pos_of_pair, half(x), w, M, topk, pieces, r.lg,
                       half(xs));
     };
-    if (streams((int64_t)M * topk, K)) return lg >= 6 ? go(permute_kernel<true, true>) : go(permute_kernel<false, true>);
-    return lg >= 6 ? go(permute_kernel<true, false>) : go(permute_kernel<false, false>);
+    if (streams((int64_t)M * topk, K)) return r.uni ? go(permute_kernel<true, true>) : go(permute_kernel<false, true>);
+    return r.uni ? go(permute_kernel<true, false>) : go(permute_kernel<false, false>);
 }
 
 int run_unpermute(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *ys, const float *w, int32_t K,
                   uint16_t *out, hipStream_t s)
 {
-    const int pieces = K / 8, lg = row_lanes_log2(pieces);
+    const int pieces = K / 8;
+    const RowLaunch r = row_launch(M, pieces);
     auto go = [&](auto *kernel) {
-        return launch(kernel, row_grid(M, pieces, lg), dim3(ROW_THREADS), 0, s, pv.pos_of_pair, half(ys), w, M, topk, pieces, lg,
+        return launch(kernel, r.grid, r.block, 0, s, pv.pos_of_pair, half(ys), w, M, topk, pieces, r.lg,
                       half(out));
     };
-    if (streams((int64_t)M * topk, K)) return lg >= 6 ? go(unpermute_kernel<true, true>) : go(unpermute_kernel<false, true>);
-    return lg >= 6 ? go(unpermute_kernel<true, false>) : go(unpermute_kernel<false, false>);
+    if (streams((int64_t)M * topk, K)) return r.uni ? go(unpermute_kernel<true, true>) : go(unpermute_kernel<false, true>);
+    return r.uni ? go(unpermute_kernel<true, false>) : go(unpermute_kernel<false, false>);
 }
 
 int run_unpermute_grad(const PlanView &pv, int32_t M, int32_t topk, const uint16_t *dout, const uint16_t *ys,
@@ -271,11 +304,29 @@ int run_unpermute_grad(const PlanView &pv, int32_t M, int32_t topk, const uint16
         return launch(kernel, token_grid(M, 1), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout), half(ys), w, M, topk,
                       pieces, half(dys), dw);
     };
-    if (streams((int64_t)M * topk, K))
-        return topk <= 2 ? go(unpermute_grad_kernel<2, true>) : topk <= 4 ? go(unpermute_grad_kernel<4, true>)
-             : topk <= 8 ? go(unpermute_grad_kernel<8, true>) : go(unpermute_grad_kernel<16, true>);
-    return topk <= 2 ? go(unpermute_grad_kernel<2, false>) : topk <= 4 ? go(unpermute_grad_kernel<4, false>)
-         : topk <= 8 ? go(unpermute_grad_kernel<8, false>) : go(unpermute_grad_kernel<16, false>);
+    const int rounds = (topk + GRAD_SLOTS - 1) / GRAD_SLOTS, ns = (topk + rounds - 1) / rounds;
+    if (streams((int64_t)M * topk, K)) {
+        switch (ns) {
+        case 1: return go(unpermute_grad_kernel<1, true>);
+        case 2: return go(unpermute_grad_kernel<2, true>);
+        case 3: return go(unpermute_grad_kernel<3, true>);
+        case 4: return go(unpermute_grad_kernel<4, true>);
+        case 5: return go(unpermute_grad_kernel<5, true>);
+        case 6: return go(unpermute_grad_kernel<6, true>);
+        case 7: return go(unpermute_grad_kernel<7, true>);
+        default: return go(unpermute_grad_kernel<8, true>);
+        }
+    }
+    switch (ns) {
+    case 1: return go(unpermute_grad_kernel<1, false>);
+    case 2: return go(unpermute_grad_kernel<2, false>);
+    case 3: return go(unpermute_grad_kernel<3, false>);
+    case 4: return go(unpermute_grad_kernel<4, false>);
+    case 5: return go(unpermute_grad_kernel<5, false>);
+    case 6: return go(unpermute_grad_kernel<6, false>);
+    case 7: return go(unpermute_grad_kernel<7, false>);
+    default: return go(unpermute_grad_kernel<8, false>);
+    }
 }
 
 }  // namespace nvfp4

@@ -34,7 +34,7 @@ extern "C" {
  * nvfp4_moe_unpermute: expert rows back to their tokens.
  *   ys fp16 [M*topk][K] in bucket order,  out fp16 [M][K], every element written:
  *   s = +0; for k = 0..topk-1 with pos(p) >= 0: s = fmaf(w[p], ys[pos(p)], s);  out = fp16_rne(s).
- *   A token without a valid slot gets +0. Rows j >= n_valid of ys are not read. Without weights it
+ *   A token without a valid slot gets +0. What rows j >= n_valid of ys hold does not matter. Without weights it
  *   is the gradient of nvfp4_moe_permute without weights (dx from dxs); with them, of the weighted one.
  * nvfp4_moe_unpermute_grad: the gradient of nvfp4_moe_unpermute with weights.
  *   dout fp16 [M][K], ys as above; dys fp16 [M*topk][K], dweights FP32 [M][topk]:
