@@ -149,10 +149,11 @@ __device__ __forceinline__ float wave_sums(float (&a)[SL])
     return s;
 }
 
-// One block per token; its waves share the row's pieces, hold each slot's partial dot product in a register
-// and add them across the wave and, through LDS, across the waves in ascending order. The slots go in rounds of NS
-// (at most GRAD_SLOTS: one round of up to 16 is straight-line code of 10 KB, whose fetch took longer than its loads,
-// 7.7 us for one token of 128 elements and 16 slots); a thread has about GRAD_SLOTS bucket-row pieces in flight.
+// One block per (token, NS of its slots); its waves share the row's pieces, hold each slot's partial dot product in a
+// register and add them across the wave and, through LDS, across the waves in ascending order: an order that depends
+// on K alone. NS is at most GRAD_SLOTS (16 slots at once are straight-line code of 10 KB, whose fetch took longer than
+// its loads: 7.7 us for one token of 128 elements), and less where there are few tokens; a thread has about GRAD_SLOTS
+// bucket-row pieces in flight.
 constexpr int GRAD_SLOTS = 8;
 
 template <int NS, bool NT>
@@ -166,58 +167,55 @@ __global__ __launch_bounds__(ROW_THREADS) void unpermute_grad_kernel(const int32
     constexpr int SL = NS <= 1 ? 1 : NS <= 2 ? 2 : NS <= 4 ? 4 : 8;  // NS as wave_sums takes it
     constexpr int PB = GRAD_SLOTS / NS;
     __shared__ float part[ROW_THREADS / 64][SL];
-    const int t = token_block(), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int t = token_block(), k0 = blockIdx.y * NS, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (t >= M) return;  // the whole block
     const int32_t *pos = pos_of_pair + (size_t)t * topk;
-    for (int k0 = 0; k0 < topk; k0 += NS) {
-        int j[NS];
-        float wk[NS], acc[SL];
+    int j[NS];
+    float wk[NS], acc[SL];
 #pragma unroll
-        for (int i = 0; i < SL; ++i) acc[i] = 0.f;
+    for (int i = 0; i < SL; ++i) acc[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            j[i] = k0 + i < topk ? pos[k0 + i] : -1;
-            wk[i] = dys && k0 + i < topk ? w[(size_t)t * topk + k0 + i] : 0.f;
+    for (int i = 0; i < NS; ++i) {
+        j[i] = k0 + i < topk ? pos[k0 + i] : -1;
+        wk[i] = dys && k0 + i < topk ? w[(size_t)t * topk + k0 + i] : 0.f;
+    }
+    for (int p0 = threadIdx.x; p0 < pieces; p0 += PB * blockDim.x) {
+        f16x8 d[PB], v[PB][NS];
+#pragma unroll
+        for (int b = 0; b < PB; ++b) {
+            const int pc = p0 + b * blockDim.x;
+            if (pc >= pieces) continue;
+            d[b] = *reinterpret_cast<const f16x8 *>(dout + ((size_t)t * pieces + pc) * 8);
+#pragma unroll
+            for (int i = 0; i < NS; ++i)  // a skipped slot reads row 0 and drops it: no branch parts the loads
+                v[b][i] = load_row<NT>(ys + ((size_t)max(j[i], 0) * pieces + pc) * 8);
         }
-        for (int p0 = threadIdx.x; p0 < pieces; p0 += PB * blockDim.x) {
-            f16x8 d[PB], v[PB][NS];
 #pragma unroll
-            for (int b = 0; b < PB; ++b) {
-                const int pc = p0 + b * blockDim.x;
-                if (pc >= pieces) continue;
-                d[b] = *reinterpret_cast<const f16x8 *>(dout + ((size_t)t * pieces + pc) * 8);
+        for (int b = 0; b < PB; ++b) {
+            const int pc = p0 + b * blockDim.x;
+            if (pc >= pieces) continue;
 #pragma unroll
-                for (int i = 0; i < NS; ++i)  // a skipped slot reads row 0 and drops it: no branch parts the loads
-                    v[b][i] = load_row<NT>(ys + ((size_t)max(j[i], 0) * pieces + pc) * 8);
-            }
+            for (int i = 0; i < NS; ++i)
+                if (j[i] >= 0) {
 #pragma unroll
-            for (int b = 0; b < PB; ++b) {
-                const int pc = p0 + b * blockDim.x;
-                if (pc >= pieces) continue;
+                    for (int e = 0; e < 8; ++e) acc[i] = fmaf((float)d[b][e], (float)v[b][i][e], acc[i]);
+                    if (dys) {
+                        float f[8];
 #pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    if (j[i] >= 0) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[i] = fmaf((float)d[b][e], (float)v[b][i][e], acc[i]);
-                        if (dys) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = wk[i] * (float)d[b][e];
-                            store_row<NT>(dys + ((size_t)j[i] * pieces + pc) * 8, round8(f));
-                        }
+                        for (int e = 0; e < 8; ++e) f[e] = wk[i] * (float)d[b][e];
+                        store_row<NT>(dys + ((size_t)j[i] * pieces + pc) * 8, round8(f));
                     }
-            }
+                }
         }
-        const float sum = wave_sums<SL>(acc);
-        if (k0 > 0) __syncthreads();  // the previous slots' sums have been read
-        if (lane % (64 / SL) == 0) part[wave][lane / (64 / SL)] = sum;
-        __syncthreads();
-        const int i = threadIdx.x;
-        if (i < NS && k0 + i < topk) {
-            float s = part[0][i];
-            for (int v = 1; v < (int)(blockDim.x >> 6); ++v) s += part[v][i];
-            dw[(size_t)t * topk + k0 + i] = s;  // a skipped pair's partial sums are all +0
-        }
+    }
+    const float sum = wave_sums<SL>(acc);
+    if (lane % (64 / SL) == 0) part[wave][lane / (64 / SL)] = sum;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < NS && k0 + i < topk) {
+        float s = part[0][i];
+        for (int v = 1; v < (int)(blockDim.x >> 6); ++v) s += part[v][i];
+        dw[(size_t)t * topk + k0 + i] = s;  // a skipped pair's partial sums are all +0
     }
 }
 
@@ -300,11 +298,14 @@ int run_unpermute_grad(const PlanView &pv, int32_t M, int32_t topk, const uint16
 {
     const int pieces = K / 8;
     const int threads = pieces >= ROW_THREADS ? ROW_THREADS : (pieces + 63) / 64 * 64;
+    // Rounds of at most GRAD_SLOTS slots; more of fewer while there are under two blocks per CU.
+    int rounds = (topk + GRAD_SLOTS - 1) / GRAD_SLOTS;
+    while (rounds < topk && (int64_t)M * rounds < 2 * (int64_t)device_cus()) rounds = 2 * rounds < topk ? 2 * rounds : topk;
+    const int ns = (topk + rounds - 1) / rounds;
     auto go = [&](auto *kernel) {
-        return launch(kernel, token_grid(M, 1), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout), half(ys), w, M, topk,
+        return launch(kernel, token_grid(M, (topk + ns - 1) / ns), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout), half(ys), w, M, topk,
                       pieces, half(dys), dw);
     };
-    const int rounds = (topk + GRAD_SLOTS - 1) / GRAD_SLOTS, ns = (topk + rounds - 1) / rounds;
     if (streams((int64_t)M * topk, K)) {
         switch (ns) {
         case 1: return go(unpermute_grad_kernel<1, true>);

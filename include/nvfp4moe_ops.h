@@ -39,8 +39,8 @@ extern "C" {
  * nvfp4_moe_unpermute_grad: the gradient of nvfp4_moe_unpermute with weights.
  *   dout fp16 [M][K], ys as above; dys fp16 [M*topk][K], dweights FP32 [M][topk]:
  *   dys[pos(p)] = fp16_rne( w[p] * dout[p / topk] ),
- *   dweights[p] = sum over n of dout[p / topk][n] * ys[pos(p)][n] in FP32, in one order fixed by K
- *   and topk; +0 for a skipped pair. Rows j >= n_valid of dys are not written. dys may be NULL: only dweights
+ *   dweights[p] = sum over n of dout[p / topk][n] * ys[pos(p)][n] in FP32, in one order fixed by K;
+ *   +0 for a skipped pair. Rows j >= n_valid of dys are not written. dys may be NULL: only dweights
  *   (which also gives the gradient of the weighted nvfp4_moe_permute with respect to its weights:
  *   dout = x, ys = dxs); topk_weights is then not read and may be NULL.
  *
