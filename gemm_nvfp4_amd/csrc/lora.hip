@@ -11,10 +11,16 @@
 //           (largest finite |v| to [2^12, 2^13)) and split into v = hi + lo, two fp16 numbers, so that
 //           the matrix pipe sums it to at least 22 bits of the row's largest |v|. One MFMA step takes 16
 //           ranks: its lane groups 0 and 1 feed hi, groups 2 and 3 lo, against the same columns of B.
-//           B's rows are the MFMA's row operand and the tokens its columns: with rows n0 + 16(i/4) + 4t +
-//           i%4 for row i of tile t, a lane holds 16 consecutive outputs of one token after four tiles.
-// Rows without an adapter take pseudo tiles behind the plan's (16 consecutive pairs, those with an
-// adapter masked) and only copy, or finish, their base result.
+//           B's rows are the MFMA's row operand and the tokens its columns, so a lane ends with four
+//           neighbouring outputs of one token.
+// Three forms of it, with the same results bitwise:
+//   beside a projection   the projection's chunk products and the shrink in one launch, their sums, the expand
+//                         and the epilogue in a second. Bound by the weight stream and the latency of two launches.
+//   lora_add by tiles     shrink, then expand by row tiles: small batches, where latency counts.
+//   lora_add by quads     shrink and expand by four row tiles with A and B staged in LDS, v folded and split by a
+//                         launch between them: bound by the traffic of x and y.
+// Fragment loads straight from memory (16 lanes read 16 rows) cost the address unit a cycle per lane, so that
+// large batches bring matrices and results through LDS in whole lines.
 #include "linear_device.hpp"
 #include "nvfp4_device.hpp"
 #include "ops.hpp"
@@ -558,7 +564,7 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
 // workspace holds) and never read. The blocks behind the folding ones copy those rows of y to out.
 // (Folding in the expand blocks instead, once per column range, saves this launch but was slower: 25.0 instead
 // of 23.0 us at 6000 rows, rank 16, four chunks; copying there too: 51 instead of 46 us at 4096 rows, rank 64.)
-constexpr int FOLD_THREADS = 256;
+constexpr int FOLD_THREADS = 64;  // small blocks: the few threads spread over all CUs (256: 7.1 instead of 6.0 us)
 
 __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *__restrict__ vp, int64_t P, int S, int rank,
                                                                   int lg, f16 *__restrict__ vs, int *__restrict__ shifts,
