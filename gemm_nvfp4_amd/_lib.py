@@ -811,6 +811,9 @@ class LoRATensor:
         c = self.__dict__.get("_desc")
         if c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale:
             return c[3]
+        if (self.a.shape != (self.adapters, self.rank, self.k) or self.b.shape != (self.adapters, self.rows, self.rank)
+                or self.scale.shape != (self.adapters,)):
+            raise ValueError("a, b and scale must keep the shapes that the LoRATensor was made with")
         dev = _current_device(self.a)
         d = nvfp4_lora(_ptr(self.a, "a", torch.float16, dev), _ptr(self.b, "b", torch.float16, dev),
                        _ptr(self.scale, "scale", torch.float32, dev), self.adapters, self.rows, self.k, self.rank)

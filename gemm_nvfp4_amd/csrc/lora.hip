@@ -218,7 +218,6 @@ __device__ __forceinline__ Quad load_quad(const TileRows &tr, int quad, int &te,
 // the chunk (a whole one would leave two blocks per CU: 22.4 instead of 18.6 us at 4096 rows, rank 64, K =
 // 5120), else at once. Staged rows have no padding; the 16-byte piece at place p of rank r is piece
 // p ^ (r & 15), so that the fragment reads of 16 ranks fall into distinct banks.
-
 template <int RT>
 __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const f16 *__restrict__ x, int64_t P, int K, int rank,
                                                           const f16 *__restrict__ a, float *__restrict__ vp)
@@ -616,8 +615,8 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
 // contiguous piece of memory) is staged in LDS by direct-to-LDS loads, the next group's while this one is
 // computed; the accumulators go through LDS, so that y and out are read and written in whole 128-byte lines.
 // Fragments of v stay in registers. The MFMA's row operand is B (rows 16u + i of the group in tile u), so a
-// lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y; fragment loads of B and y straight
-// from memory (a lane a row: one 16-byte piece per cycle and CU) took twice the time.
+// lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y (71 MB in 20 us
+// at 4096 rows, rank 64, N = 4352); fragment loads of B and y straight from memory took 87 us.
 // LDS: B pieces of 8 ranks, piece p of row n at place p ^ swizzle(n); then 16 x D_PITCH floats per wave.
 template <int RS>
 struct BStage {
@@ -670,8 +669,7 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
         const bool mine = te == quad.adapter(p);
         const unsigned char *be = reinterpret_cast<const unsigned char *>(b + (size_t)quad.adapter(p) * N * rank);
         // Place l of the group's pieces (row n = l / PIECES) is filled with the piece that belongs there; pieces
-        // past the rank and rows past N are read as some other piece, and only ever meet zeros of v or columns
-        // that are not stored.
+        // past the rank and rows past N are read as some other piece, which no stored result uses.
         auto stage = [&](int g) {
             const unsigned char *bg = be + (size_t)g * GROUP_COLS * rank * 2;
             const int cols = N - g * GROUP_COLS;
@@ -715,13 +713,17 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < RS; ++s)
+                for (int s = 0; s < RS; ++s) {
+                    if (16 * s >= rank) continue;  // wave-uniform
+                    const bool past = 16 * s + 8 * (q & 1) >= rank;  // an odd last piece: zeros on both sides
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int n = 16 * u + i;
-                        acc[u] = mfma_step(*(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16), vf[s],
-                                           acc[u]);
+                        f16x8 bf = *(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16);
+                        if (past) bf = zero8();
+                        acc[u] = mfma_step(bf, vf[s], acc[u]);
                     }
+                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     f32x4 d;

@@ -71,7 +71,9 @@ typedef struct nvfp4_lora {
  *   d[n] = scale[a] * sum_r v[r] * B_a[n][r],   v[r] = sum_k x[k] * A_a[r][k],
  * v in FP32 (one reduction order: 512-element chunks, each one MFMA chain, added in chunk order), and
  * the sum over r in FP32 from v to at least 22 bits of the row's largest |v| (v is scaled by a power
- * of two and split into two fp16 terms). A row whose adapter id is skipped (-1, or outside
+ * of two and split into two fp16 terms). Non-finite values of x and y follow IEEE rules and stay in
+ * their row; an infinity in B makes its output column NaN or infinite for the rows of that adapter. A
+ * row whose adapter id is skipped (-1, or outside
  * [0, adapters)) gets d = 0 and bitwise the result without adapters.
  *   plan   the routing plan of the adapter ids: nvfp4_moe_plan(ids [M][topk], M, topk, adapters)
  *

@@ -201,6 +201,45 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert np.array_equal(out.view(np.uint16)[rest], _bits(want)[rest])
 
 
+def test_infinite_adapter_values_stay_in_their_column_and_adapter():
+    """An infinity in B: that output column of that adapter's rows is NaN or infinite, everything else is bitwise as
+    without it, and a row alone agrees with the row in a batch (an odd number of 8-rank pieces, so that the staged
+    matrix has places behind the rank)."""
+    rows, n, k, rank, adapters = 2100, 1040, 1152, 56, 3
+    rng = np.random.default_rng(12)
+    a, b, scale = _adapters(rng, adapters, n, k, rank, False)
+    x, y, ids = _x(rng, rows, k, False), _x(rng, rows, n, False), _ids(rng, rows, adapters, "mixed")
+    plan = G.nvfp4_moe_plan(_dev(ids.reshape(rows, 1)), adapters)
+    want = _bits(G.nvfp4_lora_add(plan, rows, 1, _dev(x), _tensor(a, b, scale), _dev(y)))
+    b[1, 70, 0], b[1, 71, 55] = np.inf, -np.inf
+    lora = _tensor(a, b, scale)
+    out = G.nvfp4_lora_add(plan, rows, 1, _dev(x), lora, _dev(y))
+    got, bits = out.cpu().numpy(), _bits(out)
+    hit = np.zeros((rows, n), bool)
+    hit[np.ix_(ids == 1, [70, 71])] = True
+    assert not np.isfinite(got[hit]).any() and np.array_equal(bits[~hit], want[~hit])
+    for t in np.nonzero(ids == 1)[0][:8]:
+        p1 = G.nvfp4_moe_plan(_dev(ids[t:t + 1].reshape(1, 1)), adapters)
+        one = G.nvfp4_lora_add(p1, 1, 1, _dev(x[t:t + 1]), lora, _dev(y[t:t + 1])).cpu().numpy()[0]
+        assert np.array_equal(one, got[t], equal_nan=True)
+
+
+def test_add_offsets_past_32_bits():
+    """y of 4.6 GB, rows on both sides of its 2^32-byte line; whole numbers, compared bit for bit."""
+    rows, n, k, rank, adapters = 140000, 16384, 128, 8, 3
+    rng = np.random.default_rng(13)
+    a, b, scale = _adapters(rng, adapters, n, k, rank, True)
+    x, ids = _x(rng, rows, k, True), _ids(rng, rows, adapters, "mixed")
+    y = torch.randint(-3, 4, (rows, n), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda").half()
+    plan = G.nvfp4_moe_plan(_dev(ids.reshape(rows, 1)), adapters)
+    out = G.nvfp4_lora_add(plan, rows, 1, _dev(x), _tensor(a, b, scale), y)
+    torch.cuda.synchronize()
+    line = 2 ** 32 // (2 * n)
+    for t in np.concatenate([rng.integers(0, rows, 12), np.arange(line - 2, line + 3), [0, rows - 1]]):
+        ref = y[t].cpu().double().numpy() + _low_rank(x[t:t + 1], ids[t:t + 1], a, b, scale)[0]
+        assert np.array_equal(_bits(out[t]), _rounded(ref)), t
+
+
 # ---- adapters beside the projections --------------------------------------------------------------------
 
 # M, N, K, rank, adapters: the dense workload, its gated MLP's down projection, short and long reductions, batches
@@ -337,6 +376,18 @@ def test_graph_replays_and_two_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(held[3].view(torch.int16), want[turn].view(torch.int16)), turn
+    # a second graph on the same plan, workspace and outputs, replayed in turn with the first
+    x2, ids2 = sets[2][0].clone(), sets[2][1].clone()
+    second = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(second):
+        mlp(x2, ids2, held)
+    x.copy_(sets[1][0])
+    ids.copy_(sets[1][1])
+    for _ in range(3):
+        for g, w in ((second, want[2]), (graph, want[1])):
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(held[3].view(torch.int16), w.view(torch.int16))
     streams, bufs = [torch.cuda.Stream() for _ in range(2)], [buffers() for _ in range(2)]
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())

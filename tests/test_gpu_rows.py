@@ -168,6 +168,56 @@ def test_values_that_are_not_finite():
     assert (xs[pos[3][pos[3] >= 0], 7] == np.inf).all()
 
 
+def test_skipped_pairs_beside_a_row_of_nan():
+    """Bucket row 0 holds NaN and infinities; tokens that do not own it are untouched by it, skipped slots too."""
+    m, topk, e, k = 9, 10, 16, 136
+    ids, x, ys, w, pos = _case(m, topk, e, k, 6)
+    ys[0, ::2], ys[0, 1::2] = np.nan, np.inf
+    owner = int(np.argwhere(pos == 0)[0][0])
+    plan = G.nvfp4_moe_plan(_dev(ids), e)
+    g, gw = G.nvfp4_moe_unpermute_grad(plan, m, topk, e, _dev(x), _dev(ys), _dev(w), dys=_poisoned(m * topk, k))
+    out = G.nvfp4_moe_unpermute(plan, m, topk, e, _dev(ys), _dev(w)).cpu().numpy()
+    rest = np.arange(m) != owner
+    assert np.isfinite(out[rest]).all() and not np.isfinite(out[owner]).all()
+    gw = gw.cpu().numpy()
+    assert np.isfinite(gw[pos != 0]).all() and np.isnan(gw[pos == 0]).all() and (gw[pos < 0] == 0).all()
+    assert np.array_equal(_bits(g), _expect_sorted(x, w, pos, m * topk, topk))
+
+
+def test_offsets_past_32_bits():
+    """Bucket rows of 5.2 GB: rows on both sides of the 2^32-byte line, against the rows they come from."""
+    m, topk, e, k = 40000, 8, 64, 8192
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(0, e, (m, topk), generator=gen, device="cuda", dtype=torch.int32)
+    ids[5] = -1
+    x = torch.randn((m, k), generator=gen, device="cuda").half()
+    w = torch.rand((m, topk), generator=gen, device="cuda")
+    plan = G.nvfp4_moe_plan(ids, e)
+    pos = G.plan_fields(plan, m, topk, e)["pos_of_pair"].reshape(m, topk)
+    xs = G.nvfp4_moe_permute(plan, m, topk, e, x)
+    out = G.nvfp4_moe_unpermute(plan, m, topk, e, xs, w)
+    dys, dw = G.nvfp4_moe_unpermute_grad(plan, m, topk, e, x, xs, w)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(4)
+    line = 2 ** 32 // (2 * k)
+    for t in np.unique(np.concatenate([rng.integers(0, m, 20), [0, 5, m - 1], np.argwhere(abs(pos - line) < 2)[:, 0]])):
+        row = x[t].cpu().numpy()
+        for s in range(topk):
+            if pos[t, s] < 0:
+                continue
+            j = int(pos[t, s])
+            assert torch.equal(xs[j], x[t])
+            want = (w[t, s].cpu().numpy() * row.astype(np.float32)).astype(np.float16)
+            assert np.array_equal(_bits(dys[j]), want.view(np.uint16))
+        terms = np.where(pos[t] >= 0, w[t].cpu().double().numpy(), 0.0)
+        ref = terms.sum() * row.astype(np.float64)
+        err = np.abs(out[t].cpu().double().numpy() - ref)
+        assert (err <= U16 * np.abs(ref) + 1.01 * topk * U32 * np.abs(terms).sum() * np.abs(row.astype(np.float64)) + 2.0 ** -25).all()
+        dot = (row.astype(np.float64) ** 2).sum()
+        n = 8 * -(-(k // 8) // 256) + 9
+        assert (np.abs(dw[t].cpu().double().numpy() - np.where(pos[t] >= 0, dot, 0.0)) <= 1.01 * n * U32 * dot).all()
+
+
 def test_results_do_not_depend_on_the_batch():
     m, topk, e, k = 70, 4, 16, 1032
     ids, x, ys, w, pos = _case(m, topk, e, k, 7)
@@ -258,6 +308,24 @@ def test_graph_replays_and_streams():
         torch.cuda.synchronize()
         for b, v in zip(bufs, want):
             assert torch.equal(b.view(torch.uint8), v.view(torch.uint8))
+    # a second graph on the same plan buffer, replayed in turn with the first
+    bufs2 = [torch.empty_like(b) for b in bufs]
+    calls(*other, *bufs2)
+    torch.cuda.synchronize()
+    want2 = [b.clone() for b in bufs2]
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2):
+        calls(*other, *bufs2)
+    for _ in range(2):
+        for b in bufs + bufs2:
+            b.zero_()
+        graph2.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, v in zip(bufs, want):
+            assert torch.equal(b.view(torch.uint8), v.view(torch.uint8))
+        assert torch.equal(bufs2[1].view(torch.uint8), want2[1].view(torch.uint8))
+        assert torch.equal(bufs2[3].view(torch.uint8), want2[3].view(torch.uint8))
     G.nvfp4_moe_plan(di, e, plan=plan)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -4,6 +4,7 @@ before anything is enqueued (fake device pointers are never read), and the Pytho
 tensors that they are given with the sizes that the library will read and write."""
 import ctypes as C
 import os
+import subprocess
 
 import pytest
 import torch
@@ -59,6 +60,18 @@ def test_row_gradient_refuses(L):
     assert call(w=null) == NULL  # dys needs the weights
     for k in ("plan", "d", "y", "dy", "w", "dw"):
         assert call(**{k: odd}) == ALIGN
+
+
+def test_header_is_plain_c(tmp_path):
+    """The header compiles by itself as C, and its descriptor has the size that the binding gives it."""
+    src = tmp_path / "h.c"
+    src.write_text('#include "nvfp4moe_ops.h"\n_Static_assert(sizeof(nvfp4_lora) == %d, "size");\n'
+                   'int (*f)(const void *, int32_t, int32_t, int32_t, const uint16_t *, const float *, int32_t, uint16_t *, void *)'
+                   ' = nvfp4_moe_permute;\n' % C.sizeof(nvfp4_lora))
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    r = subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", include, "-c", str(src), "-o",
+                        str(tmp_path / "h.o")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 def _lora(a=fake, b=fake, s=fake, adapters=8, rows=64, k=256, rank=16):
@@ -172,6 +185,10 @@ def test_wrappers_check_shapes():
     for fn, what in rows:
         with pytest.raises(ValueError, match=what):
             fn()
+    swapped = _t()
+    swapped.b = _f16(E, N + 16, R)
+    with pytest.raises(ValueError, match="must keep the shapes"):
+        swapped.desc()
 
 
 def test_wrappers_refuse_cpu_tensors():
