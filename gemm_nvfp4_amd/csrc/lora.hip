@@ -618,6 +618,8 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
 // lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y (71 MB in 20 us
 // at 4096 rows, rank 64, N = 4352); fragment loads of B and y straight from memory took 87 us.
 // LDS: B pieces of 8 ranks, piece p of row n at place p ^ swizzle(n); then 16 x D_PITCH floats per wave.
+__device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0, 0};
+
 template <int RS>
 struct BStage {
     static constexpr int PIECES = 2 * RS;                 // 16-byte pieces per row, rank padded to 16 RS
@@ -668,8 +670,8 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
         if (!quad.starts(p)) continue;  // the whole block
         const bool mine = te == quad.adapter(p);
         const unsigned char *be = reinterpret_cast<const unsigned char *>(b + (size_t)quad.adapter(p) * N * rank);
-        // Place l of the group's pieces (row n = l / PIECES) is filled with the piece that belongs there; pieces
-        // past the rank and rows past N are read as some other piece, which no stored result uses.
+        // Place l of the group's pieces (row n = l / PIECES) is filled with the piece that belongs there, zeros past
+        // the rank; rows past N are read as the last row, for columns that are not stored.
         auto stage = [&](int g) {
             const unsigned char *bg = be + (size_t)g * GROUP_COLS * rank * 2;
             const int cols = N - g * GROUP_COLS;
@@ -678,8 +680,9 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
                 const int first = (wave + QUAD * v) * 64, l = first + lane, n = l / B::PIECES;
                 if (B::PIECES == 2 && wave >= 2) break;  // 64 rows of two pieces: two waves' loads
                 const int piece = B::place(n, l % B::PIECES);  // its own inverse
-                const uint32_t off = 2u * ((uint32_t)min(n, cols - 1) * (uint32_t)rank + (uint32_t)(8 * piece < rank ? 8 * piece : 0));
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(bg + off),
+                const uint32_t off = 2u * ((uint32_t)min(n, cols - 1) * (uint32_t)rank + 8u * (uint32_t)piece);
+                const void *src = 8 * piece < rank ? static_cast<const void *>(bg + off) : zero_piece;
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
                                                  (__attribute__((address_space(3))) void *)(smem + (B::BUFFERS == 2 ? (g & 1) * B::BYTES : 0) +
                                                                                             first * 16),
                                                  16, 0, 0);
@@ -713,17 +716,13 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    if (16 * s >= rank) continue;  // wave-uniform
-                    const bool past = 16 * s + 8 * (q & 1) >= rank;  // an odd last piece: zeros on both sides
+                for (int s = 0; s < RS; ++s)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int n = 16 * u + i;
-                        f16x8 bf = *(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16);
-                        if (past) bf = zero8();
-                        acc[u] = mfma_step(bf, vf[s], acc[u]);
+                        acc[u] = mfma_step(*(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16), vf[s],
+                                           acc[u]);
                     }
-                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     f32x4 d;
