@@ -806,10 +806,11 @@ class LoRATensor:
             raise ValueError("inconsistent low-rank adapter shapes")
 
     def desc(self) -> nvfp4_lora:
-        """The C descriptor; built once and reused while a, b and scale are the same tensor objects
-        (their storage must not be reallocated in place)."""
+        """The C descriptor; built once and reused while a, b and scale are the same tensors in the same memory (a
+        training step may give a tensor new storage)."""
         c = self.__dict__.get("_desc")
-        if c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale:
+        if (c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale
+                and c[3].a == c[0].data_ptr() and c[3].b == c[1].data_ptr() and c[3].scale == c[2].data_ptr()):
             return c[3]
         if (self.a.shape != (self.adapters, self.rank, self.k) or self.b.shape != (self.adapters, self.rows, self.rank)
                 or self.scale.shape != (self.adapters,)):

@@ -303,8 +303,8 @@ int run_unpermute_grad(const PlanView &pv, int32_t M, int32_t topk, const uint16
     while (rounds < topk && (int64_t)M * rounds < 2 * (int64_t)device_cus()) rounds = 2 * rounds < topk ? 2 * rounds : topk;
     const int ns = (topk + rounds - 1) / rounds;
     auto go = [&](auto *kernel) {
-        return launch(kernel, token_grid(M, (topk + ns - 1) / ns), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout), half(ys), w, M, topk,
-                      pieces, half(dys), dw);
+        return launch(kernel, token_grid(M, (topk + ns - 1) / ns), dim3((unsigned)threads), 0, s, pv.pos_of_pair, half(dout),
+                      half(ys), w, M, topk, pieces, half(dys), dw);
     };
     if (streams((int64_t)M * topk, K)) {
         switch (ns) {

@@ -224,6 +224,26 @@ def test_infinite_adapter_values_stay_in_their_column_and_adapter():
         assert np.array_equal(one, got[t], equal_nan=True)
 
 
+def test_adapters_that_get_new_memory():
+    """One LoRATensor through a training loop that puts its tensors' data elsewhere, then overwrites what was there."""
+    rng = np.random.default_rng(61)
+    rows, n, k, rank = 20, 48, 256, 8
+    x, y = _x(rng, rows, k, True), _x(rng, rows, n, True)
+    ids = _ids(rng, rows, 2, "mixed")
+    plan = G.nvfp4_moe_plan(_dev(ids.reshape(rows, 1)), 2)
+    lora = _tensor(*_adapters(rng, 2, n, k, rank, True))
+    dx, dy = _dev(x), _dev(y)
+    for _ in range(3):
+        a, b, scale = _adapters(rng, 2, n, k, rank, True)
+        for name, new in (("a", a), ("b", b), ("scale", scale)):
+            old = getattr(lora, name).data
+            getattr(lora, name).data = _dev(new)
+            old.fill_(7.0)
+            cur = [getattr(lora, t).cpu().numpy() for t in ("a", "b", "scale")]
+            out = G.nvfp4_lora_add(plan, rows, 1, dx, lora, dy)
+            assert np.array_equal(_bits(out), _rounded(y.astype(np.float64) + _low_rank(x, ids, *cur))), name
+
+
 def test_add_offsets_past_32_bits():
     """y of 4.6 GB, rows on both sides of its 2^32-byte line; whole numbers, compared bit for bit."""
     rows, n, k, rank, adapters = 140000, 16384, 128, 8, 3
