@@ -701,7 +701,7 @@ def _current_device(t: torch.Tensor) -> int:
 def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
     """Device pointer of a contiguous tensor of this type on the current device, where the launch goes. The
     checks of _dev in few steps, since a small call's host time is most of its time."""
-    if dev >= 0 and isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype is dtype and t.is_contiguous():
         return t.data_ptr()
     _dev(t, name, dtype)
     raise ValueError(f"{name} lies on {t.device}, the current device is cuda:{dev}")
@@ -714,7 +714,7 @@ def _raw_stream(stream, dev: int) -> int:
 def _rows_plan(plan: torch.Tensor, M: int, topk: int, E: int, dev: int) -> int:
     """Device pointer of a plan that is large enough (the calls take no plan size)."""
     need = _plan_bytes(M, topk, E)
-    if plan.numel() * plan.element_size() < need:
+    if plan.nbytes < need:
         _bytes(plan, "plan", need)
     return _ptr(plan, "plan", torch.int32, dev)
 
@@ -724,14 +724,16 @@ def nvfp4_moe_permute(plan: torch.Tensor, M: int, topk: int, E: int, x: torch.Te
                       stream=None) -> torch.Tensor:
     """Tokens sorted by expert: row pos(t, k) of xs is x[t], times topk_weights[t, k] where given (one
     fp16 rounding). Returns xs fp16 [M*topk, K] in bucket order; rows >= n_valid are left as they are."""
-    if x.dim() != 2 or x.shape[0] != M:
-        raise ValueError(f"x must have shape ({M}, K), got {tuple(x.shape)}")
-    K = x.shape[1]
-    if topk_weights is not None:
+    shape = x.shape
+    if len(shape) != 2 or shape[0] != M:
+        raise ValueError(f"x must have shape ({M}, K), got {tuple(shape)}")
+    K = shape[1]
+    if topk_weights is not None and topk_weights.shape != (M, topk):
         _shape(topk_weights, "topk_weights", (M, topk))
     if xs is None:
         xs = _alloc((M * topk, K), torch.float16, x.device, stream)
-    _rows(xs, "xs", M * topk, K)
+    elif xs.shape != (M * topk, K):
+        _rows(xs, "xs", M * topk, K)
     dev = _current_device(plan)
     _check("nvfp4_moe_permute", lib().nvfp4_moe_permute(
         _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(x, "x", torch.float16, dev),
@@ -746,14 +748,16 @@ def nvfp4_moe_unpermute(plan: torch.Tensor, M: int, topk: int, E: int, ys: torch
     """Expert rows back to their tokens: out[t] = sum over the valid slots, in slot order, of
     topk_weights[t, k] * ys[pos(t, k)] (weights None: of the rows themselves, the gradient of
     nvfp4_moe_permute). Returns out fp16 [M, K]."""
-    if ys.dim() != 2 or ys.shape[0] < M * topk:
-        raise ValueError(f"ys must have shape [>= {M * topk}, K], got {tuple(ys.shape)}")
-    K = ys.shape[1]
-    if topk_weights is not None:
+    shape = ys.shape
+    if len(shape) != 2 or shape[0] < M * topk:
+        raise ValueError(f"ys must have shape [>= {M * topk}, K], got {tuple(shape)}")
+    K = shape[1]
+    if topk_weights is not None and topk_weights.shape != (M, topk):
         _shape(topk_weights, "topk_weights", (M, topk))
     if out is None:
         out = _alloc((M, K), torch.float16, ys.device, stream)
-    _shape(out, "out", (M, K))
+    elif out.shape != (M, K):
+        _shape(out, "out", (M, K))
     dev = _current_device(plan)
     _check("nvfp4_moe_unpermute", lib().nvfp4_moe_unpermute(
         _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(ys, "ys", torch.float16, dev),
@@ -767,21 +771,25 @@ def nvfp4_moe_unpermute_grad(plan: torch.Tensor, M: int, topk: int, E: int, dout
                              dweights: torch.Tensor | None = None, want_dys: bool = True, stream=None):
     """The gradient of nvfp4_moe_unpermute with weights. Returns (dys fp16 [M*topk, K] in bucket order, rows
     >= n_valid left as they are, or None without want_dys; dweights FP32 [M, topk], 0 for skipped pairs)."""
-    if dout.dim() != 2 or dout.shape[0] != M:
-        raise ValueError(f"dout must have shape ({M}, K), got {tuple(dout.shape)}")
-    K = dout.shape[1]
-    _rows(ys, "ys", M * topk, K)
-    if topk_weights is not None:
-        _shape(topk_weights, "topk_weights", (M, topk))
+    shape = dout.shape
+    if len(shape) != 2 or shape[0] != M:
+        raise ValueError(f"dout must have shape ({M}, K), got {tuple(shape)}")
+    K = shape[1]
+    rows, pairs = (M * topk, K), (M, topk)
+    if ys.shape != rows:
+        _rows(ys, "ys", *rows)
+    if topk_weights is not None and topk_weights.shape != pairs:
+        _shape(topk_weights, "topk_weights", pairs)
     if not want_dys:
         dys = None
     elif dys is None:
-        dys = _alloc((M * topk, K), torch.float16, dout.device, stream)
-    if dys is not None:
-        _rows(dys, "dys", M * topk, K)
+        dys = _alloc(rows, torch.float16, dout.device, stream)
+    elif dys.shape != rows:
+        _rows(dys, "dys", *rows)
     if dweights is None:
-        dweights = _alloc((M, topk), torch.float32, dout.device, stream)
-    _shape(dweights, "dweights", (M, topk))
+        dweights = _alloc(pairs, torch.float32, dout.device, stream)
+    elif dweights.shape != pairs:
+        _shape(dweights, "dweights", pairs)
     dev = _current_device(plan)
     _check("nvfp4_moe_unpermute_grad", lib().nvfp4_moe_unpermute_grad(
         _rows_plan(plan, M, topk, E, dev), M, topk, E, _ptr(dout, "dout", torch.float16, dev),
@@ -838,7 +846,7 @@ _linear_ws_bytes = functools.lru_cache(maxsize=256)(nvfp4_linear_lora_ws_bytes)
 def _lora_ws(ws, need: int, device, stream) -> torch.Tensor:
     if ws is None:
         return _alloc((max(need, 16),), torch.uint8, device, stream)
-    if ws.numel() * ws.element_size() < need:
+    if ws.nbytes < need:
         _bytes(ws, "ws", need)
     return ws
 
@@ -850,18 +858,23 @@ def nvfp4_lora_add(plan: torch.Tensor, M: int, topk: int, x: torch.Tensor, lora:
     ids [M, topk] over lora.adapters. x fp16 [M*topk, K], y fp16 [M*topk, N]; rows in pair order (order
     0) or in the plan's bucket order (order 1; rows >= n_valid are left as they are). out may be y."""
     P = M * topk
-    _shape(x, "x", (P, lora.k))
-    _shape(y, "y", (P, lora.rows))
+    rows = (P, lora.rows)
+    if x.shape != (P, lora.k):
+        _shape(x, "x", (P, lora.k))
+    if y.shape != rows:
+        _shape(y, "y", rows)
     if out is None:
-        out = _alloc((P, lora.rows), torch.float16, x.device, stream)
-    _shape(out, "out", (P, lora.rows))
+        out = _alloc(rows, torch.float16, x.device, stream)
+    elif out.shape != rows:
+        _shape(out, "out", rows)
     ws = _lora_ws(ws, _add_ws_bytes(P, lora.k, lora.rank), x.device, stream)
     dev = _current_device(plan)
-    _ptr(lora.a, "lora.a", torch.float16, dev)  # the descriptor may have been built under another current device
+    if lora.a.get_device() != dev:  # the descriptor may have been built under another current device
+        _ptr(lora.a, "lora.a", torch.float16, dev)
     _check("nvfp4_lora_add", lib().nvfp4_lora_add(
         _rows_plan(plan, M, topk, lora.adapters, dev), M, topk, order, _ptr(x, "x", torch.float16, dev),
         C.byref(lora.desc()), _ptr(y, "y", torch.float16, dev), _ptr(out, "out", torch.float16, dev),
-        _ptr(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
+        _ptr(ws, "ws", ws.dtype, dev), ws.nbytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -881,11 +894,11 @@ def _linear_lora(plan, x, w: NVFP4Tensor, lora: LoRATensor, out, name: str, cols
     ws = _lora_ws(ws, _linear_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
     dev = _current_device(plan)
     plan_ptr = _rows_plan(plan, M, 1, lora.adapters, dev)
-    # the descriptors may have been built under another current device
-    _ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(lora.a, "lora.a", torch.float16, dev)
+    if w.codes.get_device() != dev or lora.a.get_device() != dev:  # built under another current device
+        _ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(lora.a, "lora.a", torch.float16, dev)
     return (out, (plan_ptr, _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc())),
             (C.byref(lora.desc()), _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev),
-             ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
+             ws.nbytes, _raw_stream(stream, dev)))
 
 
 def nvfp4_linear_lora(plan: torch.Tensor, x: torch.Tensor, w: NVFP4Tensor, lora: LoRATensor,
