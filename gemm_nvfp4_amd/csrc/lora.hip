@@ -292,9 +292,10 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
 }
 
 // ---- expand of tiles ------------------------------------------------------------------------------
-// One block per (row tile, 128 columns), one wave per 64 columns. After the plan's words, one round of loads
-// brings the chunk partials of v (folded by the block into LDS), B and the base result. Behind the plan's tiles
-// lie pseudo tiles of 16 consecutive rows each, for the rows without an adapter.
+// One block per (row tile, 128 columns), one wave per 64 columns. After the plan's words come the chunk partials of
+// v (folded by the block into LDS), B and the base result. Behind the plan's tiles lie pseudo tiles of 16
+// consecutive rows each, for the rows without an adapter. EARLY: B and the base result are asked for before the
+// partials are waited for, and held in registers meanwhile (launch_expand says when).
 constexpr int GROUP_COLS = 64;   // outputs of one token per wave
 constexpr int TILE_WAVES = 2;   // (4: 7.3 instead of 6.4 us at 32 rows of 4352 x 5120, rank 16, an adapter each)
 
@@ -431,7 +432,7 @@ struct BaseLoads<float, CB> {
 // l finishes columns 8 (l % 8) .. + 7 of the wave's 64, of rows l / 8 and l / 8 + 8 of the tile.
 constexpr int D_PITCH = GROUP_COLS + 4;
 
-template <typename T, int GATE, int RS>
+template <typename T, int GATE, int RS, bool EARLY>
 __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows tr, int64_t P, int S, int N, int rank,
                                                                       const f16 *__restrict__ b,
                                                                       const float *__restrict__ scale,
@@ -504,20 +505,26 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
         finish(m0 + 8, r_second, 0.f);
         return;
     }
-    // v: one thread per four ranks of a row, all chunks in flight.
-    const int r4 = rank >> 2;
-    for (int task = threadIdx.x; task < rows * r4; task += TILE_WAVES * 64) {
-        const int m = task / r4, r = 4 * (task - m * r4);
-        const int vrow = tr.bucket ? tr.tile_base[t] + m : tr.tile_pair[t * TILE + m];
-        Fold4 f;
-        f.run(vp + (size_t)vrow * rank + r, (size_t)P * rank, S);
-        *reinterpret_cast<f32x4 *>(&v32[m * V_PITCH + r]) = f.v;
-    }
     const f16 *be = b + (size_t)e * N * rank;
     f16x8 bf[SETS][SB][4];
+    auto start_rest = [&]() {
 #pragma unroll
-    for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
-    start(r_first);
+        for (int z = 0; z < SETS; ++z) load_b<SB>(bf[z], be + (size_t)z * I * rank, n0, cols, rank, 0, i, q);
+        start(r_first);
+    };
+    if (EARLY) start_rest();
+    // v: one thread per four ranks of a row, all chunks in flight.
+    const int r4 = rank >> 2, tasks = rows * r4;
+    for (int t0 = 0; t0 < tasks; t0 += TILE_WAVES * 64) {
+        const int task = t0 + threadIdx.x, m = task / r4, r = 4 * (task - m * r4);
+        const int vrow = __shfl(row, m & 15, 64);  // lane m holds row m
+        if (task < tasks) {
+            Fold4 f;
+            f.run(vp + (size_t)vrow * rank + r, (size_t)P * rank, S);
+            *reinterpret_cast<f32x4 *>(&v32[m * V_PITCH + r]) = f.v;
+        }
+    }
+    if (!EARLY) start_rest();
     lds_barrier();
     f16x8 vf[RS];
     const int sh = split_row<RS>(vf, &v32[i * V_PITCH], row >= 0 ? rank : 0, q);
@@ -794,15 +801,20 @@ int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f
 {
     const int N = lora.rows, cols = GATE == 1 ? N / 2 : N, rs = (lora.rank + 15) / 16;
     const int64_t tiles = tr.t_max + (base.others ? (P + TILE - 1) / TILE : 0);
+    const int64_t groups = (cols + TILE_WAVES * GROUP_COLS - 1) / (TILE_WAVES * GROUP_COLS);
+    // EARLY for chunk partials (an fp16 base is one load and only pays for the registers: lora_add of 64 rows of 32
+    // adapters, rank 64, 17.5 us without and 19.4 with), but for rank 16 only in up to three blocks per CU, since it leaves two waves per SIMD instead of
+    // three. Measured without and with (whole linear_lora, 4352 x 5120): rank 64 12.6 and 10.4 us at one row, 34.5 and
+    // 30.0 at 64 rows of 32 adapters; rank 16 9.4 and 9.1 at one row, 12.0 and 11.8 at 16, 24.8 and 26.3 at 64.
+    const bool early = rs > 1 || tiles * groups <= 3 * (int64_t)device_cus();
     auto go = [&](auto *kernel) {
-        return launch(kernel, dim3((unsigned)tiles, (unsigned)((cols + TILE_WAVES * GROUP_COLS - 1) / (TILE_WAVES * GROUP_COLS))),
-                      dim3(TILE_WAVES * 64), 0, s, tr, P,
-                      num_chunks(lora.k), N, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb,
-                      base.gscale, out);
+        return launch(kernel, dim3((unsigned)tiles, (unsigned)groups), dim3(TILE_WAVES * 64), 0, s, tr, P, num_chunks(lora.k), N,
+                      lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb, base.gscale, out);
     };
-    return rs <= 1 ? go(expand_tile_kernel<T, GATE, 1>) : rs <= 2 ? go(expand_tile_kernel<T, GATE, 2>)
-         : rs <= 4 ? go(expand_tile_kernel<T, GATE, 4>) : rs <= 8 ? go(expand_tile_kernel<T, GATE, 8>)
-                   : go(expand_tile_kernel<T, GATE, 16>);
+    constexpr bool E = sizeof(T) == 4;
+    return rs <= 1 ? (early ? go(expand_tile_kernel<T, GATE, 1, E>) : go(expand_tile_kernel<T, GATE, 1, false>))
+         : rs <= 2 ? go(expand_tile_kernel<T, GATE, 2, E>) : rs <= 4 ? go(expand_tile_kernel<T, GATE, 4, E>)
+         : rs <= 8 ? go(expand_tile_kernel<T, GATE, 8, E>) : go(expand_tile_kernel<T, GATE, 16, E>);
 }
 
 template <int RS>
