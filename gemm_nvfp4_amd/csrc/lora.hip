@@ -250,7 +250,8 @@ __global__ __launch_bounds__(256, 3) void shrink_quad_kernel(TileRows tr, const 
                 const int k = kb + phase * PART + 8 * ((lane % (64 / RPI)) ^ (r & 15));
                 const uint32_t off = 2u * ((uint32_t)min(r0 + r, rank - 1) * (uint32_t)K + (uint32_t)(k < K ? k : 0));
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(ae + off),
-                                                 (__attribute__((address_space(3))) void *)(as + (wave + QUAD * v) * 1024), 16, 0, 0);
+                                                 (__attribute__((address_space(3))) void *)(as + (wave + QUAD * v) * 1024),
+                                                 16, 0, 0);
             }
         };
         f32x4 acc[RT];
@@ -623,7 +624,7 @@ __global__ __launch_bounds__(FOLD_THREADS) void fold_split_kernel(const float *_
 // computed; the accumulators go through LDS, so that y and out are read and written in whole 128-byte lines.
 // Fragments of v stay in registers. The MFMA's row operand is B (rows 16u + i of the group in tile u), so a
 // lane's accumulators are four neighbouring outputs of one token. What bounds it is the traffic of y (71 MB in 20 us
-// at 4096 rows, rank 64, N = 4352); fragment loads of B and y straight from memory took 87 us.
+// at 4096 rows, rank 64, N = 4352). NT: y and out past the caches. Fragment loads of B and y straight from memory took 87 us.
 // LDS: B pieces of 8 ranks, piece p of row n at place p ^ swizzle(n); then 16 x D_PITCH floats per wave.
 __device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0, 0};
 
@@ -641,7 +642,7 @@ struct BStage {
     }
 };
 
-template <int RS>
+template <int RS, bool NT>
 __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, int rank, const f16 *__restrict__ b,
                                                           const float *__restrict__ scale, const f16 *__restrict__ vs,
                                                           const int *__restrict__ shifts, const f16 *y, f16 *out,
@@ -666,8 +667,10 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
     auto load_y = [&](int g) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (yrow[h] >= 0 && g < g_end && g * GROUP_COLS + c8 < N)
-                yv[h] = *reinterpret_cast<const f16x8 *>(y + (size_t)yrow[h] * N + g * GROUP_COLS + c8);
+            if (yrow[h] >= 0 && g < g_end && g * GROUP_COLS + c8 < N) {
+                const f16x8 *p = reinterpret_cast<const f16x8 *>(y + (size_t)yrow[h] * N + g * GROUP_COLS + c8);
+                yv[h] = NT ? __builtin_nontemporal_load(p) : *p;
+            }
     };
     f16x8 vf[RS];
     float sc = 0.f;
@@ -689,10 +692,9 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
                 const int piece = B::place(n, l % B::PIECES);  // its own inverse
                 const uint32_t off = 2u * ((uint32_t)min(n, cols - 1) * (uint32_t)rank + 8u * (uint32_t)piece);
                 const void *src = 8 * piece < rank ? static_cast<const void *>(bg + off) : zero_piece;
+                unsigned char *dst = smem + (B::BUFFERS == 2 ? (g & 1) * B::BYTES : 0) + first * 16;
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                                 (__attribute__((address_space(3))) void *)(smem + (B::BUFFERS == 2 ? (g & 1) * B::BYTES : 0) +
-                                                                                            first * 16),
-                                                 16, 0, 0);
+                                                 (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
             }
         };
         if (p > 0) lds_barrier();  // the staged fragments have been read
@@ -705,7 +707,8 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
             for (int s = 0; s < RS; ++s) {
                 const int r = 16 * s + 8 * (q & 1);
                 vf[s] = zero8();
-                if (row >= 0 && r < rank) vf[s] = *reinterpret_cast<const f16x8 *>(vs + ((size_t)row * rank + r) * 2 + 8 * (q >> 1));
+                if (row >= 0 && r < rank)
+                    vf[s] = *reinterpret_cast<const f16x8 *>(vs + ((size_t)row * rank + r) * 2 + 8 * (q >> 1));
             }
         }
         int stores = 0;  // this wave's newest memory operations, wave-uniform
@@ -727,8 +730,8 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int n = 16 * u + i;
-                        acc[u] = mfma_step(*(lds_f16x8 *)(lds_byte *)(bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16), vf[s],
-                                           acc[u]);
+                        const unsigned char *bp = bs + (n * B::PIECES + B::place(n, 2 * s + (q & 1))) * 16;
+                        acc[u] = mfma_step(*(lds_f16x8 *)(lds_byte *)bp, vf[s], acc[u]);
                     }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -749,7 +752,11 @@ __global__ __launch_bounds__(256) void expand_quad_kernel(TileRows tr, int N, in
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = f16_of_f32(fmaf(sc, e < 4 ? lo[e & 3] : hi[e & 3], (float)yc[h][e]));
                     const bool live = yrow[h] >= 0 && n0 + c8 < N;
-                    if (live) *reinterpret_cast<f16x8 *>(out + (size_t)yrow[h] * N + n0 + c8) = o;
+                    if (live) {
+                        f16x8 *p = reinterpret_cast<f16x8 *>(out + (size_t)yrow[h] * N + n0 + c8);
+                        if (NT) __builtin_nontemporal_store(o, p);
+                        else *p = o;
+                    }
                     stores += __ballot(live) != 0;
                 }
                 __builtin_amdgcn_wave_barrier();
@@ -803,13 +810,15 @@ int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f
     const int64_t tiles = tr.t_max + (base.others ? (P + TILE - 1) / TILE : 0);
     const int64_t groups = (cols + TILE_WAVES * GROUP_COLS - 1) / (TILE_WAVES * GROUP_COLS);
     // EARLY for chunk partials (an fp16 base is one load and only pays for the registers: lora_add of 64 rows of 32
-    // adapters, rank 64, 17.5 us without and 19.4 with), but for rank 16 only in up to three blocks per CU, since it leaves two waves per SIMD instead of
-    // three. Measured without and with (whole linear_lora, 4352 x 5120): rank 64 12.6 and 10.4 us at one row, 34.5 and
-    // 30.0 at 64 rows of 32 adapters; rank 16 9.4 and 9.1 at one row, 12.0 and 11.8 at 16, 24.8 and 26.3 at 64.
+    // adapters, rank 64, 17.5 us without and 19.4 with), but for rank 16 only in up to three blocks per CU, since it
+    // leaves two waves per SIMD instead of three. Measured without and with (whole linear_lora, 4352 x 5120): rank 64
+    // 12.6 and 10.4 us at one row, 34.5 and 30.0 at 64 rows of 32 adapters; rank 16 9.4 and 9.1 at one row, 12.0 and
+    // 11.8 at 16, 24.8 and 26.3 at 64.
     const bool early = rs > 1 || tiles * groups <= 3 * (int64_t)device_cus();
     auto go = [&](auto *kernel) {
-        return launch(kernel, dim3((unsigned)tiles, (unsigned)groups), dim3(TILE_WAVES * 64), 0, s, tr, P, num_chunks(lora.k), N,
-                      lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb, base.gscale, out);
+        return launch(kernel, dim3((unsigned)tiles, (unsigned)groups), dim3(TILE_WAVES * 64), 0, s, tr, P,
+                      num_chunks(lora.k), N, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vp, base.y, base.Sb,
+                      base.gscale, out);
     };
     constexpr bool E = sizeof(T) == 4;
     return rs <= 1 ? (early ? go(expand_tile_kernel<T, GATE, 1, E>) : go(expand_tile_kernel<T, GATE, 1, false>))
@@ -818,8 +827,8 @@ int launch_expand(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f
 }
 
 template <int RS>
-int launch_expand_quad(const TileRows &tr, const nvfp4_lora &lora, const f16 *vs, const int *shifts, const f16 *y, f16 *out,
-                       hipStream_t s)
+int launch_expand_quad(const TileRows &tr, int64_t P, const nvfp4_lora &lora, const f16 *vs, const int *shifts, const f16 *y,
+                       f16 *out, hipStream_t s)
 {
     const int groups = (lora.rows + GROUP_COLS - 1) / GROUP_COLS, quads = (tr.t_max + QUAD - 1) / QUAD;
     // About four blocks per CU, of two column groups at least. Measured with 1, 2, 3, 4 and 6 per CU: 24.9, 21.2,
@@ -827,9 +836,14 @@ int launch_expand_quad(const TileRows &tr, const nvfp4_lora &lora, const f16 *vs
     const int per_cu = (int)((int64_t)quads * groups / (4 * (int64_t)device_cus()));
     const int per_block = per_cu < 2 ? 2 : per_cu;
     static_assert(BStage<RS>::LDS <= 64 * 1024, "within the LDS that a launch may use without an opt-in");
-    return launch(expand_quad_kernel<RS>, dim3((unsigned)quads, (unsigned)((groups + per_block - 1) / per_block)), dim3(256),
-                  BStage<RS>::LDS, s, tr, lora.rows, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vs, shifts, y,
-                  out, per_block);
+    // y and out together past 64 MiB, in whole lines: non-temporal, so that they leave the caches to x and v. Measured
+    // without and with (whole lora_add, rows over 4352 x 5120, rank 64, with x, y and out of three calls in turn): 54.4
+    // and 51.0 us at 4096 rows, 79.4 and 74.8 at 8192; but 49.0 and 50.8 at 4096 in place, 35.3 and 36.9 at 2048; 8192
+    // rows of 2048, 31.8 and 33.0; 16384 rows of 1040, 63.0 and 64.4.
+    const bool nt = lora.rows % 64 == 0 && (out == y ? 1 : 2) * P * lora.rows * (int64_t)sizeof(f16) > (int64_t(64) << 20);
+    return launch(nt ? expand_quad_kernel<RS, true> : expand_quad_kernel<RS, false>,
+                  dim3((unsigned)quads, (unsigned)((groups + per_block - 1) / per_block)), dim3(256), BStage<RS>::LDS, s, tr,
+                  lora.rows, lora.rank, reinterpret_cast<const f16 *>(lora.b), lora.scale, vs, shifts, y, out, per_block);
 }
 
 constexpr int64_t MAX_COPY_BLOCKS = 1 << 20;  // a launch holds fewer than 2^32 threads
@@ -858,11 +872,11 @@ int add_quads(const TileRows &tr, int64_t P, const f16 *x, const nvfp4_lora &lor
                 vs, shifts, fold_blocks, tr.pair_expert, y, lora.rows, out);
     if (st != NVFP4_OK) return st;
     const int rs = (rank + 15) / 16;
-    return rs <= 1 ? launch_expand_quad<1>(tr, lora, vs, shifts, y, out, s)
-         : rs <= 2 ? launch_expand_quad<2>(tr, lora, vs, shifts, y, out, s)
-         : rs <= 4 ? launch_expand_quad<4>(tr, lora, vs, shifts, y, out, s)
-         : rs <= 8 ? launch_expand_quad<8>(tr, lora, vs, shifts, y, out, s)
-                   : launch_expand_quad<16>(tr, lora, vs, shifts, y, out, s);
+    return rs <= 1 ? launch_expand_quad<1>(tr, P, lora, vs, shifts, y, out, s)
+         : rs <= 2 ? launch_expand_quad<2>(tr, P, lora, vs, shifts, y, out, s)
+         : rs <= 4 ? launch_expand_quad<4>(tr, P, lora, vs, shifts, y, out, s)
+         : rs <= 8 ? launch_expand_quad<8>(tr, P, lora, vs, shifts, y, out, s)
+                   : launch_expand_quad<16>(tr, P, lora, vs, shifts, y, out, s);
 }
 
 }  // namespace

@@ -108,6 +108,9 @@ ADD += [(6100, 1040, 1664, 16, 7, "mixed"), (9001, 1648, 2176, 8, 180, "mixed"),
         (2050, 1104, 2176, 40, 60, "own"), (1200, 2000, 1408, 64, 1, "one"), (1030, 912, 1152, 120, 5, "mixed"),
         (515, 1232, 1280, 200, 16, "mixed"), (700, 1424, 128, 256, 2, "runs"), (2100, 1040, 1152, 64, 4, "none")]
 
+# rows past the caches: y and out together more than 64 MiB, then each of them (the call in place too)
+ADD += [(4100, 4160, 128, 64, 5, "mixed"), (8330, 4160, 256, 8, 2, "mixed")]
+
 
 @pytest.mark.parametrize("whole", [True, False])
 @pytest.mark.parametrize("rows,n,k,rank,adapters,how", ADD)
