@@ -701,14 +701,17 @@ def _current_device(t: torch.Tensor) -> int:
 def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
     """Device pointer of a contiguous tensor of this type on the current device, where the launch goes. The
     checks of _dev in few steps, since a small call's host time is most of its time."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype is dtype and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev >= 0 and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor: refused below
+        pass
     _dev(t, name, dtype)
     raise ValueError(f"{name} lies on {t.device}, the current device is cuda:{dev}")
 
 
 def _raw_stream(stream, dev: int) -> int:
-    return stream.cuda_stream if stream is not None else _stream(None, dev)
+    return _RAW_STREAM(dev) if stream is None and _RAW_STREAM is not None else _stream(stream, dev)
 
 
 def _rows_plan(plan: torch.Tensor, M: int, topk: int, E: int, dev: int) -> int:
@@ -812,21 +815,33 @@ class LoRATensor:
         self.rows = b.shape[1]
         if b.shape[0] != self.adapters or b.shape[2] != self.rank or scale.shape[0] != self.adapters:
             raise ValueError("inconsistent low-rank adapter shapes")
+        self._dev, self._byref, self._built = -1, None, None
+
+    def _layout(self) -> tuple:
+        """Where a, b and scale lie and how: what the descriptor was built from."""
+        a, b, scale = self.a, self.b, self.scale
+        return (a.data_ptr(), b.data_ptr(), scale.data_ptr(), a.shape, b.shape, scale.shape, a.dtype, b.dtype, scale.dtype,
+                a.is_contiguous() and b.is_contiguous() and scale.is_contiguous())
+
+    def _ref(self, dev: int):
+        """A reference to the C descriptor for a call on device `dev`; the descriptor is built once and kept while a, b
+        and scale lie in the same memory with the same shapes, types and order (a training step may give a tensor new
+        storage, or a view of what it had)."""
+        if self._built != self._layout():
+            self.desc()
+        if self._dev != dev:  # built under another current device
+            _ptr(self.a, "lora.a", torch.float16, dev)
+        return self._byref
 
     def desc(self) -> nvfp4_lora:
-        """The C descriptor; built once and reused while a, b and scale are the same tensors in the same memory (a
-        training step may give a tensor new storage)."""
-        c = self.__dict__.get("_desc")
-        if (c is not None and c[0] is self.a and c[1] is self.b and c[2] is self.scale
-                and c[3].a == c[0].data_ptr() and c[3].b == c[1].data_ptr() and c[3].scale == c[2].data_ptr()):
-            return c[3]
+        """The C descriptor of a, b and scale as they are."""
         if (self.a.shape != (self.adapters, self.rank, self.k) or self.b.shape != (self.adapters, self.rows, self.rank)
                 or self.scale.shape != (self.adapters,)):
             raise ValueError("a, b and scale must keep the shapes that the LoRATensor was made with")
         dev = _current_device(self.a)
         d = nvfp4_lora(_ptr(self.a, "a", torch.float16, dev), _ptr(self.b, "b", torch.float16, dev),
                        _ptr(self.scale, "scale", torch.float32, dev), self.adapters, self.rows, self.k, self.rank)
-        self._desc = (self.a, self.b, self.scale, d)
+        self._dev, self._byref, self._built = dev, C.byref(d), self._layout()
         return d
 
 
@@ -869,18 +884,15 @@ def nvfp4_lora_add(plan: torch.Tensor, M: int, topk: int, x: torch.Tensor, lora:
         _shape(out, "out", rows)
     ws = _lora_ws(ws, _add_ws_bytes(P, lora.k, lora.rank), x.device, stream)
     dev = _current_device(plan)
-    if lora.a.get_device() != dev:  # the descriptor may have been built under another current device
-        _ptr(lora.a, "lora.a", torch.float16, dev)
     _check("nvfp4_lora_add", lib().nvfp4_lora_add(
         _rows_plan(plan, M, topk, lora.adapters, dev), M, topk, order, _ptr(x, "x", torch.float16, dev),
-        C.byref(lora.desc()), _ptr(y, "y", torch.float16, dev), _ptr(out, "out", torch.float16, dev),
+        lora._ref(dev), _ptr(y, "y", torch.float16, dev), _ptr(out, "out", torch.float16, dev),
         _ptr(ws, "ws", ws.dtype, dev), ws.nbytes, _raw_stream(stream, dev)))
     return out
 
 
-def _linear_lora(plan, x, w: NVFP4Tensor, lora: LoRATensor, out, name: str, cols: int, ws, stream):
-    """The checks of the projections with adapters. Returns the output tensor and the C arguments: those before
-    the adapters' descriptor and those behind it."""
+def _linear_lora(call: str, plan, x, w: NVFP4Tensor, lora: LoRATensor, out, name: str, cols: int, layout: tuple, ws, stream):
+    """The projections with adapters: `call` of the library on checked arguments. Returns the output tensor."""
     shape = x.shape
     if len(shape) != 2 or shape[1] != w.k:
         raise ValueError(f"x must have shape (M, {w.k}), got {tuple(shape)}")
@@ -894,20 +906,21 @@ def _linear_lora(plan, x, w: NVFP4Tensor, lora: LoRATensor, out, name: str, cols
     ws = _lora_ws(ws, _linear_ws_bytes(M, w.rows, w.k, lora.rank), x.device, stream)
     dev = _current_device(plan)
     plan_ptr = _rows_plan(plan, M, 1, lora.adapters, dev)
-    if w.codes.get_device() != dev or lora.a.get_device() != dev:  # built under another current device
-        _ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(lora.a, "lora.a", torch.float16, dev)
-    return (out, (plan_ptr, _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc())),
-            (C.byref(lora.desc()), _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev),
-             ws.nbytes, _raw_stream(stream, dev)))
+    if w.codes.get_device() != dev:  # built under another current device
+        _ptr(w.codes, "w.codes", torch.uint8, dev)
+    status = getattr(lib(), call)(
+        plan_ptr, _ptr(x, "x", torch.float16, dev), M, C.byref(w.desc()), *layout, lora._ref(dev),
+        _ptr(out, name, torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev), ws.nbytes, _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check(call, status)
+    return out
 
 
 def nvfp4_linear_lora(plan: torch.Tensor, x: torch.Tensor, w: NVFP4Tensor, lora: LoRATensor,
                       y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """nvfp4_linear with each token's low-rank adapter: y = fp16(x W^T + scale_a (x A_a^T) B_a^T). plan:
     nvfp4_moe_plan of the adapter ids [M, 1] over lora.adapters (-1: no adapter). Returns y [M, N]."""
-    y, head, tail = _linear_lora(plan, x, w, lora, y, "y", w.rows, ws, stream)
-    _check("nvfp4_linear_lora", lib().nvfp4_linear_lora(*head, *tail))
-    return y
+    return _linear_lora("nvfp4_linear_lora", plan, x, w, lora, y, "y", w.rows, (), ws, stream)
 
 
 def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tensor, lora: LoRATensor, layout: int = 0,
@@ -915,6 +928,4 @@ def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tens
                              stream=None) -> torch.Tensor:
     """nvfp4_linear_swiglu with each token's low-rank adapter on the gate and up rows (lora.rows = 2I, in
     w13's row order) before SwiGLU. Returns h fp16 [M, I]."""
-    h, head, tail = _linear_lora(plan, x, w13, lora, h, "h", w13.rows // 2, ws, stream)
-    _check("nvfp4_linear_swiglu_lora", lib().nvfp4_linear_swiglu_lora(*head, layout, *tail))
-    return h
+    return _linear_lora("nvfp4_linear_swiglu_lora", plan, x, w13, lora, h, "h", w13.rows // 2, (layout,), ws, stream)

@@ -198,3 +198,56 @@ def test_wrappers_refuse_cpu_tensors():
         G.nvfp4_lora_add(_plan(), M, TOPK, _f16(M * TOPK, K), _t(), _f16(M * TOPK, N))
     with pytest.raises(ValueError, match="GPU tensor"):
         G.nvfp4_linear_lora(_plan(M, 1), _f16(M, K), _w(), _t())
+
+
+def test_adapters_changed_in_place_are_checked_again(monkeypatch):
+    """Data put in place of an adapter's at the same address: another shape, type or order raises, as it does at another
+    address, and what fits is taken. The library and the device checks are replaced, so that CPU tensors do."""
+    def ptr(t, name, dtype, dev):
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    class Library:
+        def nvfp4_lora_add(self, plan, m, topk, order, x, lora, *rest):
+            self.seen = lora._obj
+            return OK
+
+        def nvfp4_linear_lora(self, plan, x, m, w, lora, *rest):
+            self.seen = lora._obj
+            return OK
+
+    need, stub = G.nvfp4_lora_add_ws_bytes(M * TOPK, K, R), Library()
+    plans, ws = (_plan(), _plan(M, 1)), torch.zeros(need + G.nvfp4_linear_lora_ws_bytes(M, N, K, R), dtype=torch.uint8)
+    _lib._plan_bytes(M, TOPK, E), _lib._plan_bytes(M, 1, E), _lib._add_ws_bytes(M * TOPK, K, R), _lib._linear_ws_bytes(M, N, K, R)
+    monkeypatch.setattr(_lib, "lib", lambda: stub)
+    monkeypatch.setattr(_lib, "_ptr", ptr)
+    monkeypatch.setattr(_lib, "_current_device", lambda t: -1)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(_lib, "_dev", lambda t, name, dtype: t.data_ptr())
+    calls = [lambda t: G.nvfp4_lora_add(plans[0], M, TOPK, _f16(M * TOPK, K), t, _f16(M * TOPK, N), ws=ws),
+             lambda t: G.nvfp4_linear_lora(plans[1], _f16(M, K), _w(), t, ws=ws)]
+    changes = [  # tensor, its new data at the same address
+        ("a", lambda d: d[:, :8]), ("a", lambda d: d[:4]), ("a", lambda d: d.view(2 * E, R // 2, K)), ("a", lambda d: d.view(torch.bfloat16)),
+        ("a", lambda d: d.as_strided((E, R, K), (R * K, 1, R))), ("b", lambda d: d[:, :, :8]), ("b", lambda d: d.view(E, R, N)),
+        ("b", lambda d: d.as_strided((E, N, R), (N * R, 1, N))), ("b", lambda d: d.view(torch.int16)), ("scale", lambda d: d[:2]),
+        ("scale", lambda d: d.view(torch.int32)), ("scale", lambda d: d.as_strided((E,), (0,)))]
+    for call in calls:
+        for name, change in changes:
+            lora = _t()
+            call(lora)
+            t = getattr(lora, name)
+            old, before = t.data, (t.data_ptr(), stub.seen.a, stub.seen.b, stub.seen.scale)
+            t.data = change(old)
+            assert t.data_ptr() == before[0]
+            with pytest.raises((ValueError, TypeError), match="must"):
+                call(lora)
+            t.data = old  # as it was: taken again
+            call(lora)
+            assert (t.data_ptr(), stub.seen.a, stub.seen.b, stub.seen.scale) == before
+            t.data = old.clone()  # other memory that fits
+            call(lora)
+            assert getattr(stub.seen, name) == t.data_ptr() != before[0]
+            assert (stub.seen.adapters, stub.seen.rows, stub.seen.k, stub.seen.rank) == (E, N, K, R)
