@@ -500,10 +500,17 @@ __global__ __launch_bounds__(TILE_WAVES * 64) void expand_tile_kernel(TileRows t
     };
     const int m0 = lane >> 3, r_first = __shfl(row, m0, 64), r_second = __shfl(row, m0 + 8, 64);
     if (plain_rows) {
-        start(r_first);
-        finish(m0, r_first, 0.f);
-        start(r_second);
-        finish(m0 + 8, r_second, 0.f);
+        if constexpr (sizeof(T) == sizeof(f16)) {  // y's bits: a conversion would change signalling NaN
+            start(r_first);
+            if (r_first >= 0 && n < cols) *reinterpret_cast<f16x8 *>(out + (size_t)r_first * cols + n) = bl[0].v;
+            start(r_second);
+            if (r_second >= 0 && n < cols) *reinterpret_cast<f16x8 *>(out + (size_t)r_second * cols + n) = bl[0].v;
+        } else {
+            start(r_first);
+            finish(m0, r_first, 0.f);
+            start(r_second);
+            finish(m0 + 8, r_second, 0.f);
+        }
         return;
     }
     const f16 *be = b + (size_t)e * N * rank;

@@ -453,3 +453,24 @@ def test_expert_adapters_between_sort_and_combine():
             d = _low_rank(case["x"][t:t + 1], nid[t, s:s + 1], a, b, scale)[0]
             ref[t] += float(tw[t, s]) * (h0[pos[t, s]] + d)
     assert_rows_close_all(out.cpu().double().numpy(), ref, "experts with adapters")
+
+
+# below and above the work at which lora_add goes by groups of 64 rows
+@pytest.mark.parametrize("rows,n,k,rank,adapters", [(37, 80, 640, 24, 3), (2100, 1040, 1152, 64, 4)])
+def test_rows_without_an_adapter_keep_every_bit(rows, n, k, rank, adapters):
+    """y's rows without an adapter hold every fp16 bit pattern (quiet and signalling NaN, infinities, zeros of both
+    signs, subnormals); out holds the same, into another buffer and in place."""
+    rng = np.random.default_rng([14, rows])
+    ids = _ids(rng, rows, adapters, "mixed")
+    none = (ids < 0) | (ids >= adapters)
+    bits = rng.integers(0, 1 << 16, (rows, n)).astype(np.uint16)
+    at = np.nonzero(none)[0]
+    special = np.array([0x7C01, 0xFC01, 0x7DFF, 0xFDFF, 0x7E00, 0xFFFF, 0x7C00, 0xFC00, 0x8000, 0x0001, 0x83FF], np.uint16)
+    bits[at[0], :special.size], bits[at[-1], -special.size:] = special, special
+    plan = G.nvfp4_moe_plan(_dev(ids.reshape(rows, 1)), adapters)
+    lora = _tensor(*_adapters(rng, adapters, n, k, rank, True))
+    x, y = _dev(_x(rng, rows, k, True)), _dev(bits.view(np.int16)).view(torch.float16)
+    out = G.nvfp4_lora_add(plan, rows, 1, x, lora, y, out=_poisoned(rows, n))
+    assert np.array_equal(_bits(out)[none], bits[none])
+    G.nvfp4_lora_add(plan, rows, 1, x, lora, y, out=y)
+    assert np.array_equal(_bits(y)[none], bits[none])
