@@ -108,6 +108,7 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // for larger ones: decoded weights kept for all rows, one block per CU, 64 rows of x staged at once (whole call,
 // 4352 x 5120, KEEP off and on: 31.0 and 25.7 us at 128 rows, 167 and 116 at 1024, 684 and 508 at 4096).
 constexpr int FUSED_WAVES = 12;  // most waves per block
+constexpr int FUSED_GRID_X = 1 << 20;  // blocks along x, then y: a launch holds fewer than 2^32 threads along one axis
 
 template <bool KEEP>
 __global__ __launch_bounds__(FUSED_WAVES * 64, KEEP ? 3 : 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
@@ -120,11 +121,13 @@ __global__ __launch_bounds__(FUSED_WAVES * 64, KEEP ? 3 : 4) void linear_shrink_
     constexpr int ROWS = KEEP ? 64 : 32;  // activation rows staged in LDS per pass
     __shared__ __attribute__((aligned(16))) unsigned char xs[ROWS * XS_PITCH];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
-    if ((int)blockIdx.x < shrink_blocks) {
-        shrink_unit(tr, (int64_t)blockIdx.x * nwaves + wave, x, M, K, rank, a, vp);
+    const int block = (int)blockIdx.y * FUSED_GRID_X + (int)blockIdx.x;
+    if (block < shrink_blocks) {
+        shrink_unit(tr, (int64_t)block * nwaves + wave, x, M, K, rank, a, vp);
         return;
     }
-    const int S = num_chunks(K), blk = (int)blockIdx.x - shrink_blocks, c = blk % S;
+    const int S = num_chunks(K), blk = block - shrink_blocks, c = blk % S;
+    if ((blk / S) * nwaves >= N >> 4) return;  // the whole block: behind the last one of a grid in several rows
     const int n = lane & 15, q = lane >> 4;
     const int t = (blk / S) * nwaves + wave;  // this wave's weight tile
     const bool tv = t < (N >> 4);             // wave-uniform
@@ -935,8 +938,9 @@ int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, 
     const bool keep = M > 64 || (M > 32 && blocks_of(waves(cus)) <= cus);
     const int T = waves(keep ? cus : (M > 16 ? 3 : 4) * cus);
     const int64_t blocks = blocks_of(T);
-    if (blocks * T * 64 >= (int64_t(1) << 32)) return NVFP4_ERR_UNSUPPORTED;  // more threads than a launch holds
-    const int st = launch(keep ? linear_shrink_kernel<true> : linear_shrink_kernel<false>, dim3((unsigned)blocks),
+    const dim3 grid((unsigned)(blocks < FUSED_GRID_X ? blocks : FUSED_GRID_X),
+                    (unsigned)((blocks + FUSED_GRID_X - 1) / FUSED_GRID_X));
+    const int st = launch(keep ? linear_shrink_kernel<true> : linear_shrink_kernel<false>, grid,
                           dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K, part, tr, lora.rank,
                           reinterpret_cast<const f16 *>(lora.a), vp, (int)((shrinks + T - 1) / T));
     if (st != NVFP4_OK) return st;

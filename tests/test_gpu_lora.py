@@ -474,3 +474,43 @@ def test_rows_without_an_adapter_keep_every_bit(rows, n, k, rank, adapters):
     assert np.array_equal(_bits(out)[none], bits[none])
     G.nvfp4_lora_add(plan, rows, 1, x, lora, y, out=y)
     assert np.array_equal(_bits(y)[none], bits[none])
+
+
+def test_linear_of_the_largest_batch():
+    """2^26 rows, the most that a plan holds, at the largest rank: a grid of more than 2^32 threads, base partials and
+    outputs past 2^32 bytes. Whole numbers: some rows bit for bit against the exact value, and slices of the batch from
+    both ends and the middle against calls of their own."""
+    m, n, k, rank, adapters, part = 1 << 26, 16, 128, 256, 2, 1 << 16
+    need = 2 * m * (k + n) + G.nvfp4_linear_lora_ws_bytes(m, n, k, rank) + G.nvfp4_moe_plan_bytes(m, 1, adapters)
+    if torch.cuda.mem_get_info()[1] < need + (8 << 30):
+        pytest.skip("needs about 100 GB of device memory")
+    torch.cuda.empty_cache()
+    rng = np.random.default_rng(15)
+    w = _weight(rng, n, k, True)
+    a, b, scale = _adapters(rng, adapters, n, k, rank, True)
+    a[:, 16:] = 0  # sums over the ranks stay exact in FP32
+    a[:, rank - 1] = a[:, 0]
+    x = torch.empty((m // part, part, k), dtype=torch.float16, device="cuda")
+    x.copy_(_dev(_x(rng, part, k, True)))
+    for digit in range(4):  # the number of the part, in digits from -3 to 3: no two parts are alike
+        x[:, :, digit] = ((torch.arange(m // part, device="cuda") // 7 ** digit) % 7 - 3).half()[:, None]
+    x = x.view(m, k)
+    ids = torch.randint(-1, adapters, (m, 1), dtype=torch.int32, device="cuda",
+                        generator=torch.Generator(device="cuda").manual_seed(15))
+    wt, lora = G.NVFP4Tensor.from_numpy(w), _tensor(a, b, scale)
+    plan = G.nvfp4_moe_plan(ids, adapters)
+    y = G.nvfp4_linear_lora(plan, x, wt, lora)
+    torch.cuda.synchronize()
+    line = 1 << 25  # row n * 2 bytes * line = 2^30; base partials there start at 2^31 bytes
+    sel = np.concatenate([[0, 1, m - 1, line - 1, line, 2 * line - 1], rng.integers(0, m, 40)])
+    for t in sel:
+        xt, it = x[t:t + 1].cpu().numpy(), ids[t].cpu().numpy()
+        ref = xt.astype(np.float64) @ O.dequant(*w)[0].T + _low_rank(xt, it, a, b, scale)
+        assert np.array_equal(_bits(y[t]), _rounded(ref)[0]), t
+    for first in (0, m // 2 - part // 2, m - part, 12345 * 4096 + 7):
+        cut = slice(first, first + part)
+        p1 = G.nvfp4_moe_plan(ids[cut].contiguous(), adapters)
+        y1 = G.nvfp4_linear_lora(p1, x[cut].contiguous(), wt, lora)
+        assert torch.equal(y1.view(torch.int16), y[cut].view(torch.int16)), first
+    del x, y, plan, ids
+    torch.cuda.empty_cache()
