@@ -514,3 +514,154 @@ def test_linear_of_the_largest_batch():
         assert torch.equal(y1.view(torch.int16), y[cut].view(torch.int16)), first
     del x, y, plan, ids
     torch.cuda.empty_cache()
+
+
+# gated forms of 65 to 128 ranks; rank 16 in more than three expand blocks per CU (B asked for behind v); more than ten
+# chunks of base partials in the interleaved form, the longest reduction; batches with the weights kept
+SWIGLU_MORE = [(9, 96, 384, 72, 3, "mixed"), (40, 160, 640, 128, 4, "mixed"), (96, 8192, 256, 16, 20, "own"),
+               (96, 8192, 384, 8, 30, "mixed"), (7, 64, 5248, 16, 2, "mixed"), (33, 96, 10752, 40, 3, "mixed"),
+               (5, 32, 16384, 8, 2, "mixed"), (300, 224, 1152, 24, 5, "mixed"), (1111, 96, 640, 16, 3, "runs")]
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("m,rows,k,rank,adapters,how", SWIGLU_MORE)
+def test_swiglu_in_every_form(m, rows, k, rank, adapters, how, layout):
+    test_swiglu(m, rows, k, rank, adapters, how, layout)
+
+
+@pytest.mark.parametrize("m,n,k,rank,adapters,how", [(1111, 96, 1664, 16, 3, "runs"), (2050, 272, 640, 40, 70, "mixed"),
+                                                     (96, 8192, 256, 16, 20, "own"), (300, 64, 5632, 128, 4, "mixed")])
+def test_linear_of_many_rows(m, n, k, rank, adapters, how):
+    test_linear(m, n, k, rank, adapters, how, True)
+
+
+# the groups of 64 rows with more than ten and more than twenty chunks of v
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("rows,n,k,rank,adapters,how", [(700, 1040, 5632, 64, 3, "mixed"), (1500, 160, 10752, 16, 4, "mixed"),
+                                                        (600, 64, 32768, 16, 2, "runs")])
+def test_add_of_long_rows(rows, n, k, rank, adapters, how, whole):
+    test_add(rows, n, k, rank, adapters, how, whole)
+
+
+def test_long_rows_do_not_depend_on_the_batch():
+    """lora_add in groups of 64 rows, eleven chunks, against single rows and against the rows in another order."""
+    rows, n, k, rank, adapters = 700, 1040, 5632, 64, 3
+    rng = np.random.default_rng(16)
+    lora = _tensor(*_adapters(rng, adapters, n, k, rank, False))
+    x, y, ids = _x(rng, rows, k, False), _x(rng, rows, n, False), _ids(rng, rows, adapters, "mixed")
+
+    def call(sel):
+        plan = G.nvfp4_moe_plan(_dev(ids[sel].reshape(-1, 1)), adapters)
+        return _bits(G.nvfp4_lora_add(plan, len(sel), 1, _dev(x[sel]), lora, _dev(y[sel])))
+
+    full, perm = call(np.arange(rows)), rng.permutation(rows)
+    assert np.array_equal(call(perm), full[perm])
+    for t in (0, 15, 16, 333, rows - 1):
+        assert np.array_equal(call(np.array([t])), full[t:t + 1])
+
+
+def test_graph_replays_and_two_streams_of_many_rows():
+    """lora_add in groups of 64 rows (three launches that hand on partials, split terms and shifts in the workspace):
+    two graphs on one plan, workspace and output in turn, and two streams with a workspace each."""
+    rows, n, k, rank, adapters = 1500, 1040, 1152, 80, 5
+    rng = np.random.default_rng(17)
+    lora = _tensor(*_adapters(rng, adapters, n, k, rank, False))
+    sets = [(_dev(_ids(rng, rows, adapters, how).reshape(rows, 1)), _dev(_x(rng, rows, k, False)), _dev(_x(rng, rows, n, False)))
+            for how in ("mixed", "runs", "own")]
+
+    def buffers():
+        return (torch.empty(G.nvfp4_moe_plan_bytes(rows, 1, adapters) // 4, dtype=torch.int32, device="cuda"),
+                torch.empty(G.nvfp4_lora_add_ws_bytes(rows, k, rank), dtype=torch.uint8, device="cuda"),
+                torch.empty((rows, n), dtype=torch.float16, device="cuda"))
+
+    def call(ids, x, y, bufs, stream=None):
+        plan, ws, out = bufs
+        G.nvfp4_moe_plan(ids, adapters, plan=plan, stream=stream)
+        return G.nvfp4_lora_add(plan, rows, 1, x, lora, y, out=out, ws=ws, stream=stream)
+
+    want = [call(*s, buffers()).clone() for s in sets]
+    held = buffers()
+    call(*sets[0], held)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in sets[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(*s, held)
+    for turn in (0, 1, 1, 0, 1, 0):
+        held[1].fill_(0xFF)
+        held[2].zero_()
+        call(*sets[2], buffers())
+        torch.cuda.synchronize()
+        graphs[turn].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held[2].view(torch.int16), want[turn].view(torch.int16)), turn
+    streams, bufs = [torch.cuda.Stream() for _ in range(2)], [buffers() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for j in range(2):
+            call(*sets[j + 1], bufs[j], stream=streams[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert torch.equal(bufs[j][2].view(torch.int16), want[j + 1].view(torch.int16))
+
+
+def test_projection_offsets_past_32_bits():
+    """26000 rows of 4352 x 5120: ten planes of base partials, 4.5 GB. Whole numbers: rows on both sides of the
+    2^32-byte line of the planes bit for bit against the exact value, slices against calls of their own, the gated
+    forms too."""
+    m, n, k, rank, adapters, part = 26000, 4352, 5120, 16, 3, 100
+    rng = np.random.default_rng(18)
+    w = _weight(rng, n, k, True)
+    a, b, scale = _adapters(rng, adapters, n, k, rank, True)
+    ids = _ids(rng, m, adapters, "mixed")
+    x = torch.randint(-3, 4, (m, k), generator=torch.Generator(device="cuda").manual_seed(18), device="cuda").half()
+    wt, lora = G.NVFP4Tensor.from_numpy(w), _tensor(a, b, scale)
+    plan = G.nvfp4_moe_plan(_dev(ids.reshape(m, 1)), adapters)
+    ws = torch.empty(G.nvfp4_linear_lora_ws_bytes(m, n, k, rank), dtype=torch.uint8, device="cuda")
+    line = 2 ** 30 // n - 9 * m  # the row whose partial in the last plane crosses the line
+    assert 2 < line < m - 2
+    y = G.nvfp4_linear_lora(plan, x, wt, lora, ws=ws)
+    full = O.dequant(*w)[0]
+    for t in np.concatenate([[0, 1, m - 1], np.arange(line - 2, line + 3), rng.integers(0, m, 12)]):
+        xt = x[t:t + 1].cpu().numpy()
+        ref = xt.astype(np.float64) @ full.T + _low_rank(xt, ids[t:t + 1], a, b, scale)
+        assert np.array_equal(_bits(y[t]), _rounded(ref)[0]), t
+    h = [G.nvfp4_linear_swiglu_lora(plan, x, wt, lora, layout, ws=ws) for layout in (0, 1)]
+    for first in (0, line - part // 2, m - part):
+        cut = slice(first, first + part)
+        p1, x1 = G.nvfp4_moe_plan(_dev(ids[cut].reshape(part, 1)), adapters), x[cut].contiguous()
+        assert torch.equal(G.nvfp4_linear_lora(p1, x1, wt, lora).view(torch.int16), y[cut].view(torch.int16))
+        for layout in (0, 1):
+            h1 = G.nvfp4_linear_swiglu_lora(p1, x1, wt, lora, layout)
+            assert torch.equal(h1.view(torch.int16), h[layout][cut].view(torch.int16)), layout
+
+
+def test_expert_down_projections_with_adapters():
+    """Adapters of a MoE's experts where a model has them: tokens sorted by expert, each expert's gated projection and
+    down projection with nvfp4_linear on its rows, the down projection's adapters on all sorted rows at once, rows
+    combined with the routing weights; against the same in 64 bits from the library's own h."""
+    m, e, topk, k, i, rank = 40, 8, 2, 256, 128, 16
+    rng = np.random.default_rng(19)
+    case = S.moe_case(S.MoEShape(m=m, e=e, topk=topk, k=k, i=i), workload="tiny")
+    w13, w2 = G.NVFP4Tensor.from_numpy(case["w13"]), G.NVFP4Tensor.from_numpy(case["w2"])
+    ids, tw, plan = G.nvfp4_moe_route(_dev(rng.standard_normal((m, e)).astype(np.float32)), topk)
+    f = G.plan_fields(plan, m, topk, e)
+    a, b, scale = _adapters(rng, e, k, i, rank, False)
+    h = G.nvfp4_moe_w13_swiglu(plan, m, topk, e, _dev(case["x"]), w13)  # in bucket order
+    ys = torch.empty((m * topk, k), dtype=torch.float16, device="cuda")
+    for ex in range(e):
+        first, last = int(f["offsets"][ex]), int(f["offsets"][ex + 1])
+        if first < last:
+            one = G.NVFP4Tensor(w2.codes[ex:ex + 1], w2.scales[ex:ex + 1], w2.global_scale[ex:ex + 1])
+            ys[first:last] = G.nvfp4_linear(h[first:last], one)
+    G.nvfp4_lora_add(plan, m, topk, h, _tensor(a, b, scale), ys, order=1, out=ys)
+    out = G.nvfp4_moe_unpermute(plan, m, topk, e, ys, tw)
+    h64, w64 = h.cpu().numpy(), O.dequant(*case["w2"])
+    pos, nid, ref = f["pos_of_pair"].reshape(m, topk), ids.cpu().numpy(), np.zeros((m, k))
+    for t in range(m):
+        for s in range(topk):
+            row = h64[pos[t, s]:pos[t, s] + 1]
+            ref[t] += float(tw[t, s]) * (row.astype(np.float64) @ w64[nid[t, s]].T + _low_rank(row, nid[t, s:s + 1], a, b, scale))[0]
+    assert_rows_close_all(out.cpu().double().numpy(), ref, "down projections with adapters")

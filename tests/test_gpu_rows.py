@@ -369,3 +369,13 @@ def test_sort_and_combine_around_experts():
     assert (diff <= tol).all(), float((diff / tol).max())
     dys, dw = G.nvfp4_moe_unpermute_grad(plan, m, topk, e, x, ys, tw)
     _check_grad(dys, dw, case["x"], ys.cpu().numpy(), tw.cpu().numpy(), pos, "combine")
+
+
+# bucket rows past the L2s in whole lines, one to eight slots at once and two rounds of six; rows shorter than a wave
+LARGE = [(8200, 1, 16, 2048), (4100, 2, 16, 2048), (2740, 3, 16, 2048), (2060, 4, 16, 2048), (1640, 5, 16, 2048),
+         (1370, 6, 16, 2048), (1175, 7, 16, 2048), (1030, 8, 16, 2048), (6000, 12, 40, 256), (140000, 2, 8, 64)]
+
+
+@pytest.mark.parametrize("m,topk,e,k", LARGE)
+def test_rows_past_the_caches(m, topk, e, k):
+    test_rows(m, topk, e, k, "some")
