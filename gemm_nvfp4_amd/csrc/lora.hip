@@ -108,9 +108,12 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // for larger ones: decoded weights kept for all rows, one block per CU, 64 rows of x staged at once (whole call,
 // 4352 x 5120, KEEP off and on: 31.0 and 25.7 us at 128 rows, 167 and 116 at 1024, 684 and 508 at 4096).
 constexpr int FUSED_WAVES = 12;  // most waves per block
-constexpr int FUSED_GRID_X = 1 << 20;  // blocks along x, then y: a launch holds fewer than 2^32 threads along one axis
+// A launch holds fewer than 2^32 threads along one axis. WIDE, for grids past that: FUSED_GRID_X blocks along x, then y. (In
+// its own instance: the index in every grid cost the kernel that keeps the weights two spilled registers, 25.9 instead of
+// 24.5 us at 128 rows of 4352 x 5120.)
+constexpr int FUSED_GRID_X = 1 << 20;
 
-template <bool KEEP>
+template <bool KEEP, bool WIDE>
 __global__ __launch_bounds__(FUSED_WAVES * 64, KEEP ? 3 : 4) void linear_shrink_kernel(const f16 *__restrict__ x, int M,
                                                                             const uint8_t *__restrict__ codes,
                                                                             const uint8_t *__restrict__ scales, int N, int K,
@@ -121,13 +124,13 @@ __global__ __launch_bounds__(FUSED_WAVES * 64, KEEP ? 3 : 4) void linear_shrink_
     constexpr int ROWS = KEEP ? 64 : 32;  // activation rows staged in LDS per pass
     __shared__ __attribute__((aligned(16))) unsigned char xs[ROWS * XS_PITCH];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
-    const int block = (int)blockIdx.y * FUSED_GRID_X + (int)blockIdx.x;
+    const int block = (WIDE ? (int)blockIdx.y * FUSED_GRID_X : 0) + (int)blockIdx.x;
     if (block < shrink_blocks) {
         shrink_unit(tr, (int64_t)block * nwaves + wave, x, M, K, rank, a, vp);
         return;
     }
     const int S = num_chunks(K), blk = block - shrink_blocks, c = blk % S;
-    if ((blk / S) * nwaves >= N >> 4) return;  // the whole block: behind the last one of a grid in several rows
+    if (WIDE && (blk / S) * nwaves >= N >> 4) return;  // the whole block: behind the last one
     const int n = lane & 15, q = lane >> 4;
     const int t = (blk / S) * nwaves + wave;  // this wave's weight tile
     const bool tv = t < (N >> 4);             // wave-uniform
@@ -938,10 +941,11 @@ int run_linear_lora(const PlanView &pv, const PlanLayout &L, const uint16_t *x, 
     const bool keep = M > 64 || (M > 32 && blocks_of(waves(cus)) <= cus);
     const int T = waves(keep ? cus : (M > 16 ? 3 : 4) * cus);
     const int64_t blocks = blocks_of(T);
-    const dim3 grid((unsigned)(blocks < FUSED_GRID_X ? blocks : FUSED_GRID_X),
-                    (unsigned)((blocks + FUSED_GRID_X - 1) / FUSED_GRID_X));
-    const int st = launch(keep ? linear_shrink_kernel<true> : linear_shrink_kernel<false>, grid,
-                          dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K, part, tr, lora.rank,
+    const bool wide = blocks * T * 64 >= (int64_t(1) << 32);  // then M is far beyond 64
+    const dim3 grid = wide ? dim3(FUSED_GRID_X, (unsigned)((blocks + FUSED_GRID_X - 1) / FUSED_GRID_X)) : dim3((unsigned)blocks);
+    const int st = launch(wide ? linear_shrink_kernel<true, true> : keep ? linear_shrink_kernel<true, false>
+                                                                         : linear_shrink_kernel<false, false>,
+                          grid, dim3((unsigned)(T * 64)), 0, s, xh, M, w.codes, w.scales, N, K, part, tr, lora.rank,
                           reinterpret_cast<const f16 *>(lora.a), vp, (int)((shrinks + T - 1) / T));
     if (st != NVFP4_OK) return st;
     const BaseOf<float> base{part, S, w.global_scale, true};
