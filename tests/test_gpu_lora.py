@@ -665,3 +665,19 @@ def test_expert_down_projections_with_adapters():
             row = h64[pos[t, s]:pos[t, s] + 1]
             ref[t] += float(tw[t, s]) * (row.astype(np.float64) @ w64[nid[t, s]].T + _low_rank(row, nid[t, s:s + 1], a, b, scale))[0]
     assert_rows_close_all(out.cpu().double().numpy(), ref, "down projections with adapters")
+
+
+@pytest.mark.parametrize("rows,n,k", [(21, 80, 640), (1300, 2000, 1152)])
+def test_a_part_of_a_larger_table(rows, n, k):
+    """Adapters 3 to 5 of a table of nine as a descriptor of their own, the ids counted from there."""
+    rng = np.random.default_rng([20, rows])
+    a, b, scale = _adapters(rng, 9, n, k, 64, True)
+    table = _tensor(a, b, scale)
+    part = G.LoRATensor(table.a[3:6], table.b[3:6], table.scale[3:6])
+    x, y, ids = _dev(_x(rng, rows, k, True)), _dev(_x(rng, rows, n, True)), _ids(rng, rows, 3, "mixed")
+    ids[ids >= 3] = -1
+    want = np.where(ids >= 0, ids + 3, -1).astype(np.int32)
+    out = G.nvfp4_lora_add(G.nvfp4_moe_plan(_dev(ids.reshape(rows, 1)), 3), rows, 1, x, part, y)
+    ref = G.nvfp4_lora_add(G.nvfp4_moe_plan(_dev(want.reshape(rows, 1)), 9), rows, 1, x, table, y)
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    assert np.array_equal(_bits(out), _rounded(y.cpu().double().numpy() + _low_rank(x.cpu().numpy(), want, a, b, scale)))
