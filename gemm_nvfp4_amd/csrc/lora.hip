@@ -105,8 +105,11 @@ int64_t shrink_units(const TileRows &tr, const nvfp4_lora &lora)
 // so the sum over c is bitwise nvfp4_linear's. Small batches decode the weights
 // anew for every 16 rows of x: the 100 registers of a wave then let all blocks of a launch be resident at once,
 // several to a CU, so that the shrink's, whose first loads wait for the plan, run beside the weight stream. KEEP,
-// for larger ones: decoded weights kept for all rows, one block per CU, 64 rows of x staged at once (whole call,
-// 4352 x 5120, KEEP off and on: 31.0 and 25.7 us at 128 rows, 167 and 116 at 1024, 684 and 508 at 4096).
+// for larger ones: decoded weights kept for all rows, one block per CU, 64 rows of x staged at once (whole call in a
+// captured graph, 4352 x 5120, rank 16, KEEP off and on: 15.8 and 18.3 us at 32 rows, 18.2 and 18.3 at 33, 22.1 and
+// 20.5 at 64, 30.6 and 24.5 at 128, 242 and 125 at 1024, 819 and 506 at 4096). The partials are S = K / 512 planes of
+// the whole output, written here and read by the second launch: at 4096 rows 713 MB each way, 280 us of the call at the
+// rate of a copy.
 constexpr int FUSED_WAVES = 12;  // most waves per block
 // A launch holds fewer than 2^32 threads along one axis. WIDE, for grids past that: FUSED_GRID_X blocks along x, then y. (In
 // its own instance: the index in every grid cost the kernel that keeps the weights two spilled registers, 25.9 instead of
@@ -790,10 +793,14 @@ TileRows tile_rows(const PlanView &pv, const PlanLayout &L, int bucket)
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// The quad kernels take batches of enough work, with two row tiles per adapter on average. Measured, tile against
-// quad kernels (us): rank 16, K = 5120, N = 4352, one adapter: 18.4 / 17.9 at 1536 rows, 36.1 / 29.6 at 4096; rank
-// 16, K = 2048, N = 1024: 12.1 / 13.5 at 2048, 22.3 / 23.7 at 8192; rank 64, K = 5120, N = 4352: 15.5 / 15.9 at 256,
-// 32.7 / 21.7 at 1024; 64 adapters there: 35.5 / 50.1 at 1024, 58.4 / 34.6 at 2048.
+// The quad kernels take batches of enough work, with at least two row tiles for each adapter of the table. Measured in a
+// captured graph with x, y and out of three calls in turn, tile against quad kernels (us): rank 16, K = 5120, N = 4352,
+// one adapter: 15.3 / 16.1 at 1024 rows, 18.1 / 17.9 at 1536, 23.3 / 21.1 at 2048, 46.8 / 33.0 at 4096; rank 16, K = 2048,
+// N = 1024: 15.4 / 17.8 at 4096, 22.9 / 23.4 at 8192, 46.8 / 42.3 at 16384; with 64 adapters there 15.8 / 17.8 at 4096,
+// 23.2 / 22.7 at 6000; rank 8, K = N = 4096: 18.6 / 20.5 at 2048, 35.7 / 33.2 at 4096; rank 64, K = 5120, N = 4352: 16.1 /
+// 15.4 at 256, 23.4 / 17.7 at 512, 34.3 / 20.1 at 1024; with 64 adapters there 35.8 / 49.6 at 1024 (16 rows each, four
+// adapters to a quad), 59.2 / 35.0 at 2048. The host knows the table, not how many of its adapters a batch uses: 4096 rows of 8
+// adapters out of more than 128 take the tile kernels, 107 us at 256 where the quad kernels take 47.
 bool use_quads(int64_t P, const nvfp4_lora &lora)
 {
     return P * lora.rank * ((int64_t)lora.k + lora.rows) >= 250000000 && P >= 32 * (int64_t)lora.adapters;

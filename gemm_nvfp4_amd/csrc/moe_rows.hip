@@ -257,9 +257,12 @@ RowLaunch row_launch(int M, int pieces)
 }
 
 // Whether the bucket rows exceed what the L2s of the eight XCDs hold (4 MB each) and are whole 128-byte lines (lines
-// shared by two rows would go to memory twice). Measured on MI355X, without and with non-temporal rows: 81920 rows of
-// 2048 elements, permute 73.1 and 66.4 us, unpermute 76.4 and 69.0, unpermute_grad 166 and 151; 131072 rows of 1032,
-// permute 49.8 and 100.2, unpermute 56.2 and 65.0.
+// shared by two rows would go to memory twice). Measured on MI355X without / with non-temporal rows (us): permute,
+// unpermute and unpermute_grad of rows of 2048 elements, top-10, buffers changing from call to call: 16 MiB of bucket
+// rows 5.7 / 4.6, 6.4 / 8.4, 12.6 / 11.1; 32 MiB 8.6 / 7.7, 11.1 / 10.0, 20.5 / 18.0; 64 MiB 14.6 / 14.1, 20.9 / 18.3, 34.3 / 31.2;
+// 128 MiB 29.6 / 27.3, 35.1 / 31.0, 62 / 58; 320 MiB 74 / 66, 76 / 69, 152 / 137. (The same buffers again and again, which the
+// 256 MB behind the L2s hold: 64 MiB 12.5 / 13.6, 15.4 / 16.0, 26.1 / 29.4; 128 MiB 23.0 / 26.6, 24.6 / 28.5, 49 / 57.) 131072 rows
+// of 1032: permute 49.8 / 100.2, unpermute 56.2 / 65.0.
 bool streams(int64_t P, int K) { return K % 64 == 0 && P * K * 2 > (int64_t(32) << 20); }
 
 const f16 *half(const uint16_t *p) { return reinterpret_cast<const f16 *>(p); }

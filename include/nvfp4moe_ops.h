@@ -91,7 +91,12 @@ typedef struct nvfp4_lora {
  *
  *   ws   device workspace of at least nvfp4_lora_add_ws_bytes(M*topk, K, rank) or
  *        nvfp4_linear_lora_ws_bytes(M, rows, K, rank) bytes, 16-byte aligned; contents ignored on
- *        entry, overwritten. Calls that share a ws must not run concurrently.
+ *        entry, overwritten. Calls that share a ws must not run concurrently. The projections keep
+ *        ceil(K/512) FP32 planes of the whole output in it (0.7 GB for 4096 rows of 4352 x 5120); large
+ *        batches may be passed in parts, with the same results.
+ * Speed of nvfp4_lora_add: large batches take their faster kernels where M*topk >= 32*adapters, all
+ * adapters of the descriptor counted, used or not. A descriptor may cover a part of a larger table
+ * (a and b at its first adapter, the ids counted from there).
  * Apart from out == y, outputs and ws must not overlap inputs.
  * Requirements: rank % 8 == 0, 8 <= rank <= 256; K % 128 == 0, K <= 32768 (swiglu: 16384);
  * N % 16 == 0 (swiglu: I % 16 == 0), N <= 2^22; adapters <= 4096; those of nvfp4_moe_plan; plan, x, y, out, h,
