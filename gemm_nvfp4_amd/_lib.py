@@ -1,4 +1,4 @@
-"""ctypes binding of libnvfp4moe.so (include/nvfp4moe.h, include/nvfp4moe_ops.h).
+"""ctypes binding of libnvfp4moe.so (include/nvfp4moe.h, include/nvfp4moe_ops.h, include/nvfp4moe_dense.h).
 
 Argument marshalling only: torch tensors supply device memory and the current HIP stream, and
 every step of the computation runs in the library's HIP kernels. There is no fallback. If the
@@ -17,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libnvfp4moe.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "nvfp4moe.h")
 OPS_HEADER = os.path.join(os.path.dirname(HERE), "include", "nvfp4moe_ops.h")
+DENSE_HEADER = os.path.join(os.path.dirname(HERE), "include", "nvfp4moe_dense.h")
 
 NVFP4_OK = 0
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ERR_ALIGN",
@@ -88,6 +89,14 @@ _SIGS = {
                                     _vp]),
     "nvfp4_linear_swiglu_lora": (C.c_int, [_vp, _vp, _i32, C.POINTER(nvfp4_weights), _i32, C.POINTER(nvfp4_lora), _vp,
                                            _vp, _sz, _vp]),
+    "nvfp4_add_rms_norm": (C.c_int, [_vp, _vp, _vp, _i32, _i32, C.c_float, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_add_rms_norm_grad_ws_bytes": (_sz, [_i32, _i32]),
+    "nvfp4_add_rms_norm_grad": (C.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, C.c_float, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_linear_fp8_rows": (C.c_int, [_vp, _vp, _i32, C.POINTER(fp8_channel_weights), _vp, _vp]),
+    "nvfp4_linear_grad_ws_bytes": (_sz, [_i32, _i32, _i32]),
+    "nvfp4_linear_grad": (C.c_int, [_vp, _i32, C.POINTER(nvfp4_weights), _vp, _vp, _sz, _vp]),
+    "nvfp4_linear_swiglu_grad_ws_bytes": (_sz, [_i32, _i32, _i32]),
+    "nvfp4_linear_swiglu_grad": (C.c_int, [_vp, _vp, _i32, C.POINTER(nvfp4_weights), _i32, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -929,3 +938,173 @@ def nvfp4_linear_swiglu_lora(plan: torch.Tensor, x: torch.Tensor, w13: NVFP4Tens
     """nvfp4_linear_swiglu with each token's low-rank adapter on the gate and up rows (lora.rows = 2I, in
     w13's row order) before SwiGLU. Returns h fp16 [M, I]."""
     return _linear_lora("nvfp4_linear_swiglu_lora", plan, x, w13, lora, h, "h", w13.rows // 2, (layout,), ws, stream)
+
+
+# ---- around the dense projections: norm, 8-bit rows, gradients (include/nvfp4moe_dense.h) --------------
+
+def _matrix(t: torch.Tensor, name: str, cols: int | None = None) -> torch.Size:
+    """The shape of a matrix [M, cols]."""
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} must have shape (M, {'K' if cols is None else cols}), got {tuple(shape)}")
+    return shape
+
+
+def _given(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """The caller's output of exactly this shape, or a new one."""
+    if t is None:
+        return _alloc(shape, dtype, like.device, stream)
+    if t.shape != shape:
+        _shape(t, name, shape)
+    return t
+
+
+def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype, dev: int) -> int | None:
+    return None if t is None else _ptr(t, name, dtype, dev)
+
+
+def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                       eps: float = 1e-6, s: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                       q: torch.Tensor | None = None, q_scale: torch.Tensor | None = None, want_y: bool = True,
+                       want_q: bool = False, stream=None):
+    """The residual's sum and the root-mean-square norm of fp16 x [M, K]: t = x + residual,
+    v = t / sqrt(mean(t^2) + eps) * weight. Returns (s, y, q, q_scale): s = fp16(t) (None without a residual and
+    without s), y = fp16(v) (want_y), q uint8 E4M3 bytes of v / q_scale[m] with q_scale FP32 [M] (want_q, for
+    nvfp4_linear_fp8_rows). s may be x or residual, y too (but not s)."""
+    shape = _matrix(x, "x")
+    M, K = shape
+    if weight is not None and weight.shape != (K,):
+        _shape(weight, "weight", (K,))
+    if residual is not None and residual.shape != shape:
+        _shape(residual, "residual", shape)
+    if residual is not None or s is not None:
+        s = _given(s, "s", shape, torch.float16, x, stream)
+    y = _given(y, "y", shape, torch.float16, x, stream) if want_y else None
+    if want_q:
+        q = _given(q, "q", shape, torch.uint8, x, stream)
+        q_scale = _given(q_scale, "q_scale", (M,), torch.float32, x, stream)
+    else:
+        q = q_scale = None
+    dev = _current_device(x)
+    status = lib().nvfp4_add_rms_norm(
+        _ptr(x, "x", torch.float16, dev), _opt(residual, "residual", torch.float16, dev),
+        _opt(weight, "weight", torch.float16, dev), M, K, eps, _opt(s, "s", torch.float16, dev),
+        _opt(y, "y", torch.float16, dev), _opt(q, "q", torch.uint8, dev), _opt(q_scale, "q_scale", torch.float32, dev),
+        _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check("nvfp4_add_rms_norm", status)
+    return s, y, q, q_scale
+
+
+def nvfp4_add_rms_norm_grad_ws_bytes(M: int, K: int) -> int:
+    return int(lib().nvfp4_add_rms_norm_grad_ws_bytes(M, K))
+
+
+def nvfp4_linear_grad_ws_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().nvfp4_linear_grad_ws_bytes(M, N, K))
+
+
+def nvfp4_linear_swiglu_grad_ws_bytes(M: int, rows: int, K: int) -> int:
+    return int(lib().nvfp4_linear_swiglu_grad_ws_bytes(M, rows, K))
+
+
+_norm_grad_ws = functools.lru_cache(maxsize=256)(nvfp4_add_rms_norm_grad_ws_bytes)
+_linear_grad_ws = functools.lru_cache(maxsize=256)(nvfp4_linear_grad_ws_bytes)
+_swiglu_grad_ws = functools.lru_cache(maxsize=256)(nvfp4_linear_swiglu_grad_ws_bytes)
+
+
+def nvfp4_add_rms_norm_grad(t: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor | None = None,
+                            ds: torch.Tensor | None = None, eps: float = 1e-6, dx: torch.Tensor | None = None,
+                            dweight: torch.Tensor | None = None, want_dx: bool = True, want_dweight: bool = True,
+                            ws: torch.Tensor | None = None, stream=None):
+    """The gradient of nvfp4_add_rms_norm at its input t (the s of the forward call; x without a residual): dy is y's
+    gradient, ds the residual stream's own (None: none). Returns (dx fp16 [M, K], the gradient of x and of the
+    residual; dweight FP32 [K]), None for what is not wanted. dx may be dy or ds."""
+    shape = _matrix(t, "t")
+    M, K = shape
+    if dy.shape != shape:
+        _shape(dy, "dy", shape)
+    if ds is not None and ds.shape != shape:
+        _shape(ds, "ds", shape)
+    if weight is not None and weight.shape != (K,):
+        _shape(weight, "weight", (K,))
+    dx = _given(dx, "dx", shape, torch.float16, t, stream) if want_dx else None
+    dev = _current_device(t)
+    if want_dweight:
+        dweight = _given(dweight, "dweight", (K,), torch.float32, t, stream)
+        ws = _lora_ws(ws, _norm_grad_ws(M, K), t.device, stream)
+        work, work_bytes = _ptr(ws, "ws", ws.dtype, dev), ws.nbytes
+    else:
+        dweight, work, work_bytes = None, None, 0
+    status = lib().nvfp4_add_rms_norm_grad(
+        _ptr(t, "t", torch.float16, dev), _ptr(dy, "dy", torch.float16, dev), _opt(ds, "ds", torch.float16, dev),
+        _opt(weight, "weight", torch.float16, dev), M, K, eps, _opt(dx, "dx", torch.float16, dev),
+        _opt(dweight, "dweight", torch.float32, dev), work, work_bytes, _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check("nvfp4_add_rms_norm_grad", status)
+    return dx, dweight
+
+
+def nvfp4_linear_fp8_rows(xq: torch.Tensor, x_scale: torch.Tensor, w: FP8ChannelTensor, y: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """The channel-FP8 projection of 8-bit rows, uint8 E4M3 bytes xq [M, K] with x_scale FP32 [M] (as
+    nvfp4_add_rms_norm writes them): y = fp16(x_scale * s * (e4m3(xq) @ e4m3(W)^T)). Returns y [M, N]."""
+    M = _matrix(xq, "xq", w.k)[0]
+    if x_scale.shape != (M,):
+        _shape(x_scale, "x_scale", (M,))
+    y = _given(y, "y", (M, w.rows), torch.float16, xq, stream)
+    dev = _current_device(xq)
+    if w.codes.shape != (w.rows, w.k) or w.channel_scale.shape != (w.rows,):
+        raise ValueError("codes and channel_scale must keep the shapes that the FP8ChannelTensor was made with")
+    d = fp8_channel_weights(_ptr(w.codes, "w.codes", torch.uint8, dev),
+                            _ptr(w.channel_scale, "w.channel_scale", torch.float32, dev), w.rows, w.k)
+    status = lib().nvfp4_linear_fp8_rows(
+        _ptr(xq, "xq", torch.uint8, dev), _ptr(x_scale, "x_scale", torch.float32, dev), M, C.byref(d),
+        _ptr(y, "y", torch.float16, dev), _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check("nvfp4_linear_fp8_rows", status)
+    return y
+
+
+def _frozen(w: NVFP4Tensor, dev: int):
+    """A reference to the C descriptor of a weight as it is now, all its parts on the current device."""
+    if (w.codes.shape != (w.groups, w.rows, w.k // 2) or w.scales.shape != (w.groups, w.rows, w.k // 16)
+            or w.global_scale.shape != (w.groups,)):
+        raise ValueError("codes, scales and global_scale must keep the shapes that the NVFP4Tensor was made with")
+    return C.byref(nvfp4_weights(_ptr(w.codes, "w.codes", torch.uint8, dev), _ptr(w.scales, "w.scales", torch.uint8, dev),
+                                 _ptr(w.global_scale, "w.global_scale", torch.float32, dev), w.groups, w.rows, w.k))
+
+
+def nvfp4_linear_grad(dy: torch.Tensor, w: NVFP4Tensor, dx: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """The gradient of nvfp4_linear towards its input: dx = dy W of fp16 dy [M, N]. Returns dx fp16 [M, K]. With w13 and
+    the dz of nvfp4_linear_swiglu_grad it is the gated projection's. ws: nvfp4_linear_grad_ws_bytes(M, N, K) bytes."""
+    M = _matrix(dy, "dy", w.rows)[0]
+    dx = _given(dx, "dx", (M, w.k), torch.float16, dy, stream)
+    ws = _lora_ws(ws, _linear_grad_ws(M, w.rows, w.k), dy.device, stream)
+    dev = _current_device(dy)
+    status = lib().nvfp4_linear_grad(
+        _ptr(dy, "dy", torch.float16, dev), M, _frozen(w, dev), _ptr(dx, "dx", torch.float16, dev),
+        _ptr(ws, "ws", ws.dtype, dev), ws.nbytes, _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check("nvfp4_linear_grad", status)
+    return dx
+
+
+def nvfp4_linear_swiglu_grad(x: torch.Tensor, dh: torch.Tensor, w13: NVFP4Tensor, layout: int = 0,
+                             dz: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of nvfp4_linear_swiglu towards its gate and up rows, computed again from fp16 x [M, K]: dh fp16
+    [M, I] is h's gradient. Returns dz fp16 [M, 2I] in w13's row order (the gradient that nvfp4_linear_grad takes to
+    x). ws: nvfp4_linear_swiglu_grad_ws_bytes(M, 2I, K) bytes."""
+    M = _matrix(x, "x", w13.k)[0]
+    if dh.shape != (M, w13.rows // 2):
+        _shape(dh, "dh", (M, w13.rows // 2))
+    dz = _given(dz, "dz", (M, w13.rows), torch.float16, x, stream)
+    ws = _lora_ws(ws, _swiglu_grad_ws(M, w13.rows, w13.k), x.device, stream)
+    dev = _current_device(x)
+    status = lib().nvfp4_linear_swiglu_grad(
+        _ptr(x, "x", torch.float16, dev), _ptr(dh, "dh", torch.float16, dev), M, _frozen(w13, dev), layout,
+        _ptr(dz, "dz", torch.float16, dev), _ptr(ws, "ws", ws.dtype, dev), ws.nbytes, _raw_stream(stream, dev))
+    if status != NVFP4_OK:
+        _check("nvfp4_linear_swiglu_grad", status)
+    return dz

@@ -189,6 +189,8 @@ int run_reduce(const PlanView &pv, int32_t M, int32_t topk, int32_t K, const flo
 int run_linear_f32(const uint16_t *x, int32_t M, const nvfp4_weights &w, float *y, hipStream_t s);
 // Split-K forms with a workspace of linear_ws_bytes(M, w.rows, w.k) bytes (16-byte aligned).
 size_t linear_ws_bytes(int32_t M, int32_t N, int32_t K);
+// The chunk products alone: FP32 [num_chunks(k)][M][rows] into `part` (the first launch of the split-K forms).
+int run_linear_partials(const uint16_t *x, int32_t M, const nvfp4_weights &w, float *part, hipStream_t s);
 int run_linear_split(const uint16_t *x, int32_t M, const nvfp4_weights &w, uint16_t *y, void *ws, hipStream_t s);
 int run_linear_swiglu_split(const uint16_t *x, int32_t M, const nvfp4_weights &w, int32_t layout, uint16_t *h,
                             void *ws, hipStream_t s);

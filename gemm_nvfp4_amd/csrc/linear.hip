@@ -547,6 +547,11 @@ int launch_fold(const float *part, int32_t M, const nvfp4_weights &w, int layout
 }
 }  // namespace
 
+int run_linear_partials(const uint16_t *x, int32_t M, const nvfp4_weights &w, float *part, hipStream_t s)
+{
+    return launch_split(x, M, w, part, s);
+}
+
 // The split form pays once the copy of x that every one-launch block reads (M * K * 2 bytes) is
 // large: past 8 rows and 96 KiB. Measured on MI355X, 4352x5120: 7.3 vs 8.6 us at one row, 8.2 vs
 // 9.2 at eight (one-launch faster), 9.3 vs 10.7 at twelve, 12.1 vs 16.1 at 32; the 5120x2176 down

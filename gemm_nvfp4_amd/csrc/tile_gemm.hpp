@@ -1,0 +1,222 @@
+// tile_gemm.hpp -- C = A B^T over two row-major operands of one type (fp16, or E4M3 bytes), both contiguous along the
+// reduction axis: the tiled product behind the gradients through decoded weights (linear_grad.hip) and the
+// projection of 8-bit rows (linear_rows.hip).
+//
+// A block of WM x WN waves owns BM x BN outputs; a wave MT x NT tiles of 16 x 16. The reduction axis is walked in
+// stages of 128 bytes (64 fp16 or 128 E4M3 elements): both operands' rows come into LDS by direct-to-LDS loads,
+// one 1 KB instruction for eight rows, NS - 1 stages ahead, with one block barrier per stage.
+//
+// LDS: a row is 128 bytes, its eight 16-byte units XOR-ed with 2 * ((row / 4) % 4). A fragment read takes unit
+// (q or q + 4) of rows 0..15 in lane group q; a half-wave of a 16-byte read is conflict-free where its 32 units
+// fall on 32 slots modulo 512 bytes (four rows): rows r, r + 4, r + 8, r + 12 of the two lane groups then land on
+// the eight different units of their slot. A direct-to-LDS load writes 16 bytes a lane in lane order, so the swizzle
+// stands in the lane's global address instead; it stays within the row's 128 bytes.
+//
+// The weight rows feed MFMA's first operand and the batch's rows the second, so a lane's four results of a tile are
+// four neighbouring columns of one row. Weight row 16 t + 4 q + j of a wave's tiles holds column 4 NT q + 4 t + j:
+// over its NT tiles a lane then has 4 NT neighbouring columns, which it stores without a transposition.
+//
+// fp16: two v_mfma_f32_16x16x32_f16 per stage and tile; E4M3: one v_mfma_f32_16x16x128_f8f6f4, the form that runs at
+// twice the fp16 rate. The element order inside a stage is the same in both operands, and any such order is as
+// good as another.
+#pragma once
+
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int STAGE_BYTES = 128;
+
+__host__ __device__ constexpr int unit_swizzle(int row) { return 2 * ((row >> 2) & 3); }
+
+// One 16 x 16 x 128 product of E4M3 operands; the exponent scales are 1 (E8M0 127).
+__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+}
+
+// Waits until at most N of this wave's vector memory operations are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    static_assert(N < 64, "vmcnt has six bits");
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// 16 bytes a lane from a buffer to LDS: lane i's bytes land at `to` + 16 i. Offsets past the buffer give zeros.
+__device__ __forceinline__ void load_to_lds(rsrc_t from, unsigned char *to, uint32_t voff, uint32_t soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, voff, soff, 0, 0);
+}
+
+template <bool FP8_, int MT_, int NT_, int WM_, int WN_, int NS_>
+struct Tile {
+    static constexpr bool FP8 = FP8_;
+    static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, NS = NS_;
+    static constexpr int WAVES = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
+    static constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES;  // loads per wave and stage
+    static constexpr int BYTES = (BM + BN) * STAGE_BYTES;           // one stage
+    static_assert(LA * 8 * WAVES == BM && LB * 8 * WAVES == BN, "whole loads per wave");
+    static_assert(NS * BYTES <= 160 * 1024, "LDS of a CU");
+};
+
+// This wave's and lane's place in a block.
+struct Place {
+    int wave, lane, wm, wn, r, q;
+};
+template <class T>
+__device__ __forceinline__ Place place_of()
+{
+    Place p;
+    p.lane = threadIdx.x & 63;
+    p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    p.wm = p.wave / T::WN, p.wn = p.wave % T::WN;
+    p.r = p.lane & 15, p.q = p.lane >> 4;
+    return p;
+}
+
+// The row of a tile that load i of this wave brings for this lane, and the lane's byte within the row.
+template <class T>
+__device__ __forceinline__ int load_row(const Place &p, int i)
+{
+    return (p.wave + T::WAVES * i) * 8 + (p.lane >> 3);
+}
+__device__ __forceinline__ uint32_t load_byte(int row, int lane) { return 16u * ((lane & 7) ^ unit_swizzle(row)); }
+
+// The column (of the block's BN) that row `row` of the staged weight tile holds.
+template <class T>
+__device__ __forceinline__ int column_of_row(int row)
+{
+    const int w = row / (16 * T::NT), t = (row / 16) % T::NT, q = (row / 4) & 3, j = row & 3;
+    return w * 16 * T::NT + 4 * T::NT * q + 4 * t + j;
+}
+
+// Both operands' buffers, from the block's first row on.
+struct Operands {
+    rsrc_t a, b;
+};
+
+// acc += A B^T over stages [first, last). va, vb: each load's byte offset at stage 0 (BUF_OOB or above: zeros).
+// tail: elements' bytes of the last stage that exist (128: all); later units of A are fed as zeros (B's must exist and
+// be finite, or be zeros too). FLUSH: stages per chunk (0: one chain); chunk sums are added in order, the chunks
+// counted from stage 0, so `first` must be a multiple of FLUSH.
+template <class T, int FLUSH>
+__device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p, const Operands &in,
+                                             const uint32_t (&va)[T::LA], const uint32_t (&vb)[T::LB], int first, int last,
+                                             int tail, f32x4 (&out)[T::MT][T::NT])
+{
+    constexpr int MT = T::MT, NT = T::NT, NS = T::NS;
+    auto issue = [&](int k, int buf, bool cut) {
+        unsigned char *s = smem + buf * T::BYTES;
+        const uint32_t so = (uint32_t)k * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < T::LA; ++i) {
+            uint32_t v = va[i];
+            if (cut) v = (int)load_byte(load_row<T>(p, i), p.lane) < tail ? v : BUF_OOB;
+            load_to_lds(in.a, s + (p.wave + T::WAVES * i) * 1024, v, so);
+        }
+        s += T::BM * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < T::LB; ++i) load_to_lds(in.b, s + (p.wave + T::WAVES * i) * 1024, vb[i], so);
+    };
+    auto load = [&](int k, int buf) {
+        if (tail < STAGE_BYTES && k == last - 1) issue(k, buf, true);
+        else issue(k, buf, false);
+    };
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (FLUSH) out[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    // Byte offset of this lane's first unit in the first row tile of A and of B; the second unit is 64 bytes on, XOR-ed.
+    const int sw = unit_swizzle(p.r);
+    const int u0 = 16 * (p.q ^ sw), u1 = 16 * ((p.q + 4) ^ sw);
+    const int a0 = (p.wm * MT * 16 + p.r) * STAGE_BYTES, b0 = (T::BM + p.wn * NT * 16 + p.r) * STAGE_BYTES;
+    auto unit = [&](int buf, int row0, int tile, int u) {
+        return *reinterpret_cast<const f16x8 *>(smem + buf * T::BYTES + row0 + tile * 16 * STAGE_BYTES + u);
+    };
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+        if (first + s < last) load(first + s, s);
+    int buf = 0, chunk = 0;
+    for (int k = first; k < last; ++k) {
+        // stage k has landed: at most the NS - 2 stages behind it are still in flight
+        if (NS > 2 && k + NS - 2 < last) wait_loads<(NS - 2) * (T::LA + T::LB)>();
+        else wait_loads<0>();
+        lds_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
+        const int into = buf == 0 ? NS - 1 : buf - 1;
+        if (k + NS - 1 < last) load(k + NS - 1, into);
+        if constexpr (T::FP8) {
+            auto frag = [&](int row0, int tile) {
+                return __builtin_shufflevector(__builtin_bit_cast(i32x4, unit(buf, row0, tile, u0)),
+                                               __builtin_bit_cast(i32x4, unit(buf, row0, tile, u1)), 0, 1, 2, 3, 4, 5, 6, 7);
+            };
+            i32x8 bf[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) bf[t] = frag(b0, t);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const i32x8 af = frag(a0, m);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_e4m3(bf[t], af, acc[m][t]);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f16x8 bf[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bf[t] = unit(buf, b0, t, h ? u1 : u0);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const f16x8 af = unit(buf, a0, m, h ? u1 : u0);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[m][t] = mfma_step(bf[t], af, acc[m][t]);
+                }
+            }
+        }
+        if (FLUSH && (++chunk == FLUSH || k + 1 == last)) {
+            chunk = 0;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    out[m][t] += acc[m][t];
+                    acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+        }
+        buf = buf == NS - 1 ? 0 : buf + 1;
+    }
+    if (!FLUSH) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) out[m][t] = acc[m][t];
+    }
+}
+
+// Tile (m, n) of block `b` of `mt` x `nt` tiles. The hardware deals block ids to the 8 XCDs in turn: consecutive tiles
+// are given to one XCD, in groups of four tile rows, so that the blocks that run at once on an XCD share their operands'
+// rows in its L2. False for the padding ids of the last XCD.
+__device__ __forceinline__ bool tile_of_block(int b, int mt, int nt, int &m, int &n)
+{
+    const int tiles = mt * nt, per = (tiles + 7) >> 3;
+    const int i = (b & 7) * per + (b >> 3);
+    if (i >= tiles) return false;
+    constexpr int GROUP = 4;
+    const int g = i / (GROUP * nt), in = i - g * GROUP * nt;
+    const int rows = min(GROUP, mt - g * GROUP);
+    m = g * GROUP + in % rows;
+    n = in / rows;
+    return true;
+}
+inline unsigned tile_grid(int64_t tiles) { return (unsigned)(8 * ((tiles + 7) / 8)); }
+
+}  // namespace nvfp4
