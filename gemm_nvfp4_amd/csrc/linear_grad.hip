@@ -63,9 +63,9 @@ __device__ __forceinline__ void decode_columns(f16x8 (&b)[8], const uint32_t (&c
     }
 }
 
-// Block (column group g, chunk c): plane c, columns 128 g .. + 127, of all M <= 16 MT rows. Lane (r, q) of a wave
-// holds columns 128 g + 8 r .. + 7 and, per 32-row step, weight rows 8 q .. + 7. Weight rows at or past N read as
-// zeros (codes and scales), so do dy's elements there and its rows at or past M.
+// Block (column group g, chunk c): plane c, columns 128 g .. + 127, of all M <= 16 MT rows. Lane (r, q) of a wave holds
+// columns 128 g + 8 r .. + 7 and, per 32-row step, weight rows 8 q .. + 7. Weight rows at or past N read as zeros (codes
+// and scales), so do dy's elements there and its rows at or past M.
 template <int MT>
 __global__ __launch_bounds__(ST_WAVES * 64) void grad_stream_kernel(const f16 *__restrict__ dy, int M,
                                                                     const uint8_t *__restrict__ codes,
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__r
     const int first = min(stages, (int)blockIdx.y * per), last = min(stages, first + per);
     const int tail = last == stages && red % 64 ? red % 64 * 2 : STAGE_BYTES;
     f32x4 acc[T::MT][T::NT];
-    tile_product<T, 0>(smem, p, in, va, vb, first, last, tail, acc);
+    tile_product<T>(smem, p, in, va, vb, first, last, tail, acc);
     const float gs = PLANE ? 1.0f : gscale[0];
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
         vb[i] = i0 + pair < I ? (uint32_t)pair * step + load_byte(r, p.lane) : BUF_OOB;
     }
     f32x4 acc[T::MT][T::NT];
-    tile_product<T, 0>(smem, p, in, va, vb, 0, K / 64, STAGE_BYTES, acc);
+    tile_product<T>(smem, p, in, va, vb, 0, K / 64, STAGE_BYTES, acc);
     const float gs = gscale[0];
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
@@ -347,36 +347,87 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
 }
 
 // ---- host --------------------------------------------------------------------------------------------
-using Large = Tile<false, 8, 4, 2, 4, 2>;  // 256 x 256
-using Small = Tile<false, 4, 4, 2, 2, 2>;  // 128 x 128, two blocks per CU
+// The tile shapes. `per_cu`: blocks of a shape that a CU holds; `ns`: what a 64-element stage takes with every CU full,
+// measured at 4096 rows of 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds of tiles). Rounds decide:
+// 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of 256 x 256 (272 tiles on 256 CUs), 200
+// in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 126 with 320 x 128, 143 with 128 x 128.
+using T384x192 = Tile<false, 6, 6, 4, 2, 2>;
+using T256x256 = Tile<false, 8, 4, 2, 4, 2>;
+using T192x256 = Tile<false, 6, 4, 2, 4, 2>;
+using T192x192 = Tile<false, 3, 6, 4, 2, 2>;
+using T320x128 = Tile<false, 5, 4, 4, 2, 2>;
+using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
+using T64x128 = Tile<false, 2, 4, 2, 2, 3>;
+using T64x64 = Tile<false, 2, 2, 2, 2, 4>;
+struct Shape {
+    int bm, bn, per_cu, ns;
+};
+constexpr Shape SHAPES[] = {{384, 192, 1, 1940}, {256, 256, 1, 1510}, {192, 256, 1, 1320}, {192, 192, 1, 1170},
+                            {320, 128, 1, 1390}, {128, 128, 2, 870},  {64, 128, 2, 700},   {64, 64, 2, 540}};
 
 struct Choice {
-    bool large;
-    int splits;
+    int shape, splits;
+    int64_t ns;
 };
 
-// The large tile where it gives every CU one at least; else the small one, the reduction axis split until the CUs
-// hold about two blocks each, in runs of at least eight stages.
+// The shape, and the number of runs that the reduction axis is cut into, with the least estimated time: rounds of
+// blocks over the CUs, and for more than one run the planes' way to memory and back and the fold's launch.
 Choice choose(int64_t M, int64_t cols, int64_t red)
 {
-    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((cols + bn - 1) / bn); };
-    if (tiles(Large::BM, Large::BN) >= CUS) return {true, 1};
-    const int64_t t = tiles(Small::BM, Small::BN), stages = (red + 63) / 64;
-    int64_t s = 2 * CUS / (t < 1 ? 1 : t);
-    if (s > stages / 8) s = stages / 8;
-    return {false, (int)(s < 1 ? 1 : s)};
+    const int64_t stages = (red + 63) / 64;
+    Choice best = {0, 1, INT64_MAX};
+    for (int i = 0; i < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++i) {
+        const Shape &h = SHAPES[i];
+        const int64_t tiles = ((M + h.bm - 1) / h.bm) * ((cols + h.bn - 1) / h.bn), slots = (int64_t)CUS * h.per_cu;
+        for (int s = 1; s <= 8 && s * 8 <= stages; ++s) {
+            const int64_t rounds = (tiles * s + slots - 1) / slots;
+            int64_t ns = rounds * ((stages + s - 1) / s) * (tiles * s <= CUS && h.per_cu > 1 ? h.ns * 4 / 5 : h.ns);
+            if (s > 1) ns += 4000 + M * cols * 8 * s / 2500;  // there and back, with the fold's launch
+            if (ns < best.ns) best = {i, s, ns};
+        }
+    }
+    return best;
+}
+
+template <class F>
+int with_shape(int i, F &&f)
+{
+    switch (i) {  // the order of SHAPES
+    case 0: return f(T384x192{});
+    case 1: return f(T256x256{});
+    case 2: return f(T192x256{});
+    case 3: return f(T192x192{});
+    case 4: return f(T320x128{});
+    case 5: return f(T128x128{});
+    case 6: return f(T64x128{});
+    default: return f(T64x64{});
+    }
+}
+
+// Whether the gated gradient of M rows takes the packed weights (the chunk products of linear.hip in passes of 64 rows,
+// and their fold) or decodes them first. Estimates in ns fitted to measurements, 4352 x 5120: 15 us at 64 rows by the
+// packed ones and 32 decoded, 22 and 41 at 128, 35 and 49 at 256, 48 and 52 at 333, 71 and 60 at 512; 2048 x 2048: 12 and
+// 14 at 64 rows, 17 and 15 at 128, 26 and 17 at 256.
+bool swiglu_packed(int64_t M, int64_t rows, int64_t K)
+{
+    if (M <= ST_MAX_M) return true;
+    const int64_t passes = (M + 63) / 64, elements = rows * K;
+    const int64_t packed = 6000 + elements / 5000 + passes * (4000 + num_chunks((int)K) * rows * 64 * 8 / 8500);
+    return packed < choose(M, rows, K).ns + 2000 + elements * 53 / 100000;
 }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 int padded(int n) { return (n + 63) & ~63; }
 
-template <class T>
-int launch_plain(const f16 *a, int M, int red, const f16 *b, int ld, int cols, const float *gscale, void *out, int splits,
-                 bool plane, hipStream_t s)
+int launch_plain(const Choice &c, const f16 *a, int M, int red, const f16 *b, int ld, int cols, const float *gscale, void *out,
+                 hipStream_t s)
 {
-    const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((cols + T::BN - 1) / T::BN);
-    return launch(plane ? grad_tile_kernel<T, true> : grad_tile_kernel<T, false>, dim3(tile_grid(tiles), (unsigned)splits),
-                  dim3(T::WAVES * 64), 0, s, a, M, red, b, ld, cols, gscale, out);
+    return with_shape(c.shape, [&](auto tile) {
+        using T = decltype(tile);
+        const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((cols + T::BN - 1) / T::BN);
+        return launch(c.splits > 1 ? grad_tile_kernel<T, true> : grad_tile_kernel<T, false>,
+                      dim3(tile_grid(tiles), (unsigned)c.splits), dim3(T::WAVES * 64), 0, s, a, M, red, b, ld, cols, gscale, out);
+    });
 }
 
 int launch_swiglu_fold(const float *part, int S, int M, int I, const nvfp4_weights &w, int layout, const f16 *dh, f16 *dz,
@@ -423,16 +474,15 @@ int run_linear_grad(const uint16_t *dy, int32_t M, const nvfp4_weights &w, uint1
                     K, ld, wt);
     if (st != NVFP4_OK) return st;
     const Choice c = choose(M, K, N);
-    if (c.large) return launch_plain<Large>(d, M, N, wt, ld, K, w.global_scale, o, 1, false, s);
-    if (c.splits == 1) return launch_plain<Small>(d, M, N, wt, ld, K, w.global_scale, o, 1, false, s);
+    if (c.splits == 1) return launch_plain(c, d, M, N, wt, ld, K, w.global_scale, o, s);
     float *part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + up256((size_t)K * ld * 2));
-    st = launch_plain<Small>(d, M, N, wt, ld, K, w.global_scale, part, c.splits, true, s);
+    st = launch_plain(c, d, M, N, wt, ld, K, w.global_scale, part, s);
     return st != NVFP4_OK ? st : fold(part, c.splits);
 }
 
 size_t linear_swiglu_grad_ws_bytes(int32_t M, int32_t rows, int32_t K)
 {
-    if (M <= ST_MAX_M) return up256(linear_ws_bytes(M, rows, K));
+    if (swiglu_packed(M, rows, K)) return up256(linear_ws_bytes(M, rows, K));
     const Choice c = choose(M, rows, K);
     const size_t planes = c.splits > 1 ? (size_t)c.splits * M * rows * sizeof(float) : 0;
     return up256((size_t)rows * K * 2) + up256(planes);
@@ -444,7 +494,7 @@ int run_linear_swiglu_grad(const uint16_t *x, const uint16_t *dh, int32_t M, con
     const int K = w.k, I = w.rows / 2;
     const f16 *xf = reinterpret_cast<const f16 *>(x), *df = reinterpret_cast<const f16 *>(dh);
     f16 *o = reinterpret_cast<f16 *>(dz);
-    if (M <= ST_MAX_M) {
+    if (swiglu_packed(M, w.rows, K)) {
         float *part = static_cast<float *>(ws);
         const int st = run_linear_partials(x, M, w, part, s);
         return st != NVFP4_OK ? st : launch_swiglu_fold(part, num_chunks(K), M, I, w, layout, df, o, s);
@@ -454,16 +504,15 @@ int run_linear_swiglu_grad(const uint16_t *x, const uint16_t *dh, int32_t M, con
     int st = launch(decode_kernel, dim3((unsigned)((eights + 255) / 256)), dim3(256), 0, s, w.codes, w.scales, eights, wd);
     if (st != NVFP4_OK) return st;
     const Choice c = choose(M, w.rows, K);
-    auto whole = [&](auto tile) {
-        using T = decltype(tile);
-        const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((I + T::BN / 2 - 1) / (T::BN / 2));
-        return launch(swiglu_grad_tile_kernel<T>, dim3(tile_grid(tiles)), dim3(T::WAVES * 64), 0, s, xf, M, K, wd, I, layout,
-                      w.global_scale, df, o);
-    };
-    if (c.large) return whole(Large{});
-    if (c.splits == 1) return whole(Small{});
+    if (c.splits == 1)
+        return with_shape(c.shape, [&](auto tile) {
+            using T = decltype(tile);
+            const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((I + T::BN / 2 - 1) / (T::BN / 2));
+            return launch(swiglu_grad_tile_kernel<T>, dim3(tile_grid(tiles)), dim3(T::WAVES * 64), 0, s, xf, M, K, wd, I, layout,
+                          w.global_scale, df, o);
+        });
     float *part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + up256((size_t)w.rows * K * 2));
-    st = launch_plain<Small>(xf, M, K, wd, K, w.rows, w.global_scale, part, c.splits, true, s);
+    st = launch_plain(c, xf, M, K, wd, K, w.rows, w.global_scale, part, s);
     return st != NVFP4_OK ? st : launch_swiglu_fold(part, c.splits, M, I, w, layout, df, o, s);
 }
 

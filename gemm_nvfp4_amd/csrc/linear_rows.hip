@@ -1,10 +1,9 @@
 // linear_rows.hip -- the channel-FP8 projection of 8-bit rows (include/nvfp4moe_dense.h): both operands E4M3, FP32
 // sums, a scale per row and one per column.
 //
-// One reduction order at every batch size: 512-element chunks, each a chain of four 128-element MFMA steps from +0,
-// added in chunk order from +0. Few rows stream the weights once: a block per 16 columns whose waves share the chunks
-// (all of a wave's weights are requested before the first product) and meet in LDS. More rows take the tiled product of
-// tile_gemm.hpp, which adds its accumulators to the sum after every fourth stage.
+// One reduction order at every batch size: a single chain of 128-element MFMA steps from +0, in the order of the
+// reduction axis. Few rows stream the weights once: a block for every 16 columns, whose waves hold the whole axis in
+// flight and hand the chain on from one to the next. More rows take the tiled product of tile_gemm.hpp, whose shape the batch chooses.
 #include "dense.hpp"
 #include "nvfp4_device.hpp"
 #include "tile_gemm.hpp"
@@ -12,67 +11,83 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int ROWS_CHUNK = 512, ROWS_STEPS = ROWS_CHUNK / STAGE_BYTES;
-constexpr int ROWS_WAVES = 16;
-constexpr int ROWS_STREAM_M = 32;
-constexpr int LDS_PITCH = 20;  // floats between a partial tile's rows
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-inline int rows_chunks(int K) { return (K + ROWS_CHUNK - 1) / ROWS_CHUNK; }
+constexpr int ROWS_STREAM_M = 64;
+constexpr int ROWS_GROUP = 5;  // steps whose operands a wave holds at once
 
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b)
 {
     return __builtin_shufflevector(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Block b: columns 16 b .. + 15 of all M <= 16 MT rows. LDS: [chunks][MT][16 rows][LDS_PITCH] partial tiles.
+// Block b: columns 16 b .. + 15 of all M <= 16 MT rows. The waves share the steps in groups of ROWS_GROUP, in turn. All
+// of a group's loads are in flight before the wave's turn comes, so the block has the whole reduction axis in flight
+// (up to ROWS_GROUP steps a wave) and yet computes one chain: a wave takes the accumulators over from the one before,
+// through LDS, and asks for its next group as soon as it has passed them on.
 template <int MT>
-__global__ __launch_bounds__(ROWS_WAVES * 64) void rows_stream_kernel(const uint8_t *__restrict__ xq,
-                                                                      const float *__restrict__ xs, int M,
-                                                                      const uint8_t *__restrict__ w,
-                                                                      const float *__restrict__ cs, int N, int K,
-                                                                      f16 *__restrict__ y)
+__global__ __launch_bounds__(MT == 1 ? 1024 : 512) void rows_stream_kernel(const uint8_t *__restrict__ xq,
+                                                                           const float *__restrict__ xs, int M,
+                                                                           const uint8_t *__restrict__ w,
+                                                                           const float *__restrict__ cs, int N, int K,
+                                                                           f16 *__restrict__ y)
 {
-    extern __shared__ __attribute__((aligned(16))) float part[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 16, S = (K + ROWS_CHUNK - 1) / ROWS_CHUNK;
+    constexpr int G = ROWS_GROUP;
+    __shared__ f32x4 handed[MT][64];
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int n0 = blockIdx.x * 16, S = K / STAGE_BYTES;
     const rsrc_t rw = make_rsrc(w + (size_t)n0 * K, 16u * K);
     const rsrc_t rx = make_rsrc(xq, (uint32_t)M * K);
-    for (int c = wave; c < S; c += waves) {
-        const int kb = c * ROWS_CHUNK, steps = min(ROWS_STEPS, (K - kb) / STAGE_BYTES);
-        u32x4 b[ROWS_STEPS][2], a[MT][ROWS_STEPS][2];
+    const uint32_t wo = (uint32_t)r * K + 16 * q;
+    uint32_t xo[MT];
 #pragma unroll
-        for (int s = 0; s < ROWS_STEPS; ++s)
+    for (int m = 0; m < MT; ++m) xo[m] = 16 * m + r < M ? (uint32_t)(16 * m + r) * K + 16 * q : BUF_OOB;
+    u32x4 b[G][2], a[MT][G][2];
+    auto load = [&](int s0) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                b[s][u] = bload16(rw, s < steps ? (uint32_t)r * K + kb + s * STAGE_BYTES + 64 * u + 16 * q : BUF_OOB, 0);
+        for (int s = 0; s < G; ++s)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int u = 0; u < 2; ++u) {
+                // steps past the end re-read the last one; they are not used
+                const uint32_t at = (uint32_t)min(s0 + s, S - 1) * STAGE_BYTES + 64 * u;
+                b[s][u] = bload16(rw, wo, at);
 #pragma unroll
-            for (int s = 0; s < ROWS_STEPS; ++s)
+                for (int m = 0; m < MT; ++m) a[m][s][u] = bload16(rx, xo[m], at);
+            }
+    };
+    load(wave * G);
+    for (int g0 = 0; g0 * G < S; g0 += waves) {
+        for (int turn = 0; turn < waves; ++turn) {
+            const int s0 = (g0 + turn) * G;
+            if (turn == wave && s0 < S) {
+                f32x4 acc[MT];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    a[m][s][u] = bload16(rx, s < steps && 16 * m + r < M
-                                                 ? (uint32_t)(16 * m + r) * K + kb + s * STAGE_BYTES + 64 * u + 16 * q
-                                                 : BUF_OOB, 0);
+                for (int m = 0; m < MT; ++m) acc[m] = s0 == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : handed[m][lane];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < G; ++s)
+                    if (s0 + s < S) {
 #pragma unroll
-            for (int s = 0; s < ROWS_STEPS; ++s)
-                if (s < steps) acc = mfma_e4m3(join(b[s][0], b[s][1]), join(a[m][s][0], a[m][s][1]), acc);
-            // lane (r, q): columns 4 q .. 4 q + 3 of row r
-            *reinterpret_cast<f32x4 *>(part + ((c * MT + m) * 16 + r) * LDS_PITCH + 4 * q) = acc;
+                        for (int m = 0; m < MT; ++m)
+                            acc[m] = mfma_e4m3(join(b[s][0], b[s][1]), join(a[m][s][0], a[m][s][1]), acc[m]);
+                    }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) handed[m][lane] = acc[m];
+                if (s0 + waves * G < S) load(s0 + waves * G);
+            }
+            lds_barrier();
         }
     }
-    lds_barrier();
-    for (int i = threadIdx.x; i < MT * 256; i += blockDim.x) {
-        const int m = i >> 4, n = i & 15;
-        if (m >= M) break;
-        float s = 0.0f;
-        for (int c = 0; c < S; ++c) s += part[((size_t)c * MT * 16 + m) * LDS_PITCH + n];
-        y[(size_t)m * N + n0 + n] = f16_of_f32((xs[m] * cs[n0 + n]) * s);
+    // lane (r, q) of row tile m: columns 4 q .. 4 q + 3 of row r; a wave a row tile
+    for (int m = wave; m < MT; m += waves) {
+        const int row = 16 * m + r;
+        if (row >= M) continue;
+        const f32x4 acc = handed[m][lane];
+        const float sx = xs[row];
+        f16x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = f16_of_f32((sx * cs[n0 + 4 * q + e]) * acc[e]);
+        *reinterpret_cast<f16x4 *>(y + (size_t)row * N + n0 + 4 * q) = o;
     }
 }
 
@@ -102,8 +117,7 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
         vb[i] = c0 + c < N ? (uint32_t)c * K + load_byte(r, p.lane) : BUF_OOB;
     }
     f32x4 acc[T::MT][T::NT];
-    tile_product<T, ROWS_STEPS>(smem, p, in, va, vb, 0, K / STAGE_BYTES, STAGE_BYTES, acc);
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    tile_product<T>(smem, p, in, va, vb, 0, K / STAGE_BYTES, STAGE_BYTES, acc);
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
         const int row = m0 + (p.wm * T::MT + m) * 16 + p.r;
@@ -121,9 +135,16 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
     }
 }
 
-using Large = Tile<true, 6, 4, 2, 4, 2>;   // 192 x 256
-using Medium = Tile<true, 4, 4, 2, 2, 2>;  // 128 x 128, two blocks per CU
-using Small = Tile<true, 2, 2, 2, 2, 3>;   // 64 x 64, three blocks per CU
+// Tile shapes, and what a stage of every CU at work on one (two of the small ones) takes, in ns: measured on 256 (512)
+// tiles at 40 stages. What bounds them is the way from the L2s to LDS (12 to 15 TB/s over the chip: 64 KB a stage for
+// 256 x 256), with the matrix pipes about half busy.
+using T384x192 = Tile<true, 6, 6, 4, 2, 2>;
+using T256x256 = Tile<true, 8, 4, 2, 4, 2>;
+using T192x256 = Tile<true, 6, 4, 2, 4, 2>;
+using T192x192 = Tile<true, 6, 3, 2, 4, 2>;
+using T128x128 = Tile<true, 4, 4, 2, 2, 2>;
+using T64x128 = Tile<true, 2, 4, 2, 2, 3>;
+using T64x64 = Tile<true, 2, 2, 2, 2, 4>;
 
 }  // namespace
 
@@ -133,20 +154,44 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
     const int N = w.rows, K = w.k;
     f16 *o = reinterpret_cast<f16 *>(y);
     if (M <= ROWS_STREAM_M) {
-        const int S = rows_chunks(K), waves = S < ROWS_WAVES ? S : ROWS_WAVES, mt = (M + 15) / 16;
-        const size_t shmem = (size_t)S * mt * 16 * LDS_PITCH * sizeof(float);
-        return launch(mt == 1 ? rows_stream_kernel<1> : rows_stream_kernel<2>, dim3((unsigned)(N / 16)),
-                      dim3((unsigned)(waves * 64)), shmem, s, xq, xs, M, w.codes, w.channel_scale, N, K, o);
+        const int groups = (K / STAGE_BYTES + ROWS_GROUP - 1) / ROWS_GROUP, most = M <= 16 ? 16 : 8;
+        const int mt = (M + 15) / 16;
+        auto *kernel = mt == 1 ? rows_stream_kernel<1> : mt == 2 ? rows_stream_kernel<2> : mt == 3 ? rows_stream_kernel<3>
+                                                                                                  : rows_stream_kernel<4>;
+        return launch(kernel, dim3((unsigned)(N / 16)), dim3((unsigned)(64 * (groups < most ? groups : most))), 0, s, xq, xs, M,
+                      w.codes, w.channel_scale, N, K, o);
     }
+    int result = NVFP4_ERR_LAUNCH;
+    int64_t least = INT64_MAX;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    // The shape whose rounds of tiles over the CUs take the least time.
+    int best = 0;
+    auto consider = [&](int i, int64_t bm, int64_t bn, int per_cu, int ns) {
+        const int64_t cost = (tiles(bm, bn) + 256 * per_cu - 1) / (256 * per_cu) * ns;
+        if (cost < least) least = cost, best = i;
+    };
+    consider(0, 384, 192, 1, 1950);
+    consider(1, 256, 256, 1, 1620);
+    consider(2, 192, 256, 1, 1300);
+    consider(3, 192, 192, 1, 1070);
+    consider(4, 128, 128, 2, 1000);
+    consider(5, 64, 128, 2, 760);
+    consider(6, 64, 64, 2, 580);
     auto tiled = [&](auto tile) {
         using T = decltype(tile);
-        return launch(rows_tile_kernel<T>, dim3(tile_grid(tiles(T::BM, T::BN))), dim3(T::WAVES * 64), 0, s, xq, xs, M, w.codes,
-                      w.channel_scale, N, K, o);
+        result = launch(rows_tile_kernel<T>, dim3(tile_grid(tiles(T::BM, T::BN))), dim3(T::WAVES * 64), 0, s, xq, xs, M, w.codes,
+                        w.channel_scale, N, K, o);
     };
-    if (tiles(Large::BM, Large::BN) >= 256) return tiled(Large{});
-    if (tiles(Medium::BM, Medium::BN) >= 256) return tiled(Medium{});
-    return tiled(Small{});
+    switch (best) {
+    case 0: tiled(T384x192{}); break;
+    case 1: tiled(T256x256{}); break;
+    case 2: tiled(T192x256{}); break;
+    case 3: tiled(T192x192{}); break;
+    case 4: tiled(T128x128{}); break;
+    case 5: tiled(T64x128{}); break;
+    default: tiled(T64x64{}); break;
+    }
+    return result;
 }
 
 }  // namespace nvfp4

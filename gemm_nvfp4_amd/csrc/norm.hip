@@ -20,18 +20,18 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;  // the same bits in every lane: each step adds the same pair in both of its lanes
 }
 
-// Sums of NS values over the T threads of a row. T = 64: within the wave. Else over the block's waves, in
-// order; `red` holds NS * T / 64 floats and is not reused before the next barrier pair.
+// Sums of NS values over the T threads of a row, of which this is number j. T = 64: within the wave. Else over the row's
+// waves, in order; `red` holds NS * T / 64 floats and is not written again before another barrier.
 template <int T, int NS>
-__device__ __forceinline__ void row_sums(float (&v)[NS], float *red)
+__device__ __forceinline__ void row_sums(float (&v)[NS], float *red, int j)
 {
 #pragma unroll
     for (int i = 0; i < NS; ++i) v[i] = wave_sum(v[i]);
     if constexpr (T > 64) {
         constexpr int W = T / 64;
-        if ((threadIdx.x & 63) == 0) {
+        if ((j & 63) == 0) {
 #pragma unroll
-            for (int i = 0; i < NS; ++i) red[i * W + (threadIdx.x >> 6)] = v[i];
+            for (int i = 0; i < NS; ++i) red[i * W + (j >> 6)] = v[i];
         }
         lds_barrier();
 #pragma unroll
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_kernel(
             sum[0] = fmaf(t[v][e], t[v][e], sum[0]);
         }
     }
-    row_sums<T, 1>(sum, red);
+    row_sums<T, 1>(sum, red, j);
     const float rstd = 1.0f / sqrtf(sum[0] / (float)K + eps);
     uint32_t top = 0;
 #pragma unroll
@@ -140,12 +140,14 @@ __global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_kernel(
 }
 
 // ---- gradient --------------------------------------------------------------------------------------
-// Groups of T threads walk the rows in steps of the number of groups; each thread keeps its columns' share of
-// dweight in registers. A block's groups meet in LDS in order, and the blocks' sums [G][K] are added by a
-// second launch. G depends on M alone.
-constexpr int GRAD_BLOCKS = 512;
+// Groups of T threads walk the rows in steps of the number of groups; each thread sums its columns' share of dweight,
+// in registers, or in LDS where 1024 threads leave no registers for it. A block's groups meet in LDS in order, and
+// the blocks' sums [G][K] are added by a second launch: G, at most one block per CU, decides how much that moves (333
+// rows of 5120 took 11.5 us with a block a row and 7 MB of sums). The next row's loads are in flight while a row's sums
+// are taken. G depends on M and K alone.
+constexpr int GRAD_BLOCKS = 256;
 
-inline int grad_groups(int T) { return T == 64 ? WAVE_ROWS : 1; }
+constexpr int grad_groups(int T) { return T == 64 ? 8 : T == 256 ? 2 : 1; }  // 512 threads but for the widest rows
 inline int grad_blocks(int M, int T)
 {
     const int g = grad_groups(T);
@@ -154,79 +156,114 @@ inline int grad_blocks(int M, int T)
 }
 
 template <int T, int V>
-__global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_grad_kernel(
-    const f16 *__restrict__ t, const f16 *dy, const f16 *ds, const f16 *__restrict__ w, int M, int K, float eps, f16 *dx,
-    float *__restrict__ part)
+__global__ __launch_bounds__(T * grad_groups(T)) void norm_grad_kernel(const f16 *__restrict__ t, const f16 *dy, const f16 *ds,
+                                                                       const f16 *__restrict__ w, int M, int K, float eps,
+                                                                       f16 *dx, float *__restrict__ part)
 {
-    constexpr int GROUPS = T == 64 ? WAVE_ROWS : 1;
-    __shared__ float red[2][2 * (T / 64)];
-    __shared__ float sums[T == 64 ? 64 * V * 8 : 1];
-    const int j = T == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int group = T == 64 ? threadIdx.x >> 6 : 0;
-    const int pieces = K >> 3;
-    float dw[V][8];
-    f16x8 g[V];
+    constexpr int GROUPS = grad_groups(T);
+    // 1024 threads have 128 registers each: no next row, dweight in LDS, weight and ds read where they are used.
+    constexpr bool IN_LDS = T == 1024, AHEAD = T < 1024;
+    __shared__ float red[2][GROUPS][2 * (T / 64)];
+    __shared__ __attribute__((aligned(16))) f32x4 sums[(IN_LDS || GROUPS > 1) ? 2 * V * T : 1];
+    const int j = threadIdx.x % T, group = threadIdx.x / T;
+    const int pieces = K >> 3, stride = gridDim.x * GROUPS;
+    f32x4 dw[V][2];
+    auto weight = [&](int p) { return w && p < pieces ? load8(w + 8 * p) : f16x8{1, 1, 1, 1, 1, 1, 1, 1}; };
+    f16x8 g[AHEAD ? V : 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int p = j + v * T;
-        g[v] = f16x8{1, 1, 1, 1, 1, 1, 1, 1};
-        if (w && p < pieces) g[v] = load8(w + 8 * p);
+        if (AHEAD) g[v] = weight(j + v * T);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            if (IN_LDS) sums[(v * 2 + h) * T + j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            else dw[v][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
     }
-    int turn = 0;
-    for (int row = blockIdx.x * GROUPS + group; row < M; row += gridDim.x * GROUPS, turn ^= 1) {
+    f16x8 a[V], d[V];
+    auto load = [&](int row) {
         const size_t base = (size_t)row * K;
-        f16x8 a[V], d[V], c[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int p = j + v * T;
-            a[v] = d[v] = c[v] = zero8();
-            if (p < pieces) {
+            a[v] = d[v] = zero8();
+            if (p < pieces && row < M) {
                 a[v] = load8(t + base + 8 * p);
                 d[v] = load8(dy + base + 8 * p);
-                if (ds) c[v] = load8(ds + base + 8 * p);
             }
+        }
+    };
+    const int row0 = blockIdx.x * GROUPS + group;
+    load(row0);
+    int turn = 0;
+    // Every group of a block makes the same number of turns, since they share the barriers; rows past the last are zeros.
+    for (int first = blockIdx.x * GROUPS; first < M; first += stride, turn ^= 1) {
+        const int row = first + group;
+        const size_t base = (size_t)row * K;
+        const bool in = row < M;
+        auto residual = [&](int p) { return ds && in && p < pieces ? load8(ds + base + 8 * p) : zero8(); };
+        f16x8 c[AHEAD ? V : 1];
+        if (AHEAD) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = residual(j + v * T);
         }
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            const f16x8 gv = AHEAD ? g[AHEAD ? v : 0] : weight(j + v * T);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float tv = (float)a[v][e];
                 sum[0] = fmaf(tv, tv, sum[0]);
-                sum[1] = fmaf((float)g[v][e] * (float)d[v][e], tv, sum[1]);
+                sum[1] = fmaf((float)gv[e] * (float)d[v][e], tv, sum[1]);
             }
         }
-        row_sums<T, 2>(sum, red[turn]);
+        f16x8 a0[V], d0[V];
+        if (AHEAD) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) a0[v] = a[v], d0[v] = d[v];
+            if (first + stride < M) load(row + stride);
+        }
+        row_sums<T, 2>(sum, red[turn][group], j);
         const float rstd = 1.0f / sqrtf(sum[0] / (float)K + eps);
         const float along = rstd * rstd * (sum[1] / (float)K);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int p = j + v * T;
+            const f16x8 &av = AHEAD ? a0[v] : a[v], &dv = AHEAD ? d0[v] : d[v];
+            const f16x8 gv = AHEAD ? g[AHEAD ? v : 0] : weight(p), cv = AHEAD ? c[AHEAD ? v : 0] : residual(p);
             f16x8 o;
+            f32x4 part_dw[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) part_dw[h] = IN_LDS ? sums[(v * 2 + h) * T + j] : dw[v][h];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float tv = (float)a[v][e], dv = (float)d[v][e];
-                dw[v][e] = fmaf(dv, tv * rstd, dw[v][e]);
-                const float dxv = rstd * ((float)g[v][e] * dv - tv * along);
-                o[e] = f16_of_f32(ds ? (float)c[v][e] + dxv : dxv);
+                const float tv = (float)av[e], dy1 = (float)dv[e];
+                // a row past the last has rstd = 1 / sqrt(eps), infinite for eps = 0: it must add nothing
+                part_dw[e >> 2][e & 3] = fmaf(dy1, in ? tv * rstd : 0.0f, part_dw[e >> 2][e & 3]);
+                const float dxv = rstd * ((float)gv[e] * dy1 - tv * along);
+                o[e] = f16_of_f32(ds ? (float)cv[e] + dxv : dxv);
             }
-            if (dx && p < pieces) *reinterpret_cast<f16x8 *>(dx + base + 8 * p) = o;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (IN_LDS) sums[(v * 2 + h) * T + j] = part_dw[h];
+                else dw[v][h] = part_dw[h];
+            }
+            if (dx && in && p < pieces) *reinterpret_cast<f16x8 *>(dx + base + 8 * p) = o;
         }
+        if (!AHEAD && first + stride < M) load(row + stride);
     }
     if (!part) return;  // uniform over the grid
     float *out = part + (size_t)blockIdx.x * K;
-    if constexpr (T == 64) {
+    if constexpr (GROUPS > 1) {
         for (int i = 0; i < GROUPS; ++i) {
             if (group == i) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float *c = &sums[(v * 8 + e) * 64 + j];
-                        *c = i == 0 ? dw[v][e] : *c + dw[v][e];
-                        dw[v][e] = *c;
+                    for (int h = 0; h < 2; ++h) {
+                        f32x4 &c = sums[(v * 2 + h) * T + j];
+                        dw[v][h] = i == 0 ? dw[v][h] : c + dw[v][h];
+                        c = dw[v][h];
                     }
             }
             lds_barrier();
@@ -237,8 +274,9 @@ __global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_grad_kernel
     for (int v = 0; v < V; ++v) {
         const int p = j + v * T;
         if (p < pieces) {
-            *reinterpret_cast<float4 *>(out + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-            *reinterpret_cast<float4 *>(out + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<f32x4 *>(out + 8 * p + 4 * h) = IN_LDS ? sums[(v * 2 + h) * T + j] : dw[v][h];
         }
     }
 }
@@ -316,7 +354,7 @@ int run_norm_grad(const uint16_t *t, const uint16_t *dy, const uint16_t *ds, con
     if (M > 0) {
         const int r = by_width(K, [&](auto T, auto V) {
             constexpr int tt = decltype(T)::value, v = decltype(V)::value;
-            return launch(norm_grad_kernel<tt, v>, dim3((unsigned)G), dim3((unsigned)(tt * (tt == 64 ? WAVE_ROWS : 1))), 0, st,
+            return launch(norm_grad_kernel<tt, v>, dim3((unsigned)G), dim3((unsigned)(tt * grad_groups(tt))), 0, st,
                           reinterpret_cast<const f16 *>(t), reinterpret_cast<const f16 *>(dy),
                           reinterpret_cast<const f16 *>(ds), reinterpret_cast<const f16 *>(w), M, K, eps,
                           reinterpret_cast<f16 *>(dx), part);

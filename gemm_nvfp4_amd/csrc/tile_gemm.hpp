@@ -30,12 +30,12 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int STAGE_BYTES = 128;
 
-__host__ __device__ constexpr int unit_swizzle(int row) { return 2 * ((row >> 2) & 3); }
+__host__ __device__ constexpr int unit_swizzle(int row) { return (row >> 1) & 7; }
 
 // One 16 x 16 x 128 product of E4M3 operands; the exponent scales are 1 (E8M0 127).
 __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c)
 {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 // Waits until at most N of this wave's vector memory operations are in flight.
@@ -101,14 +101,13 @@ struct Operands {
     rsrc_t a, b;
 };
 
-// acc += A B^T over stages [first, last). va, vb: each load's byte offset at stage 0 (BUF_OOB or above: zeros).
+// acc = A B^T over stages [first, last). va, vb: each load's byte offset at stage 0 (BUF_OOB or above: zeros).
 // tail: elements' bytes of the last stage that exist (128: all); later units of A are fed as zeros (B's must exist and
-// be finite, or be zeros too). FLUSH: stages per chunk (0: one chain); chunk sums are added in order, the chunks
-// counted from stage 0, so `first` must be a multiple of FLUSH.
-template <class T, int FLUSH>
+// be finite, or be zeros too). One chain of products for each output, in the order of the stages.
+template <class T>
 __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p, const Operands &in,
                                              const uint32_t (&va)[T::LA], const uint32_t (&vb)[T::LB], int first, int last,
-                                             int tail, f32x4 (&out)[T::MT][T::NT])
+                                             int tail, f32x4 (&acc)[T::MT][T::NT])
 {
     constexpr int MT = T::MT, NT = T::NT, NS = T::NS;
     auto issue = [&](int k, int buf, bool cut) {
@@ -128,14 +127,10 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
         if (tail < STAGE_BYTES && k == last - 1) issue(k, buf, true);
         else issue(k, buf, false);
     };
-    f32x4 acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (FLUSH) out[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     // Byte offset of this lane's first unit in the first row tile of A and of B; the second unit is 64 bytes on, XOR-ed.
     const int sw = unit_swizzle(p.r);
     const int u0 = 16 * (p.q ^ sw), u1 = 16 * ((p.q + 4) ^ sw);
@@ -146,7 +141,7 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
         if (first + s < last) load(first + s, s);
-    int buf = 0, chunk = 0;
+    int buf = 0;
     for (int k = first; k < last; ++k) {
         // stage k has landed: at most the NS - 2 stages behind it are still in flight
         if (NS > 2 && k + NS - 2 < last) wait_loads<(NS - 2) * (T::LA + T::LB)>();
@@ -154,51 +149,54 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
         lds_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
         const int into = buf == 0 ? NS - 1 : buf - 1;
         if (k + NS - 1 < last) load(k + NS - 1, into);
+        // Fragments are read ahead of their products: A's two tiles ahead, B's second half during the first.
         if constexpr (T::FP8) {
             auto frag = [&](int row0, int tile) {
                 return __builtin_shufflevector(__builtin_bit_cast(i32x4, unit(buf, row0, tile, u0)),
                                                __builtin_bit_cast(i32x4, unit(buf, row0, tile, u1)), 0, 1, 2, 3, 4, 5, 6, 7);
             };
-            i32x8 bf[NT];
+            i32x8 bf[NT], af[MT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) bf[t] = frag(b0, t);
+            af[0] = frag(a0, 0);
+            if (MT > 1) af[1] = frag(a0, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * (NT + (MT > 1 ? 2 : 1)), 0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const i32x8 af = frag(a0, m);
+                if (m + 2 < MT) {
+                    af[m + 2] = frag(a0, m + 2);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_e4m3(bf[t], af, acc[m][t]);
+                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_e4m3(bf[t], af[m], acc[m][t]);
+                __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
             }
         } else {
+            f16x8 bf[2][NT], af[2 * MT];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                f16x8 bf[NT];
+            for (int t = 0; t < NT; ++t) bf[0][t] = unit(buf, b0, t, u0);
+            af[0] = unit(buf, a0, 0, u0);
+            af[1] = unit(buf, a0, 1 % MT, MT > 1 ? u0 : u1);
+            __builtin_amdgcn_sched_group_barrier(0x100, NT + 2, 0);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) bf[t] = unit(buf, b0, t, h ? u1 : u0);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const f16x8 af = unit(buf, a0, m, h ? u1 : u0);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[m][t] = mfma_step(bf[t], af, acc[m][t]);
+            for (int s = 0; s < 2 * MT; ++s) {
+                if (s + 2 < 2 * MT) {
+                    af[s + 2] = unit(buf, a0, (s + 2) % MT, s + 2 < MT ? u0 : u1);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 }
+                if (s < MT) {  // B's second half, spread over the first half's steps
+#pragma unroll
+                    for (int t = s * NT / MT; t < (s + 1) * NT / MT; ++t) {
+                        bf[1][t] = unit(buf, b0, t, u1);
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[s % MT][t] = mfma_step(bf[s / MT][t], af[s], acc[s % MT][t]);
+                __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
             }
         }
-        if (FLUSH && (++chunk == FLUSH || k + 1 == last)) {
-            chunk = 0;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    out[m][t] += acc[m][t];
-                    acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-        }
         buf = buf == NS - 1 ? 0 : buf + 1;
-    }
-    if (!FLUSH) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) out[m][t] = acc[m][t];
     }
 }
 
