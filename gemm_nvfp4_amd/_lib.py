@@ -959,10 +959,6 @@ def _given(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, 
     return t
 
 
-def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype, dev: int) -> int | None:
-    return None if t is None else _ptr(t, name, dtype, dev)
-
-
 def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                        eps: float = 1e-6, s: torch.Tensor | None = None, y: torch.Tensor | None = None,
                        q: torch.Tensor | None = None, q_scale: torch.Tensor | None = None, want_y: bool = True,
@@ -971,26 +967,34 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, resi
     v = t / sqrt(mean(t^2) + eps) * weight. Returns (s, y, q, q_scale): s = fp16(t) (None without a residual and
     without s), y = fp16(v) (want_y), q uint8 E4M3 bytes of v / q_scale[m] with q_scale FP32 [M] (want_q, for
     nvfp4_linear_fp8_rows). s may be x or residual, y too (but not s)."""
-    shape = _matrix(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        _matrix(x, "x")
     M, K = shape
+    f16 = torch.float16
     if weight is not None and weight.shape != (K,):
         _shape(weight, "weight", (K,))
     if residual is not None and residual.shape != shape:
         _shape(residual, "residual", shape)
     if residual is not None or s is not None:
-        s = _given(s, "s", shape, torch.float16, x, stream)
-    y = _given(y, "y", shape, torch.float16, x, stream) if want_y else None
-    if want_q:
-        q = _given(q, "q", shape, torch.uint8, x, stream)
-        q_scale = _given(q_scale, "q_scale", (M,), torch.float32, x, stream)
+        s = _given(s, "s", shape, f16, x, stream)
+    if not want_y:
+        y = None
     else:
+        y = _given(y, "y", shape, f16, x, stream)
+    if not want_q:
         q = q_scale = None
+    else:
+        q, q_scale = _given(q, "q", shape, torch.uint8, x, stream), _given(q_scale, "q_scale", (M,), torch.float32, x, stream)
     dev = _current_device(x)
-    status = lib().nvfp4_add_rms_norm(
-        _ptr(x, "x", torch.float16, dev), _opt(residual, "residual", torch.float16, dev),
-        _opt(weight, "weight", torch.float16, dev), M, K, eps, _opt(s, "s", torch.float16, dev),
-        _opt(y, "y", torch.float16, dev), _opt(q, "q", torch.uint8, dev), _opt(q_scale, "q_scale", torch.float32, dev),
-        _raw_stream(stream, dev))
+    x_ptr = _ptr(x, "x", f16, dev)
+    residual_ptr = None if residual is None else _ptr(residual, "residual", f16, dev)
+    weight_ptr = None if weight is None else _ptr(weight, "weight", f16, dev)
+    s_ptr = None if s is None else _ptr(s, "s", f16, dev)
+    y_ptr = None if y is None else _ptr(y, "y", f16, dev)
+    q_ptr, scale_ptr = (None, None) if q is None else (_ptr(q, "q", torch.uint8, dev), _ptr(q_scale, "q_scale", torch.float32, dev))
+    status = lib().nvfp4_add_rms_norm(x_ptr, residual_ptr, weight_ptr, M, K, eps, s_ptr, y_ptr, q_ptr, scale_ptr,
+                                      _raw_stream(stream, dev))
     if status != NVFP4_OK:
         _check("nvfp4_add_rms_norm", status)
     return s, y, q, q_scale
@@ -1020,26 +1024,31 @@ def nvfp4_add_rms_norm_grad(t: torch.Tensor, dy: torch.Tensor, weight: torch.Ten
     """The gradient of nvfp4_add_rms_norm at its input t (the s of the forward call; x without a residual): dy is y's
     gradient, ds the residual stream's own (None: none). Returns (dx fp16 [M, K], the gradient of x and of the
     residual; dweight FP32 [K]), None for what is not wanted. dx may be dy or ds."""
-    shape = _matrix(t, "t")
+    shape = t.shape
+    if len(shape) != 2:
+        _matrix(t, "t")
     M, K = shape
+    f16 = torch.float16
     if dy.shape != shape:
         _shape(dy, "dy", shape)
     if ds is not None and ds.shape != shape:
         _shape(ds, "ds", shape)
     if weight is not None and weight.shape != (K,):
         _shape(weight, "weight", (K,))
-    dx = _given(dx, "dx", shape, torch.float16, t, stream) if want_dx else None
-    dev = _current_device(t)
+    dx = _given(dx, "dx", shape, f16, t, stream) if want_dx else None
     if want_dweight:
         dweight = _given(dweight, "dweight", (K,), torch.float32, t, stream)
         ws = _lora_ws(ws, _norm_grad_ws(M, K), t.device, stream)
-        work, work_bytes = _ptr(ws, "ws", ws.dtype, dev), ws.nbytes
     else:
-        dweight, work, work_bytes = None, None, 0
-    status = lib().nvfp4_add_rms_norm_grad(
-        _ptr(t, "t", torch.float16, dev), _ptr(dy, "dy", torch.float16, dev), _opt(ds, "ds", torch.float16, dev),
-        _opt(weight, "weight", torch.float16, dev), M, K, eps, _opt(dx, "dx", torch.float16, dev),
-        _opt(dweight, "dweight", torch.float32, dev), work, work_bytes, _raw_stream(stream, dev))
+        dweight = ws = None
+    dev = _current_device(t)
+    ds_ptr = None if ds is None else _ptr(ds, "ds", f16, dev)
+    weight_ptr = None if weight is None else _ptr(weight, "weight", f16, dev)
+    dx_ptr = None if dx is None else _ptr(dx, "dx", f16, dev)
+    dweight_ptr, ws_ptr, ws_bytes = (None, None, 0) if ws is None else (
+        _ptr(dweight, "dweight", torch.float32, dev), _ptr(ws, "ws", ws.dtype, dev), ws.nbytes)
+    status = lib().nvfp4_add_rms_norm_grad(_ptr(t, "t", f16, dev), _ptr(dy, "dy", f16, dev), ds_ptr, weight_ptr, M, K, eps,
+                                           dx_ptr, dweight_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev))
     if status != NVFP4_OK:
         _check("nvfp4_add_rms_norm_grad", status)
     return dx, dweight

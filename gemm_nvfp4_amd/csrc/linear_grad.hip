@@ -18,7 +18,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int FOLD_THREADS = 256;
-constexpr int CUS = 256;  // of an MI355X; the choice of a kernel, and so the order of a sum, does not ask the device
 
 // ---- few rows: dx from the packed weights ------------------------------------------------------------
 constexpr int ST_WAVES = 8, ST_ROWS = 64;            // waves per block, weight rows per wave
@@ -255,24 +254,25 @@ __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__r
     if (!tile_of_block(blockIdx.x, (M + T::BM - 1) / T::BM, (cols + T::BN - 1) / T::BN, tm, tn)) return;
     const Place p = place_of<T>();
     const int m0 = tm * T::BM, c0 = tn * T::BN;
-    const Operands in = {make_rsrc(a + (size_t)m0 * red, (uint32_t)min(T::BM, M - m0) * red * 2u),
-                         make_rsrc(b + (size_t)c0 * ld, (uint32_t)min(T::BN, cols - c0) * ld * 2u)};
-    uint32_t va[T::LA], vb[T::LB];
+    Rows<T::LA> ra;
+    Rows<T::LB> rb;
+    ra.buf = make_rsrc(a + (size_t)m0 * red, (uint32_t)min(T::BM, M - m0) * red * 2u);
+    rb.buf = make_rsrc(b + (size_t)c0 * ld, (uint32_t)min(T::BN, cols - c0) * ld * 2u);
 #pragma unroll
     for (int i = 0; i < T::LA; ++i) {
         const int r = load_row<T>(p, i);
-        va[i] = m0 + r < M ? (uint32_t)r * red * 2u + load_byte(r, p.lane) : BUF_OOB;
+        ra.off[i] = m0 + r < M ? (uint32_t)r * red * 2u + load_byte(r, p.lane) : BUF_OOB;
     }
 #pragma unroll
     for (int i = 0; i < T::LB; ++i) {
         const int r = load_row<T>(p, i), c = column_of_row<T>(r);
-        vb[i] = c0 + c < cols ? (uint32_t)c * ld * 2u + load_byte(r, p.lane) : BUF_OOB;
+        rb.off[i] = c0 + c < cols ? (uint32_t)c * ld * 2u + load_byte(r, p.lane) : BUF_OOB;
     }
     const int stages = (red + 63) / 64, per = (stages + gridDim.y - 1) / gridDim.y;
     const int first = min(stages, (int)blockIdx.y * per), last = min(stages, first + per);
     const int tail = last == stages && red % 64 ? red % 64 * 2 : STAGE_BYTES;
     f32x4 acc[T::MT][T::NT];
-    tile_product<T>(smem, p, in, va, vb, first, last, tail, acc);
+    tile_product<T>(smem, p, ra, rb, first, last, tail, acc);
     const float gs = PLANE ? 1.0f : gscale[0];
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
@@ -314,23 +314,24 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
     const int up = (p.wave >> 1) & 1;  // load rows 8 (wave + WAVES i): tile (wave + WAVES i) / 2
     const f16 *wb = w + (layout ? (size_t)2 * i0 + up : (size_t)up * I + i0) * K;
     const uint32_t step = (uint32_t)K * (layout ? 4u : 2u);  // bytes from pair to pair
-    const Operands in = {make_rsrc(x + (size_t)m0 * K, (uint32_t)min(T::BM, M - m0) * K * 2u),
-                         make_rsrc(wb, (uint32_t)(min(BI, I - i0) - 1) * step + K * 2u)};
-    uint32_t va[T::LA], vb[T::LB];
+    Rows<T::LA> ra;
+    Rows<T::LB> rb;
+    ra.buf = make_rsrc(x + (size_t)m0 * K, (uint32_t)min(T::BM, M - m0) * K * 2u);
+    rb.buf = make_rsrc(wb, (uint32_t)(min(BI, I - i0) - 1) * step + K * 2u);
 #pragma unroll
     for (int i = 0; i < T::LA; ++i) {
         const int r = load_row<T>(p, i);
-        va[i] = m0 + r < M ? (uint32_t)r * K * 2u + load_byte(r, p.lane) : BUF_OOB;
+        ra.off[i] = m0 + r < M ? (uint32_t)r * K * 2u + load_byte(r, p.lane) : BUF_OOB;
     }
 #pragma unroll
     for (int i = 0; i < T::LB; ++i) {
         const int r = load_row<T>(p, i);
         const int t = (r >> 4) % T::NT, wc = r / (16 * T::NT);
         const int pair = wc * 8 * T::NT + ((r >> 2) & 3) * 2 * T::NT + 4 * (t >> 1) + (r & 3);
-        vb[i] = i0 + pair < I ? (uint32_t)pair * step + load_byte(r, p.lane) : BUF_OOB;
+        rb.off[i] = i0 + pair < I ? (uint32_t)pair * step + load_byte(r, p.lane) : BUF_OOB;
     }
     f32x4 acc[T::MT][T::NT];
-    tile_product<T>(smem, p, in, va, vb, 0, K / 64, STAGE_BYTES, acc);
+    tile_product<T>(smem, p, ra, rb, 0, K / 64, STAGE_BYTES, acc);
     const float gs = gscale[0];
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
@@ -359,9 +360,6 @@ using T320x128 = Tile<false, 5, 4, 4, 2, 2>;
 using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
 using T64x128 = Tile<false, 2, 4, 2, 2, 3>;
 using T64x64 = Tile<false, 2, 2, 2, 2, 4>;
-struct Shape {
-    int bm, bn, per_cu, ns;
-};
 constexpr Shape SHAPES[] = {{384, 192, 1, 1940}, {256, 256, 1, 1510}, {192, 256, 1, 1320}, {192, 192, 1, 1170},
                             {320, 128, 1, 1390}, {128, 128, 2, 870},  {64, 128, 2, 700},   {64, 64, 2, 540}};
 
@@ -378,10 +376,10 @@ Choice choose(int64_t M, int64_t cols, int64_t red)
     Choice best = {0, 1, INT64_MAX};
     for (int i = 0; i < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++i) {
         const Shape &h = SHAPES[i];
-        const int64_t tiles = ((M + h.bm - 1) / h.bm) * ((cols + h.bn - 1) / h.bn), slots = (int64_t)CUS * h.per_cu;
-        for (int s = 1; s <= 8 && s * 8 <= stages; ++s) {
-            const int64_t rounds = (tiles * s + slots - 1) / slots;
-            int64_t ns = rounds * ((stages + s - 1) / s) * (tiles * s <= CUS && h.per_cu > 1 ? h.ns * 4 / 5 : h.ns);
+        const int64_t tiles = h.tiles(M, cols);
+        for (int s = 1; s <= 8 && (s == 1 || s * 8 <= stages); ++s) {
+            const bool alone = h.per_cu > 1 && tiles * s <= TILE_CUS;  // a block has its CU to itself
+            int64_t ns = h.rounds(tiles * s) * ((stages + s - 1) / s) * (alone ? h.ns * 4 / 5 : h.ns);
             if (s > 1) ns += 4000 + M * cols * 8 * s / 2500;  // there and back, with the fold's launch
             if (ns < best.ns) best = {i, s, ns};
         }
@@ -424,7 +422,7 @@ int launch_plain(const Choice &c, const f16 *a, int M, int red, const f16 *b, in
 {
     return with_shape(c.shape, [&](auto tile) {
         using T = decltype(tile);
-        const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((cols + T::BN - 1) / T::BN);
+        const int64_t tiles = SHAPES[c.shape].tiles(M, cols);
         return launch(c.splits > 1 ? grad_tile_kernel<T, true> : grad_tile_kernel<T, false>,
                       dim3(tile_grid(tiles), (unsigned)c.splits), dim3(T::WAVES * 64), 0, s, a, M, red, b, ld, cols, gscale, out);
     });
@@ -507,7 +505,7 @@ int run_linear_swiglu_grad(const uint16_t *x, const uint16_t *dh, int32_t M, con
     if (c.splits == 1)
         return with_shape(c.shape, [&](auto tile) {
             using T = decltype(tile);
-            const int64_t tiles = (int64_t)((M + T::BM - 1) / T::BM) * ((I + T::BN / 2 - 1) / (T::BN / 2));
+            const int64_t tiles = SHAPES[c.shape].tiles(M, w.rows);
             return launch(swiglu_grad_tile_kernel<T>, dim3(tile_grid(tiles)), dim3(T::WAVES * 64), 0, s, xf, M, K, wd, I, layout,
                           w.global_scale, df, o);
         });

@@ -13,7 +13,7 @@ namespace {
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int ROWS_STREAM_M = 64;
+constexpr int ROWS_STREAM_M = 64;  // most rows of the streaming kernel
 constexpr int ROWS_GROUP = 5;  // steps whose operands a wave holds at once
 
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b)
@@ -103,21 +103,22 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
     if (!tile_of_block(blockIdx.x, (M + T::BM - 1) / T::BM, (N + T::BN - 1) / T::BN, tm, tn)) return;
     const Place p = place_of<T>();
     const int m0 = tm * T::BM, c0 = tn * T::BN;
-    const Operands in = {make_rsrc(xq + (size_t)m0 * K, (uint32_t)min(T::BM, M - m0) * K),
-                         make_rsrc(w + (size_t)c0 * K, (uint32_t)min(T::BN, N - c0) * K)};
-    uint32_t va[T::LA], vb[T::LB];
+    Rows<T::LA> ra;
+    Rows<T::LB> rb;
+    ra.buf = make_rsrc(xq + (size_t)m0 * K, (uint32_t)min(T::BM, M - m0) * K);
+    rb.buf = make_rsrc(w + (size_t)c0 * K, (uint32_t)min(T::BN, N - c0) * K);
 #pragma unroll
     for (int i = 0; i < T::LA; ++i) {
         const int r = load_row<T>(p, i);
-        va[i] = m0 + r < M ? (uint32_t)r * K + load_byte(r, p.lane) : BUF_OOB;
+        ra.off[i] = m0 + r < M ? (uint32_t)r * K + load_byte(r, p.lane) : BUF_OOB;
     }
 #pragma unroll
     for (int i = 0; i < T::LB; ++i) {
         const int r = load_row<T>(p, i), c = column_of_row<T>(r);
-        vb[i] = c0 + c < N ? (uint32_t)c * K + load_byte(r, p.lane) : BUF_OOB;
+        rb.off[i] = c0 + c < N ? (uint32_t)c * K + load_byte(r, p.lane) : BUF_OOB;
     }
     f32x4 acc[T::MT][T::NT];
-    tile_product<T>(smem, p, in, va, vb, 0, K / STAGE_BYTES, STAGE_BYTES, acc);
+    tile_product<T>(smem, p, ra, rb, 0, K / STAGE_BYTES, STAGE_BYTES, acc);
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
         const int row = m0 + (p.wm * T::MT + m) * 16 + p.r;
@@ -135,9 +136,16 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
     }
 }
 
-// Tile shapes, and what a stage of every CU at work on one (two of the small ones) takes, in ns: measured on 256 (512)
-// tiles at 40 stages. What bounds them is the way from the L2s to LDS (12 to 15 TB/s over the chip: 64 KB a stage for
-// 256 x 256), with the matrix pipes about half busy.
+// Up to 32 rows always stream (32 rows of 4352 x 5120: 18.5 us against the tiles' 22). From 33 to 64 the tiles win (22 us
+// against 25 to 31) but where the columns make too few of them to fill the chip: 1024 x 16384 at 64 rows streams in 41 us
+// and takes 58 in tiles.
+bool use_stream(int M, int N) { return M <= 32 || (M <= ROWS_STREAM_M && N <= 2048); }
+
+// The tile shapes. `per_cu`: blocks of a shape that a CU holds; `ns`: what a 128-element stage takes with every CU full,
+// measured on whole rounds of tiles at 40 stages (1.0 to 2.65 PFLOP/s). The shape whose rounds over the CUs take the least
+// time is taken: 8192 x 4352 outputs of K = 5120 take 176 us in the two rounds of 384 x 192, 216 in the four of 192 x 256;
+// 333 x 4352 take 24 us with 64 x 64 and 35 with 192 x 128. What bounds the large shapes is the way from the L2s into LDS
+// (64 KB a stage for 256 x 256, 12 to 15 TB/s over the chip) and the matrix pipes, each a little more than half busy.
 using T384x192 = Tile<true, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<true, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<true, 6, 4, 2, 4, 2>;
@@ -145,6 +153,22 @@ using T192x192 = Tile<true, 6, 3, 2, 4, 2>;
 using T128x128 = Tile<true, 4, 4, 2, 2, 2>;
 using T64x128 = Tile<true, 2, 4, 2, 2, 3>;
 using T64x64 = Tile<true, 2, 2, 2, 2, 4>;
+constexpr Shape SHAPES[] = {{384, 192, 1, 1950}, {256, 256, 1, 1620}, {192, 256, 1, 1300}, {192, 192, 1, 1070},
+                            {128, 128, 2, 1000}, {64, 128, 2, 760},   {64, 64, 2, 580}};
+
+template <class F>
+int with_shape(int i, F &&f)
+{
+    switch (i) {  // the order of SHAPES
+    case 0: return f(T384x192{});
+    case 1: return f(T256x256{});
+    case 2: return f(T192x256{});
+    case 3: return f(T192x192{});
+    case 4: return f(T128x128{});
+    case 5: return f(T64x128{});
+    default: return f(T64x64{});
+    }
+}
 
 }  // namespace
 
@@ -153,7 +177,7 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
 {
     const int N = w.rows, K = w.k;
     f16 *o = reinterpret_cast<f16 *>(y);
-    if (M <= ROWS_STREAM_M) {
+    if (use_stream(M, N)) {
         const int groups = (K / STAGE_BYTES + ROWS_GROUP - 1) / ROWS_GROUP, most = M <= 16 ? 16 : 8;
         const int mt = (M + 15) / 16;
         auto *kernel = mt == 1 ? rows_stream_kernel<1> : mt == 2 ? rows_stream_kernel<2> : mt == 3 ? rows_stream_kernel<3>
@@ -161,37 +185,17 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
         return launch(kernel, dim3((unsigned)(N / 16)), dim3((unsigned)(64 * (groups < most ? groups : most))), 0, s, xq, xs, M,
                       w.codes, w.channel_scale, N, K, o);
     }
-    int result = NVFP4_ERR_LAUNCH;
-    int64_t least = INT64_MAX;
-    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    // The shape whose rounds of tiles over the CUs take the least time.
     int best = 0;
-    auto consider = [&](int i, int64_t bm, int64_t bn, int per_cu, int ns) {
-        const int64_t cost = (tiles(bm, bn) + 256 * per_cu - 1) / (256 * per_cu) * ns;
-        if (cost < least) least = cost, best = i;
-    };
-    consider(0, 384, 192, 1, 1950);
-    consider(1, 256, 256, 1, 1620);
-    consider(2, 192, 256, 1, 1300);
-    consider(3, 192, 192, 1, 1070);
-    consider(4, 128, 128, 2, 1000);
-    consider(5, 64, 128, 2, 760);
-    consider(6, 64, 64, 2, 580);
-    auto tiled = [&](auto tile) {
-        using T = decltype(tile);
-        result = launch(rows_tile_kernel<T>, dim3(tile_grid(tiles(T::BM, T::BN))), dim3(T::WAVES * 64), 0, s, xq, xs, M, w.codes,
-                        w.channel_scale, N, K, o);
-    };
-    switch (best) {
-    case 0: tiled(T384x192{}); break;
-    case 1: tiled(T256x256{}); break;
-    case 2: tiled(T192x256{}); break;
-    case 3: tiled(T192x192{}); break;
-    case 4: tiled(T128x128{}); break;
-    case 5: tiled(T64x128{}); break;
-    default: tiled(T64x64{}); break;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++i) {
+        const int64_t ns = SHAPES[i].rounds(SHAPES[i].tiles(M, N)) * SHAPES[i].ns;
+        if (ns < least) least = ns, best = i;
     }
-    return result;
+    return with_shape(best, [&](auto tile) {
+        using T = decltype(tile);
+        return launch(rows_tile_kernel<T>, dim3(tile_grid(SHAPES[best].tiles(M, N))), dim3(T::WAVES * 64), 0, s, xq, xs, M,
+                      w.codes, w.channel_scale, N, K, o);
+    });
 }
 
 }  // namespace nvfp4

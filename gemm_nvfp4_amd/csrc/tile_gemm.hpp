@@ -58,6 +58,9 @@ template <bool FP8_, int MT_, int NT_, int WM_, int WN_, int NS_>
 struct Tile {
     static constexpr bool FP8 = FP8_;
     static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, NS = NS_;
+    // products of one fragment of A with NT of B in a stage, and how many of these a fragment is read ahead (four are 3%
+    // faster than two with 256 x 256)
+    static constexpr int STEPS = FP8 ? MT : 2 * MT, AHEAD = STEPS < 4 ? STEPS : 4;
     static constexpr int WAVES = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
     static constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES;  // loads per wave and stage
     static constexpr int BYTES = (BM + BN) * STAGE_BYTES;           // one stage
@@ -96,48 +99,102 @@ __device__ __forceinline__ int column_of_row(int row)
     return w * 16 * T::NT + 4 * T::NT * q + 4 * t + j;
 }
 
-// Both operands' buffers, from the block's first row on.
-struct Operands {
-    rsrc_t a, b;
-};
-
-// acc = A B^T over stages [first, last). va, vb: each load's byte offset at stage 0 (BUF_OOB or above: zeros).
-// tail: elements' bytes of the last stage that exist (128: all); later units of A are fed as zeros (B's must exist and
-// be finite, or be zeros too). One chain of products for each output, in the order of the stages.
+// What one stage adds to a wave's tiles: acc += A B^T over the 128 bytes of the rows staged at `ar` (the block's rows of
+// A) and `br` (of B). A step is the products of one fragment of A with NT of B; fragments are read ahead of their
+// products: A's AHEAD steps, B's second half during the first.
 template <class T>
-__device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p, const Operands &in,
-                                             const uint32_t (&va)[T::LA], const uint32_t (&vb)[T::LB], int first, int last,
-                                             int tail, f32x4 (&acc)[T::MT][T::NT])
+__device__ __forceinline__ void stage_products(const unsigned char *ar, const unsigned char *br, const Place &p,
+                                               f32x4 (&acc)[T::MT][T::NT])
 {
-    constexpr int MT = T::MT, NT = T::NT, NS = T::NS;
-    auto issue = [&](int k, int buf, bool cut) {
-        unsigned char *s = smem + buf * T::BYTES;
-        const uint32_t so = (uint32_t)k * STAGE_BYTES;
-#pragma unroll
-        for (int i = 0; i < T::LA; ++i) {
-            uint32_t v = va[i];
-            if (cut) v = (int)load_byte(load_row<T>(p, i), p.lane) < tail ? v : BUF_OOB;
-            load_to_lds(in.a, s + (p.wave + T::WAVES * i) * 1024, v, so);
-        }
-        s += T::BM * STAGE_BYTES;
-#pragma unroll
-        for (int i = 0; i < T::LB; ++i) load_to_lds(in.b, s + (p.wave + T::WAVES * i) * 1024, vb[i], so);
-    };
-    auto load = [&](int k, int buf) {
-        if (tail < STAGE_BYTES && k == last - 1) issue(k, buf, true);
-        else issue(k, buf, false);
-    };
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // Byte offset of this lane's first unit in the first row tile of A and of B; the second unit is 64 bytes on, XOR-ed.
+    constexpr int MT = T::MT, NT = T::NT, D = T::AHEAD;
+    // This lane's rows, and its two units of a row: q and q + 4, swizzled (a tile's rows start at multiples of 16).
     const int sw = unit_swizzle(p.r);
     const int u0 = 16 * (p.q ^ sw), u1 = 16 * ((p.q + 4) ^ sw);
-    const int a0 = (p.wm * MT * 16 + p.r) * STAGE_BYTES, b0 = (T::BM + p.wn * NT * 16 + p.r) * STAGE_BYTES;
-    auto unit = [&](int buf, int row0, int tile, int u) {
-        return *reinterpret_cast<const f16x8 *>(smem + buf * T::BYTES + row0 + tile * 16 * STAGE_BYTES + u);
+    ar += (p.wm * MT * 16 + p.r) * STAGE_BYTES;
+    br += (p.wn * NT * 16 + p.r) * STAGE_BYTES;
+    auto unit = [](const unsigned char *rows, int tile, int u) {
+        return *reinterpret_cast<const f16x8 *>(rows + tile * 16 * STAGE_BYTES + u);
     };
+    if constexpr (T::FP8) {
+        auto frag = [&](const unsigned char *rows, int tile) {
+            return __builtin_shufflevector(__builtin_bit_cast(i32x4, unit(rows, tile, u0)),
+                                           __builtin_bit_cast(i32x4, unit(rows, tile, u1)), 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        i32x8 bf[NT], af[MT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) bf[t] = frag(br, t);
+#pragma unroll
+        for (int m = 0; m < D; ++m) af[m] = frag(ar, m);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * (NT + D), 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (m + D < MT) {
+                af[m + D] = frag(ar, m + D);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t] = mfma_e4m3(bf[t], af[m], acc[m][t]);
+            __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
+        }
+    } else {
+        f16x8 bf[2][NT], af[2 * MT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) bf[0][t] = unit(br, t, u0);
+#pragma unroll
+        for (int s = 0; s < D; ++s) af[s] = unit(ar, s % MT, s < MT ? u0 : u1);
+        __builtin_amdgcn_sched_group_barrier(0x100, NT + D, 0);
+#pragma unroll
+        for (int s = 0; s < 2 * MT; ++s) {
+            if (s + D < 2 * MT) {
+                af[s + D] = unit(ar, (s + D) % MT, s + D < MT ? u0 : u1);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            if (s < MT) {  // B's second half, spread over the first half's steps
+#pragma unroll
+                for (int t = s * NT / MT; t < (s + 1) * NT / MT; ++t) {
+                    bf[1][t] = unit(br, t, u1);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[s % MT][t] = mfma_step(bf[s / MT][t], af[s], acc[s % MT][t]);
+            __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
+        }
+    }
+}
+
+// Rows of one operand: a buffer from the block's first row on, and each load's byte offset at stage 0 (BUF_OOB: zeros).
+template <int L>
+struct Rows {
+    rsrc_t buf;
+    uint32_t off[L];
+};
+
+// acc = A B^T over stages [first, last): one chain of products for each output, in the order of the stages. tail: bytes of
+// the last stage of A's rows that exist (128: all); later units are fed as zeros (B's must exist and be finite).
+template <class T>
+__device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p, const Rows<T::LA> &a, const Rows<T::LB> &b,
+                                             int first, int last, int tail, f32x4 (&acc)[T::MT][T::NT])
+{
+    constexpr int NS = T::NS;
+    auto load = [&](int k, int buf) {
+        unsigned char *to = smem + buf * T::BYTES + p.wave * 1024;
+        const uint32_t so = (uint32_t)k * STAGE_BYTES;
+        const bool cut = tail < STAGE_BYTES && k == last - 1;  // uniform
+#pragma unroll
+        for (int i = 0; i < T::LA; ++i) {
+            uint32_t v = a.off[i];
+            if (cut) v = (int)load_byte(load_row<T>(p, i), p.lane) < tail ? v : BUF_OOB;
+            load_to_lds(a.buf, to + T::WAVES * i * 1024, v, so);
+        }
+        to += T::BM * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < T::LB; ++i) load_to_lds(b.buf, to + T::WAVES * i * 1024, b.off[i], so);
+    };
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+        for (int t = 0; t < T::NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
         if (first + s < last) load(first + s, s);
@@ -147,55 +204,9 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
         if (NS > 2 && k + NS - 2 < last) wait_loads<(NS - 2) * (T::LA + T::LB)>();
         else wait_loads<0>();
         lds_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
-        const int into = buf == 0 ? NS - 1 : buf - 1;
-        if (k + NS - 1 < last) load(k + NS - 1, into);
-        // Fragments are read ahead of their products: A's two tiles ahead, B's second half during the first.
-        if constexpr (T::FP8) {
-            auto frag = [&](int row0, int tile) {
-                return __builtin_shufflevector(__builtin_bit_cast(i32x4, unit(buf, row0, tile, u0)),
-                                               __builtin_bit_cast(i32x4, unit(buf, row0, tile, u1)), 0, 1, 2, 3, 4, 5, 6, 7);
-            };
-            i32x8 bf[NT], af[MT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) bf[t] = frag(b0, t);
-            af[0] = frag(a0, 0);
-            if (MT > 1) af[1] = frag(a0, 1);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2 * (NT + (MT > 1 ? 2 : 1)), 0);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m + 2 < MT) {
-                    af[m + 2] = frag(a0, m + 2);
-                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_e4m3(bf[t], af[m], acc[m][t]);
-                __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
-            }
-        } else {
-            f16x8 bf[2][NT], af[2 * MT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) bf[0][t] = unit(buf, b0, t, u0);
-            af[0] = unit(buf, a0, 0, u0);
-            af[1] = unit(buf, a0, 1 % MT, MT > 1 ? u0 : u1);
-            __builtin_amdgcn_sched_group_barrier(0x100, NT + 2, 0);
-#pragma unroll
-            for (int s = 0; s < 2 * MT; ++s) {
-                if (s + 2 < 2 * MT) {
-                    af[s + 2] = unit(buf, a0, (s + 2) % MT, s + 2 < MT ? u0 : u1);
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                }
-                if (s < MT) {  // B's second half, spread over the first half's steps
-#pragma unroll
-                    for (int t = s * NT / MT; t < (s + 1) * NT / MT; ++t) {
-                        bf[1][t] = unit(buf, b0, t, u1);
-                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[s % MT][t] = mfma_step(bf[s / MT][t], af[s], acc[s % MT][t]);
-                __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
-            }
-        }
+        if (k + NS - 1 < last) load(k + NS - 1, buf == 0 ? NS - 1 : buf - 1);
+        const unsigned char *at = smem + buf * T::BYTES;
+        stage_products<T>(at, at + T::BM * STAGE_BYTES, p, acc);
         buf = buf == NS - 1 ? 0 : buf + 1;
     }
 }
@@ -216,5 +227,14 @@ __device__ __forceinline__ bool tile_of_block(int b, int mt, int nt, int &m, int
     return true;
 }
 inline unsigned tile_grid(int64_t tiles) { return (unsigned)(8 * ((tiles + 7) / 8)); }
+
+// A tile shape as the host weighs it: its sizes, the blocks that a CU holds at once, and the time of a stage, in ns.
+// The CUs are counted as an MI355X has them, without asking the device: sizes alone decide which kernel runs.
+constexpr int TILE_CUS = 256;
+struct Shape {
+    int bm, bn, per_cu, ns;
+    int64_t tiles(int64_t rows, int64_t cols) const { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); }
+    int64_t rounds(int64_t blocks) const { return (blocks + (int64_t)TILE_CUS * per_cu - 1) / ((int64_t)TILE_CUS * per_cu); }
+};
 
 }  // namespace nvfp4
