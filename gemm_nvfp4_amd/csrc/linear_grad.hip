@@ -360,8 +360,9 @@ using T320x128 = Tile<false, 5, 4, 4, 2, 2>;
 using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
 using T64x128 = Tile<false, 2, 4, 2, 2, 3>;
 using T64x64 = Tile<false, 2, 2, 2, 2, 4>;
-constexpr Shape SHAPES[] = {{384, 192, 1, 1940}, {256, 256, 1, 1510}, {192, 256, 1, 1320}, {192, 192, 1, 1170},
-                            {320, 128, 1, 1390}, {128, 128, 2, 870},  {64, 128, 2, 700},   {64, 64, 2, 540}};
+constexpr Shape SHAPES[] = {{384, 192, 1, 1940, 1940}, {256, 256, 1, 1510, 1510}, {192, 256, 1, 1320, 1320},
+                            {192, 192, 1, 1170, 1170}, {320, 128, 1, 1390, 1390}, {128, 128, 2, 700, 435},
+                            {64, 128, 2, 560, 350},    {64, 64, 2, 430, 270}};
 
 struct Choice {
     int shape, splits;
@@ -378,8 +379,7 @@ Choice choose(int64_t M, int64_t cols, int64_t red)
         const Shape &h = SHAPES[i];
         const int64_t tiles = h.tiles(M, cols);
         for (int s = 1; s <= 8 && (s == 1 || s * 8 <= stages); ++s) {
-            const bool alone = h.per_cu > 1 && tiles * s <= TILE_CUS;  // a block has its CU to itself
-            int64_t ns = h.rounds(tiles * s) * ((stages + s - 1) / s) * (alone ? h.ns * 4 / 5 : h.ns);
+            int64_t ns = h.ns(tiles * s, (stages + s - 1) / s);
             if (s > 1) ns += 4000 + M * cols * 8 * s / 2500;  // there and back, with the fold's launch
             if (ns < best.ns) best = {i, s, ns};
         }

@@ -136,25 +136,32 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
     }
 }
 
-// Up to 32 rows always stream (32 rows of 4352 x 5120: 18.5 us against the tiles' 22). From 33 to 64 the tiles win (22 us
-// against 25 to 31) but where the columns make too few of them to fill the chip: 1024 x 16384 at 64 rows streams in 41 us
-// and takes 58 in tiles.
-bool use_stream(int M, int N) { return M <= 32 || (M <= ROWS_STREAM_M && N <= 2048); }
+// Up to 16 rows always stream. Up to 64 the stream wins where the reduction axis is long, which it has in flight at
+// once and the tiles walk: 48 rows of 2048 x 8192 take 19.5 us against 26, 64 of 1024 x 16384 41 against 50; of a shorter
+// one the tiles win: 32 rows of 2048 x 2048 take 5.8 us against 6.6, 48 of 4352 x 5120 18 against 25. The two meet
+// near 170 elements a row (5120 elements: 24 rows 16.9 against 17.5 us, 32 rows 18.5 against 17.6).
+bool use_stream(int M, int K) { return M <= 16 || (M <= ROWS_STREAM_M && K >= 170 * M); }
 
-// The tile shapes. `per_cu`: blocks of a shape that a CU holds; `ns`: what a 128-element stage takes with every CU full,
-// measured on whole rounds of tiles at 40 stages (1.0 to 2.65 PFLOP/s). The shape whose rounds over the CUs take the least
-// time is taken: 8192 x 4352 outputs of K = 5120 take 176 us in the two rounds of 384 x 192, 216 in the four of 192 x 256;
-// 333 x 4352 take 24 us with 64 x 64 and 35 with 192 x 128. What bounds the large shapes is the way from the L2s into LDS
-// (64 KB a stage for 256 x 256, 12 to 15 TB/s over the chip) and the matrix pipes, each a little more than half busy.
+// The tile shapes; their times (Shape) are measured at 40 stages (K = 5120). The shape of the least estimated time is
+// taken. Many tiles: whole rounds over the CUs decide, at 1.0 to 2.65 PFLOP/s; 8192 x 4352 outputs of K = 5120 take 174 us
+// in the two rounds of 384 x 192, 216 in the four of 192 x 256. What bounds the large shapes is the way from the
+// L2s into LDS (64 KB a stage for 256 x 256, 12 to 15 TB/s over the chip) and the matrix pipes, each a little
+// more than half busy. Few tiles: a block alone on its CU waits for its own loads, of which a CU keeps only so many in
+// flight (a ring of 9 stages is no faster than one of 3), so small tiles on all CUs win: 128 x 4352 outputs
+// take 18.8 us with 32 x 32, 20.6 with 64 x 32, 22.7 with 64 x 64; and shallow rings, of which a CU holds more blocks: 512 x 4352
+// outputs take 28.2 us with four blocks of 64 x 64 and two stages to a CU, 44 with two of five stages.
 using T384x192 = Tile<true, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<true, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<true, 6, 4, 2, 4, 2>;
 using T192x192 = Tile<true, 6, 3, 2, 4, 2>;
 using T128x128 = Tile<true, 4, 4, 2, 2, 2>;
 using T64x128 = Tile<true, 2, 4, 2, 2, 3>;
-using T64x64 = Tile<true, 2, 2, 2, 2, 4>;
-constexpr Shape SHAPES[] = {{384, 192, 1, 1950}, {256, 256, 1, 1620}, {192, 256, 1, 1300}, {192, 192, 1, 1070},
-                            {128, 128, 2, 1000}, {64, 128, 2, 760},   {64, 64, 2, 580}};
+using T64x64 = Tile<true, 2, 2, 2, 2, 2>;
+using T64x32 = Tile<true, 2, 1, 2, 2, 2>;
+using T32x32 = Tile<true, 1, 1, 2, 2, 3>;
+constexpr Shape SHAPES[] = {{384, 192, 1, 1950, 1950}, {256, 256, 1, 1620, 1620}, {192, 256, 1, 1300, 1300},
+                            {192, 192, 1, 1070, 1070}, {128, 128, 2, 770, 500},   {64, 128, 2, 600, 355},
+                            {64, 64, 4, 480, 235},     {64, 32, 6, 435, 150},     {32, 32, 6, 385, 105}};
 
 template <class F>
 int with_shape(int i, F &&f)
@@ -166,7 +173,9 @@ int with_shape(int i, F &&f)
     case 3: return f(T192x192{});
     case 4: return f(T128x128{});
     case 5: return f(T64x128{});
-    default: return f(T64x64{});
+    case 6: return f(T64x64{});
+    case 7: return f(T64x32{});
+    default: return f(T32x32{});
     }
 }
 
@@ -177,7 +186,7 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
 {
     const int N = w.rows, K = w.k;
     f16 *o = reinterpret_cast<f16 *>(y);
-    if (use_stream(M, N)) {
+    if (use_stream(M, K)) {
         const int groups = (K / STAGE_BYTES + ROWS_GROUP - 1) / ROWS_GROUP, most = M <= 16 ? 16 : 8;
         const int mt = (M + 15) / 16;
         auto *kernel = mt == 1 ? rows_stream_kernel<1> : mt == 2 ? rows_stream_kernel<2> : mt == 3 ? rows_stream_kernel<3>
@@ -188,7 +197,7 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
     int best = 0;
     int64_t least = INT64_MAX;
     for (int i = 0; i < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++i) {
-        const int64_t ns = SHAPES[i].rounds(SHAPES[i].tiles(M, N)) * SHAPES[i].ns;
+        const int64_t ns = SHAPES[i].ns(SHAPES[i].tiles(M, N), K / STAGE_BYTES);
         if (ns < least) least = ns, best = i;
     }
     return with_shape(best, [&](auto tile) {

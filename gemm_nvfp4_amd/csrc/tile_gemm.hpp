@@ -6,11 +6,12 @@
 // stages of 128 bytes (64 fp16 or 128 E4M3 elements): both operands' rows come into LDS by direct-to-LDS loads,
 // one 1 KB instruction for eight rows, NS - 1 stages ahead, with one block barrier per stage.
 //
-// LDS: a row is 128 bytes, its eight 16-byte units XOR-ed with 2 * ((row / 4) % 4). A fragment read takes unit
-// (q or q + 4) of rows 0..15 in lane group q; a half-wave of a 16-byte read is conflict-free where its 32 units
-// fall on 32 slots modulo 512 bytes (four rows): rows r, r + 4, r + 8, r + 12 of the two lane groups then land on
-// the eight different units of their slot. A direct-to-LDS load writes 16 bytes a lane in lane order, so the swizzle
-// stands in the lane's global address instead; it stays within the row's 128 bytes.
+// LDS: a row is 128 bytes, its eight 16-byte units XOR-ed with (row / 2) % 8. A 16-byte read is conflict-free where 16
+// neighbouring lanes fall on the 16 units of 256 bytes (two rows). A fragment read takes unit q or q + 4 of rows
+// 0..15 in lanes 0..15 of group q: two rows of a parity and their neighbours differ in (row / 2) % 8, so the sixteen
+// rows take each unit of both parities once (counted: no conflicts; XOR-ed with 2 * ((row / 4) % 4) half of
+// all LDS cycles went to them). A direct-to-LDS load writes 16 bytes a lane in lane order, so the swizzle stands in
+// the lane's global address instead; it stays within the row's 128 bytes.
 //
 // The weight rows feed MFMA's first operand and the batch's rows the second, so a lane's four results of a tile are
 // four neighbouring columns of one row. Weight row 16 t + 4 q + j of a wave's tiles holds column 4 NT q + 4 t + j:
@@ -228,13 +229,20 @@ __device__ __forceinline__ bool tile_of_block(int b, int mt, int nt, int &m, int
 }
 inline unsigned tile_grid(int64_t tiles) { return (unsigned)(8 * ((tiles + 7) / 8)); }
 
-// A tile shape as the host weighs it: its sizes, the blocks that a CU holds at once, and the time of a stage, in ns.
-// The CUs are counted as an MI355X has them, without asking the device: sizes alone decide which kernel runs.
+// A tile shape as the host weighs it: its sizes, the blocks that a CU holds at once, and what a stage takes, in ns: of a
+// block alone on its CU (bound by the way of its own loads), and per block where a CU holds several (bound by what
+// the CU loads or multiplies). The CUs are counted as an MI355X has them, without asking the device: sizes alone decide
+// which kernel runs.
 constexpr int TILE_CUS = 256;
 struct Shape {
-    int bm, bn, per_cu, ns;
+    int bm, bn, per_cu, alone, each;
     int64_t tiles(int64_t rows, int64_t cols) const { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); }
-    int64_t rounds(int64_t blocks) const { return (blocks + (int64_t)TILE_CUS * per_cu - 1) / ((int64_t)TILE_CUS * per_cu); }
+    int64_t ns(int64_t blocks, int64_t stages) const
+    {
+        const int64_t full = blocks / (TILE_CUS * per_cu), rest = blocks % (TILE_CUS * per_cu);
+        const int64_t last = (rest + TILE_CUS - 1) / TILE_CUS * each;
+        return stages * (full * per_cu * each + (rest == 0 ? 0 : last > alone ? last : alone));
+    }
 };
 
 }  // namespace nvfp4

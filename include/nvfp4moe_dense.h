@@ -58,8 +58,8 @@ int nvfp4_add_rms_norm_grad(const uint16_t *t, const uint16_t *dy, const uint16_
  * The channel-FP8 projection of 8-bit rows (nvfp4_linear_fp8 with its activations in 8 bits too):
  *   y[m][n] = fp16_rne( (x_scale[m] * s[n]) * sum_k e4m3(xq[m][k]) * e4m3(W[n][k]) ),  FP32 accumulation,
  *   xq uint8 [M][K] E4M3FN bytes, x_scale FP32 [M], w rows = N, k = K, y fp16 [M][N].
- * The sum is taken in 512-element chunks, added in order; a batch is bitwise equal to single-row calls. NaN bytes
- * and infinite or NaN scales follow IEEE rules and stay in their row or column.
+ * The sum is one chain of 128-element steps, in order, at every batch size: a batch is bitwise equal to single-row
+ * calls. NaN bytes and infinite or NaN scales follow IEEE rules and stay in their row or column.
  * Requirements: K % 128 == 0 and K <= 16384; N % 16 == 0; M <= 2^26; xq, y, codes 16-byte aligned, FP32 4-byte.
  * Errors: as nvfp4_linear_fp8.
  * --------------------------------------------------------------------------------------------- */

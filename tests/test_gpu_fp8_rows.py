@@ -12,7 +12,7 @@ import gemm_nvfp4_amd as G
 
 pytestmark = pytest.mark.gpu
 
-# batch sizes on both sides of every change of kernel (streams up to 32 rows; tiles of 64, 128 and 192 rows)
+# batch sizes on both sides of every change of kernel: up to 16 rows stream, up to 64 where K >= 170 rows, more take tiles
 BATCHES = [1, 2, 15, 16, 17, 32, 33, 64, 65, 130, 333]
 
 
@@ -67,12 +67,14 @@ def test_random_bytes(m, n, k):
 @pytest.mark.parametrize("n,k", [(4352, 5120), (208, 1664)])
 def test_rows_do_not_depend_on_the_batch(n, k):
     """One result for a row at every batch size: streams, small, medium and large tiles."""
-    m = 2400
+    m = 4000
     xq, xs, wq, ws = _case(n, m, n, k, False)
     w = G.FP8ChannelTensor(torch.from_numpy(wq).cuda(), torch.from_numpy(ws).cuda())
     x, s = torch.from_numpy(xq).cuda(), torch.from_numpy(xs).cuda()
     y = G.nvfp4_linear_fp8_rows(x, s, w)
-    for lo, hi in ((0, 1), (77, 94), (100, 133), (2399, 2400), (1000, 1080), (300, 700), (0, 1100)):
+    # streams of 1, 17 and 30 rows, then tiles: of 4352 x 5120 one size for each shape
+    for lo, hi in ((0, 1), (3999, 4000), (77, 94), (100, 130), (1000, 1080), (300, 556), (300, 700), (200, 1050),
+                   (3, 1299), (1, 2051), (0, 2400), (7, 3207)):
         part = G.nvfp4_linear_fp8_rows(x[lo:hi].contiguous(), s[lo:hi].contiguous(), w)
         assert torch.equal(part.view(torch.int16), y[lo:hi].view(torch.int16)), (lo, hi)
 
