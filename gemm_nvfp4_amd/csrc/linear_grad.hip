@@ -17,6 +17,8 @@
 namespace nvfp4 {
 namespace {
 
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
 constexpr int FOLD_THREADS = 256;
 
 // ---- few rows: dx from the packed weights ------------------------------------------------------------
@@ -148,7 +150,6 @@ __global__ __launch_bounds__(FOLD_THREADS) void grad_fold_kernel(const float *__
     if (i >= plane) return;
     const f32x4 s = plane_sum(part + i, plane, S);
     const float gs = gscale[0];
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
     f16x4 o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = f16_of_f32(s[e] * gs);
@@ -164,8 +165,6 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float &d
     du = dh * (g * sig);
     dg = dh * u * (sig * (1.0f + g * (1.0f - sig)));
 }
-
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 // dz of four gate/up pairs i .. i + 3 of row m, from their sums before the global scale.
 __device__ __forceinline__ void store_dz(f16 *dz, size_t row, int I, int i, int layout, const f32x4 &g, const f32x4 &u, float gs,
@@ -348,21 +347,23 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
 }
 
 // ---- host --------------------------------------------------------------------------------------------
-// The tile shapes. `per_cu`: blocks of a shape that a CU holds; `ns`: what a 64-element stage takes with every CU full,
-// measured at 4096 rows of 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds of tiles). Rounds decide:
-// 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of 256 x 256 (272 tiles on 256 CUs), 200
-// in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 126 with 320 x 128, 143 with 128 x 128.
+// The tile shapes; their times (Shape) are measured at 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds
+// of tiles). Rounds decide at many rows: 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of
+// 256 x 256 (272 tiles on 256 CUs), 200 in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 126 with
+// 320 x 128, 143 with 128 x 128. At some hundred rows the CUs are filled by small tiles with rings of two stages,
+// several to a CU: 512 x 5120 outputs of 4352 rows take 60 us with 64 x 64 (88 with four stages and two blocks), 64 with
+// 128 x 64, 71 with 128 x 128.
 using T384x192 = Tile<false, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<false, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<false, 6, 4, 2, 4, 2>;
 using T192x192 = Tile<false, 3, 6, 4, 2, 2>;
 using T320x128 = Tile<false, 5, 4, 4, 2, 2>;
 using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
-using T64x128 = Tile<false, 2, 4, 2, 2, 3>;
-using T64x64 = Tile<false, 2, 2, 2, 2, 4>;
+using T128x64 = Tile<false, 4, 2, 2, 2, 2>;
+using T64x64 = Tile<false, 2, 2, 2, 2, 2>;
 constexpr Shape SHAPES[] = {{384, 192, 1, 1940, 1940}, {256, 256, 1, 1510, 1510}, {192, 256, 1, 1320, 1320},
-                            {192, 192, 1, 1170, 1170}, {320, 128, 1, 1390, 1390}, {128, 128, 2, 700, 435},
-                            {64, 128, 2, 560, 350},    {64, 64, 2, 430, 270}};
+                            {192, 192, 1, 1170, 1170}, {320, 128, 1, 1390, 1390}, {128, 128, 2, 800, 450},
+                            {128, 64, 3, 600, 375},    {64, 64, 4, 530, 250}};
 
 struct Choice {
     int shape, splits;
@@ -397,7 +398,7 @@ int with_shape(int i, F &&f)
     case 3: return f(T192x192{});
     case 4: return f(T320x128{});
     case 5: return f(T128x128{});
-    case 6: return f(T64x128{});
+    case 6: return f(T128x64{});
     default: return f(T64x64{});
     }
 }
