@@ -1,17 +1,19 @@
 // linear_grad.hip -- gradients through frozen NVFP4 weights (include/nvfp4moe_dense.h): of the dense projection
 // towards its input, dx = dy W, and of the gated projection towards its gate and up rows, which are computed again.
 //
-// Two regimes by the batch size:
+// Three regimes by the batch size:
 //   * few rows: the packed weights are streamed once. dx: the reduction axis is the weight's rows, the packed axis the
 //     output's columns, so a lane takes eight rows' dwords (eight codes each) and transposes them in registers into
 //     eight B fragments, one per code position; no value crosses a lane. A block's waves share 512 rows of the weight,
 //     add their tiles in LDS in order and store one FP32 plane; a second launch adds the planes in order. Gated:
 //     the chunk products of the split-K projection (linear.hip), then a fold with the gradient's epilogue;
+//   * some hundred rows, gated: tiles on the packed weights, decoded in registers (packed_gemm.hpp), in one launch;
 //   * many rows: the weight is decoded once into the workspace (for dx transposed), exactly, as fp16, and the tiled
 //     product of tile_gemm.hpp runs on it, with the gradient in its epilogue. Where the output has too few tiles for
 //     the CUs the reduction axis is split too, and the same folds add the planes.
 #include "dense.hpp"
 #include "nvfp4_device.hpp"
+#include "packed_gemm.hpp"
 #include "tile_gemm.hpp"
 
 namespace nvfp4 {
@@ -346,6 +348,64 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
     }
 }
 
+// ---- some hundred rows, gated: packed weights ----------------------------------------------------------------
+// The gated gradient from the packed rows in one launch. Weight row 4 q + j of a wave's tile t is pair
+// i0 + 8 NT w + 2 NT q + 2 t + j % 2, gate (j < 2) or up: a lane has both of 2 NT neighbouring pairs of a row.
+// 4352 x 5120: 333 rows take 34 us (435 TFLOP/s; 47 us by chunk products, 53 decoded), 700 rows 52 us (600; 70 decoded), 1900
+// rows 90 us (940; 115 decoded). A block alone on its CU is bound by a stage's latency (0.9 us: the way into LDS, sixteen
+// fragment reads, four decodes in a row), several by the LDS reads of A, which NT tiles of a wave share.
+template <class T>
+__global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(const f16 *__restrict__ x, int M, int K,
+                                                                        const uint8_t *__restrict__ codes,
+                                                                        const uint8_t *__restrict__ scales, int I, int layout,
+                                                                        const float *__restrict__ gscale,
+                                                                        const f16 *__restrict__ dh, f16 *__restrict__ dz)
+{
+    constexpr int BI = T::BN / 2, NP = 2 * T::NT;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[T::LDS];
+    int tm, tn;
+    if (!tile_of_block(blockIdx.x, (M + T::BM - 1) / T::BM, (I + BI - 1) / BI, tm, tn)) return;
+    const PackedPlace p = packed_place<T>();
+    const int m0 = tm * T::BM, i0 = tn * BI + p.wave * 8 * T::NT;
+    PackedRows<T> b;
+#pragma unroll
+    for (int t = 0; t < T::NT; ++t) {
+        const int i = min(i0 + NP * (p.r >> 2) + 2 * t + (p.r & 1), I - 1), up = (p.r >> 1) & 1;
+        const size_t row = layout ? 2 * (size_t)i + up : (size_t)up * I + i;
+        b.codes[t] = codes + row * (K >> 1) + 16 * p.q;
+        b.scales[t] = scales + row * (K >> 4) + 2 * p.q;
+    }
+    f32x4 acc[T::MT][T::NT];
+    if (!packed_product<T>(smem, p, x + (size_t)m0 * K, min(T::BM, M - m0), K, b, acc)) return;
+    const float gs = gscale[0];
+    const int i = i0 + NP * p.q;  // I % 16 == 0: all of a lane's pairs or none
+    if (i >= I) return;
+    typedef _Float16 pairs_t __attribute__((ext_vector_type(NP)));
+    typedef _Float16 both_t __attribute__((ext_vector_type(2 * NP)));
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m) {
+        const int row = m0 + 16 * m + p.r;
+        if (row >= M) continue;
+        const pairs_t d = *reinterpret_cast<const pairs_t *>(dh + (size_t)row * I + i);
+        pairs_t g, u;
+        both_t z;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const f32x4 &s = acc[m][e >> 1];
+            float dg, du;
+            swiglu_grad(s[e & 1] * gs, s[2 + (e & 1)] * gs, (float)d[e], dg, du);
+            g[e] = z[2 * e] = f16_of_f32(dg), u[e] = z[2 * e + 1] = f16_of_f32(du);
+        }
+        f16 *o = dz + (size_t)row * 2 * I;
+        if (layout) {
+            *reinterpret_cast<both_t *>(o + 2 * i) = z;
+        } else {
+            *reinterpret_cast<pairs_t *>(o + i) = g;
+            *reinterpret_cast<pairs_t *>(o + I + i) = u;
+        }
+    }
+}
+
 // ---- host --------------------------------------------------------------------------------------------
 // The tile shapes; their times (Shape) are measured at 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds
 // of tiles). Rounds decide at many rows: 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of
@@ -403,16 +463,30 @@ int with_shape(int i, F &&f)
     }
 }
 
-// Whether the gated gradient of M rows takes the packed weights (the chunk products of linear.hip in passes of 64 rows,
-// and their fold) or decodes them first. Estimates in ns fitted to measurements, 4352 x 5120: 15 us at 64 rows by the
-// packed ones and 32 decoded, 22 and 41 at 128, 35 and 49 at 256, 48 and 52 at 333, 71 and 60 at 512; 2048 x 2048: 12 and
-// 14 at 64 rows, 17 and 15 at 128, 26 and 17 at 256.
-bool swiglu_packed(int64_t M, int64_t rows, int64_t K)
+// The tiles on packed weights, for the gated gradient. Times of a stage of 128 elements (of two with KS = 2, whose groups
+// walk them together), measured at 4352 x 5120.
+using P64x64x2 = PackedTile<4, 1, 4, 2, 4>;
+using P64x64 = PackedTile<4, 1, 4, 1, 4>;
+using P128x128 = PackedTile<8, 2, 4, 1, 2>;
+constexpr Shape PACKED[] = {{64, 64, 2, 1200, 800}, {64, 64, 4, 920, 400}, {128, 128, 2, 1700, 1000}};
+
+// How the gated gradient of M rows is computed: by the chunk products of linear.hip in passes of 64 rows and their fold
+// (CHUNKS), in tiles on the packed weights (the number of the shape), or in tiles on decoded ones (DECODED). Estimates in
+// ns fitted to measurements; 4352 x 5120, us by the three: 128 rows 22, 30, 41; 333 rows 48, 35, 53; 512 rows 71, 47, 61;
+// 1000 rows 138, 79, 88; 1900 rows packed 90, 2000 rows 121 decoded; 4096 rows 215 packed, 166 decoded.
+enum { CHUNKS = -2, DECODED = -1 };
+int swiglu_way(int64_t M, int64_t rows, int64_t K)
 {
-    if (M <= ST_MAX_M) return true;
-    const int64_t passes = (M + 63) / 64, elements = rows * K;
-    const int64_t packed = 6000 + elements / 5000 + passes * (4000 + num_chunks((int)K) * rows * 64 * 8 / 8500);
-    return packed < choose(M, rows, K).ns + 2000 + elements * 53 / 100000;
+    if (M <= ST_MAX_M) return CHUNKS;
+    const int64_t elements = rows * K, stages = K / PACKED_STAGE;
+    int way = CHUNKS;
+    int64_t least = 7000 + elements / 4000 + M * (31 + num_chunks((int)K) * rows * 8 / 5000);  // the planes, there and back
+    for (int i = 0; i < 3; ++i) {
+        const int64_t ns = 2000 + PACKED[i].ns(PACKED[i].tiles(M, rows), i == 0 ? (stages + 1) / 2 : stages);
+        if (ns < least) least = ns, way = i;
+    }
+    const int64_t decoded = choose(M, rows, K).ns + 2000 + elements * 53 / 100000;
+    return decoded < least ? DECODED : way;
 }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -481,7 +555,9 @@ int run_linear_grad(const uint16_t *dy, int32_t M, const nvfp4_weights &w, uint1
 
 size_t linear_swiglu_grad_ws_bytes(int32_t M, int32_t rows, int32_t K)
 {
-    if (swiglu_packed(M, rows, K)) return up256(linear_ws_bytes(M, rows, K));
+    const int way = swiglu_way(M, rows, K);
+    if (way == CHUNKS) return up256(linear_ws_bytes(M, rows, K));
+    if (way != DECODED) return 256;  // nothing is kept there; 0 means sizes that are rejected
     const Choice c = choose(M, rows, K);
     const size_t planes = c.splits > 1 ? (size_t)c.splits * M * rows * sizeof(float) : 0;
     return up256((size_t)rows * K * 2) + up256(planes);
@@ -493,10 +569,19 @@ int run_linear_swiglu_grad(const uint16_t *x, const uint16_t *dh, int32_t M, con
     const int K = w.k, I = w.rows / 2;
     const f16 *xf = reinterpret_cast<const f16 *>(x), *df = reinterpret_cast<const f16 *>(dh);
     f16 *o = reinterpret_cast<f16 *>(dz);
-    if (swiglu_packed(M, w.rows, K)) {
+    const int way = swiglu_way(M, w.rows, K);
+    if (way == CHUNKS) {
         float *part = static_cast<float *>(ws);
         const int st = run_linear_partials(x, M, w, part, s);
         return st != NVFP4_OK ? st : launch_swiglu_fold(part, num_chunks(K), M, I, w, layout, df, o, s);
+    }
+    if (way != DECODED) {
+        auto tiles = [&](auto tile) {
+            using T = decltype(tile);
+            return launch(swiglu_grad_packed_kernel<T>, dim3(tile_grid(PACKED[way].tiles(M, w.rows))), dim3(T::THREADS), 0, s, xf, M,
+                          K, w.codes, w.scales, I, layout, w.global_scale, df, o);
+        };
+        return way == 0 ? tiles(P64x64x2{}) : way == 1 ? tiles(P64x64{}) : tiles(P128x128{});
     }
     f16 *wd = static_cast<f16 *>(ws);
     const size_t eights = (size_t)w.rows * K / 8;

@@ -1,0 +1,146 @@
+// packed_gemm.hpp -- C = A B^T with A fp16 [M][K] and B NVFP4 rows, decoded in registers: the tiled product of the gated
+// projection's gradient at a few hundred rows (linear_grad.hip), where the product over decoded weights (tile_gemm.hpp)
+// would spend as long on writing and reading them: they take 3.6 times the packed bytes.
+//
+// A block owns BM x BN outputs; its waves stand side by side along B, a wave has MT x NT tiles of 16 x 16. The
+// reduction axis is walked in stages of 128 elements:
+//   * A's rows, 256 bytes each, come into LDS by direct-to-LDS loads a stage ahead, with one block barrier a stage. A
+//     row's sixteen 16-byte units are XOR-ed with the row's number modulo 16, in the lane's global address, so that the
+//     16 lanes of a fragment read fall on the 16 units of 256 bytes;
+//   * each wave loads its own codes a stage ahead, 16 bytes a lane and tile: lane group q owns elements 32 q .. + 31 of
+//     the stage, MFMA step d takes elements 32 q + 8 d .. + 7 of them, and A's fragment of that step is unit 4 q + d of
+//     the row. A step's weights are decoded while the products of the step before run.
+// KS wave groups of a block share the reduction axis in runs of stages, and the first group adds the others' sums in
+// order: a stage takes about a microsecond of waiting, and few blocks are bound by its number.
+//
+// The weight rows feed MFMA's first operand, the batch's rows the second: a lane's four results of a tile belong to one
+// row of A, and the kernel chooses which weight rows they are.
+#pragma once
+
+#include "tile_gemm.hpp"
+
+namespace nvfp4 {
+
+constexpr int PACKED_STAGE = 128;  // elements
+
+template <int MT_, int NT_, int WN_, int KS_, int OCC_>
+struct PackedTile {
+    static constexpr int MT = MT_, NT = NT_, WN = WN_, KS = KS_, OCC = OCC_;  // OCC: waves of a SIMD that have registers
+    static constexpr int BM = MT * 16, BN = WN * NT * 16, THREADS = 64 * WN * KS;
+    static constexpr int LA = BM / 4 / WN;                // A's loads per wave and stage
+    static constexpr int BYTES = BM * PACKED_STAGE * 2;   // one stage of A
+    static constexpr int LDS = KS * 2 * BYTES;
+    static_assert(LA * 4 * WN == BM && WN % 4 == 0, "whole loads per wave, all of one unit per lane");
+    static_assert(KS == 1 || MT * NT * WN * 1024 <= 2 * BYTES, "a group's sums fit its stages");
+};
+
+// This wave's and lane's place: lane 16 q + r of wave `wave` of group `group`.
+struct PackedPlace {
+    int group, wave, lane, r, q;
+};
+template <class T>
+__device__ __forceinline__ PackedPlace packed_place()
+{
+    PackedPlace p;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    p.group = w / T::WN, p.wave = w % T::WN;
+    p.lane = threadIdx.x & 63, p.r = p.lane & 15, p.q = p.lane >> 4;
+    return p;
+}
+
+// The lane's codes and block scales of its weight row in each of its tiles, at its first element of the row.
+template <class T>
+struct PackedRows {
+    const uint8_t *codes[T::NT], *scales[T::NT];
+};
+
+// acc = A B^T, A's rows from `a` on (`rows` of them, at most BM; the others count as zeros), K % 128 == 0. The result is in
+// the first group's waves; the others return false.
+template <class T>
+__device__ __forceinline__ bool packed_product(unsigned char *smem_all, const PackedPlace &p, const f16 *a, int rows, int K,
+                                               const PackedRows<T> &b, f32x4 (&acc)[T::MT][T::NT])
+{
+    constexpr int MT = T::MT, NT = T::NT, ROW = PACKED_STAGE * 2;
+    const int stages = K / PACKED_STAGE, per = (stages + T::KS - 1) / T::KS;
+    const int first = min(stages, p.group * per), last = min(stages, first + per);
+    unsigned char *const smem = smem_all + p.group * 2 * T::BYTES;
+    const rsrc_t buf = make_rsrc(a, (uint32_t)rows * K * 2u);
+    const int row0 = 4 * p.wave + (p.lane >> 4);  // load i of a wave: rows 4 (wave + WN i) .. + 3, whole sixteens apart
+    uint32_t off[T::LA];
+#pragma unroll
+    for (int i = 0; i < T::LA; ++i) {
+        const int row = row0 + 4 * T::WN * i;
+        off[i] = row < rows ? (uint32_t)row * K * 2u + 16u * ((p.lane & 15) ^ (row0 & 15)) : BUF_OOB;
+    }
+    auto load_a = [&](int k) {
+        unsigned char *to = smem + ((k - first) & 1) * T::BYTES + p.wave * 1024;
+#pragma unroll
+        for (int i = 0; i < T::LA; ++i) load_to_lds(buf, to + T::WN * i * 1024, off[i], (uint32_t)k * ROW);
+    };
+    u32x4 codes[NT];
+    uint16_t scales[NT];
+    auto load_b = [&](int k) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            codes[t] = *reinterpret_cast<const u32x4 *>(b.codes[t] + (size_t)k * (PACKED_STAGE / 2));
+            scales[t] = *reinterpret_cast<const uint16_t *>(b.scales[t] + (size_t)k * (PACKED_STAGE / 16));
+        }
+    };
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (first < last) load_b(first), load_a(first);
+    const int a0 = p.r * ROW;
+    int unit[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) unit[d] = a0 + 16 * ((4 * p.q + d) ^ p.r);
+    for (int k = first; k < first + per; ++k) {  // every group passes every barrier
+        wait_loads<0>();  // this wave's part of stage k
+        lds_barrier();    // everyone's part, and everyone is done with the other buffer
+        if (k >= last) continue;
+        const unsigned char *const at = smem + ((k - first) & 1) * T::BYTES;
+        f16x8 af[4][MT], bf[2][NT];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) af[d][m] = *reinterpret_cast<const f16x8 *>(at + unit[d] + m * 16 * ROW);
+        if (k + 1 < last) load_a(k + 1);
+        auto decode = [&](int d) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) bf[d & 1][t] = decode8(codes[t][d], e4m3_pair<false>(scales[t])[d >> 1]);
+        };
+        decode(0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if (d < 3) decode(d + 1);
+            else if (k + 1 < last) load_b(k + 1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_step(bf[d & 1][t], af[d][m], acc[m][t]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if constexpr (T::KS > 1) {
+        lds_barrier();  // the last stages have been read
+        f32x4 *sums = reinterpret_cast<f32x4 *>(smem) + p.wave * MT * NT * 64 + p.lane;
+        if (p.group > 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sums[(m * NT + t) * 64] = acc[m][t];
+        }
+        lds_barrier();
+        if (p.group > 0) return false;
+#pragma unroll
+        for (int g = 1; g < T::KS; ++g)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[m][t] += sums[g * 2 * (T::BYTES / 16) + (m * NT + t) * 64];
+    }
+    return true;
+}
+
+}  // namespace nvfp4

@@ -157,7 +157,11 @@ def test_swiglu_grad(m, n, k, layout):
     assert np.all(np.abs(dz.double().cpu().numpy() - ref) <= bound)
 
 
-@pytest.mark.parametrize("m,n,k,layout", [(333, 4352, 5120, 1), (2100, 4352, 1152, 0), (3000, 4384, 896, 1), (20, 2048, 16384, 0)])
+# packed tiles of 64 x 64 with two groups and with one and of 128 x 128, each in both layouts with ragged rows and columns
+# and an odd number of stages; then decoded weights and chunk products
+@pytest.mark.parametrize("m,n,k,layout", [(333, 4352, 5120, 1), (397, 4384, 1152, 0), (500, 4352, 896, 1), (1500, 4384, 640, 0),
+                                          (1000, 4384, 5120, 0), (1100, 4352, 4992, 1), (2100, 4352, 1152, 0),
+                                          (4100, 2080, 896, 1), (2500, 4352, 5120, 0), (20, 2048, 16384, 0)])
 def test_swiglu_grad_large(m, n, k, layout):
     w = _weight(m, n, k, False)
     rng = np.random.default_rng(m)
