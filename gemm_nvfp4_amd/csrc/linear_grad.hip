@@ -5,8 +5,9 @@
 //   * few rows: the packed weights are streamed once. dx: the reduction axis is the weight's rows, the packed axis the
 //     output's columns, so a lane takes eight rows' dwords (eight codes each) and transposes them in registers into
 //     eight B fragments, one per code position; no value crosses a lane. A block's waves share 512 rows of the weight,
-//     add their tiles in LDS in order and store one FP32 plane; a second launch adds the planes in order. Gated:
-//     the chunk products of the split-K projection (linear.hip), then a fold with the gradient's epilogue;
+//     hold them decoded while the rows of dy pass by in sixteens, add their tiles in LDS in order and store one FP32
+//     plane; a second launch adds the planes in order. Gated: the chunk products of the split-K projection
+//     (linear.hip), then a fold with the gradient's epilogue;
 //   * some hundred rows, gated: tiles on the packed weights, decoded in registers (packed_gemm.hpp), in one launch;
 //   * many rows: the weight is decoded once into the workspace (for dx transposed), exactly, as fp16, and the tiled
 //     product of tile_gemm.hpp runs on it, with the gradient in its epilogue. Where the output has too few tiles for
@@ -27,9 +28,9 @@ constexpr int FOLD_THREADS = 256;
 constexpr int ST_WAVES = 8, ST_ROWS = 64;            // waves per block, weight rows per wave
 constexpr int ST_CHUNK = ST_WAVES * ST_ROWS;         // weight rows per plane
 constexpr int ST_COLS = 128;                         // output columns per block
-constexpr int ST_MAX_M = 64;
+constexpr int FEW_ROWS = 64, ST_MAX_M = 512;  // always, and at most
 
-inline int grad_planes(int N) { return (N + ST_CHUNK - 1) / ST_CHUNK; }
+__host__ __device__ inline int grad_planes(int N) { return (N + ST_CHUNK - 1) / ST_CHUNK; }
 
 // Eight rows' dwords, and their block scales' bytes, to the fragments of the eight code positions:
 // b[c][i] = code c of row i times row i's scale.
@@ -66,27 +67,36 @@ __device__ __forceinline__ void decode_columns(f16x8 (&b)[8], const uint32_t (&c
     }
 }
 
-// Block (column group g, chunk c): plane c, columns 128 g .. + 127, of all M <= 16 MT rows. Lane (r, q) of a wave holds
-// columns 128 g + 8 r .. + 7 and, per 32-row step, weight rows 8 q .. + 7. Weight rows at or past N read as zeros (codes
-// and scales), so do dy's elements there and its rows at or past M.
-template <int MT>
-__global__ __launch_bounds__(ST_WAVES * 64) void grad_stream_kernel(const f16 *__restrict__ dy, int M,
-                                                                    const uint8_t *__restrict__ codes,
-                                                                    const uint8_t *__restrict__ scales, int N, int K,
-                                                                    float *__restrict__ part)
+// Block (column group g, chunk c): plane c, columns 128 g .. + 127, of all rows. Lane (r, q) of a wave holds columns
+// 128 g + 8 r .. + 7 and, per 32-row step, weight rows 8 q .. + 7: it decodes them once, and the rows of dy pass by in
+// sixteens. Weight rows at or past N read as zeros (codes and scales), so do dy's elements there and its rows at or past M.
+__global__ __launch_bounds__(ST_WAVES * 64, 4) void grad_stream_kernel(const f16 *__restrict__ dy, int M,
+                                                                       const uint8_t *__restrict__ codes,
+                                                                       const uint8_t *__restrict__ scales, int N, int K,
+                                                                       float *__restrict__ part)
 {
     __shared__ __attribute__((aligned(16))) float tiles[ST_WAVES][16][ST_COLS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const int groups = K / ST_COLS;
-    const int g = blockIdx.x % groups, c = blockIdx.x / groups;
+    // neighbouring columns, which share cache lines of codes and scales, go to one XCD
+    const int groups = K / ST_COLS, blocks = groups * grad_planes(N);
+    const int block = (int)(blockIdx.x & 7) * ((blocks + 7) >> 3) + (int)(blockIdx.x >> 3);
+    if (block >= blocks) return;
+    const int g = block % groups, c = block / groups;
     const int n0 = c * ST_CHUNK, rows = min(ST_CHUNK, N - n0);
     const int col = g * ST_COLS + 8 * r;
     const rsrc_t rc = make_rsrc(codes + (size_t)n0 * (K >> 1), (uint32_t)rows * (K >> 1));
     const rsrc_t rs = make_rsrc(scales + (size_t)n0 * (K >> 4), (uint32_t)rows * (K >> 4));
     const rsrc_t rd = make_rsrc(dy, (uint32_t)M * N * 2u);
     uint32_t w[2][8], sc[2][8];
-    f16x8 a[2][MT];
+    f16x8 a[2], b[2][8];
+    auto load_a = [&](int m0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = wave * ST_ROWS + h * 32 + 8 * q;
+            a[h] = __builtin_bit_cast(f16x8, bload16(rd, n < rows && m0 + r < M ? ((uint32_t)(m0 + r) * N + n0 + n) * 2u : BUF_OOB, 0));
+        }
+    };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int n = wave * ST_ROWS + h * 32 + 8 * q;
@@ -95,42 +105,33 @@ __global__ __launch_bounds__(ST_WAVES * 64) void grad_stream_kernel(const f16 *_
             w[h][i] = bload4(rc, (uint32_t)(n + i) * (K >> 1) + (col >> 1), 0);
             sc[h][i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (uint32_t)(n + i) * (K >> 4) + (col >> 4), 0, 0);
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const bool in = n < rows && 16 * m + r < M;
-            a[h][m] = __builtin_bit_cast(f16x8, bload16(rd, in ? ((uint32_t)(16 * m + r) * N + n0 + n) * 2u : BUF_OOB, 0));
-        }
     }
-    f32x4 acc[MT][8];
+    load_a(0);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[m][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        f16x8 b[8];
-        decode_columns(b, w[h], sc[h]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[m][e] = mfma_step(a[h][m], b[e], acc[m][e]);
-    }
+    for (int h = 0; h < 2; ++h) decode_columns(b[h], w[h], sc[h]);
     const int om = threadIdx.x >> 5, oc = 4 * (threadIdx.x & 31);  // 512 threads: one float4 of the 16 x 128 tile each
+#pragma unroll 1
+    for (int m0 = 0; m0 < M; m0 += 16) {
+        f32x4 acc[8];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m > 0) lds_barrier();  // the previous tile's sums have been read
+        for (int e = 0; e < 8; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = mfma_step(a[h], b[h][e], acc[e]);
+        if (m0 + 16 < M) load_a(m0 + 16);
+        if (m0 > 0) lds_barrier();  // the previous tile's sums have been read
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f32x4 *o = reinterpret_cast<f32x4 *>(&tiles[wave][4 * q + j][8 * r]);
-            o[0] = f32x4{acc[m][0][j], acc[m][1][j], acc[m][2][j], acc[m][3][j]};
-            o[1] = f32x4{acc[m][4][j], acc[m][5][j], acc[m][6][j], acc[m][7][j]};
+            o[0] = f32x4{acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
+            o[1] = f32x4{acc[4][j], acc[5][j], acc[6][j], acc[7][j]};
         }
         lds_barrier();
         f32x4 s = *reinterpret_cast<const f32x4 *>(&tiles[0][om][oc]);
 #pragma unroll
         for (int v = 1; v < ST_WAVES; ++v) s += *reinterpret_cast<const f32x4 *>(&tiles[v][om][oc]);
-        const int row = 16 * m + om;
-        if (row < M) *reinterpret_cast<f32x4 *>(part + ((size_t)c * M + row) * K + g * ST_COLS + oc) = s;
+        if (m0 + om < M) *reinterpret_cast<f32x4 *>(part + ((size_t)c * M + m0 + om) * K + g * ST_COLS + oc) = s;
     }
 }
 
@@ -409,21 +410,20 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(
 // ---- host --------------------------------------------------------------------------------------------
 // The tile shapes; their times (Shape) are measured at 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds
 // of tiles). Rounds decide at many rows: 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of
-// 256 x 256 (272 tiles on 256 CUs), 200 in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 126 with
-// 320 x 128, 143 with 128 x 128. At some hundred rows the CUs are filled by small tiles with rings of two stages,
+// 256 x 256 (272 tiles on 256 CUs), 200 in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 143 with
+// 128 x 128. At some hundred rows the CUs are filled by small tiles with rings of two stages,
 // several to a CU: 512 x 5120 outputs of 4352 rows take 60 us with 64 x 64 (88 with four stages and two blocks), 64 with
 // 128 x 64, 71 with 128 x 128.
 using T384x192 = Tile<false, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<false, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<false, 6, 4, 2, 4, 2>;
 using T192x192 = Tile<false, 3, 6, 4, 2, 2>;
-using T320x128 = Tile<false, 5, 4, 4, 2, 2>;
 using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
 using T128x64 = Tile<false, 4, 2, 2, 2, 2>;
 using T64x64 = Tile<false, 2, 2, 2, 2, 2>;
 constexpr Shape SHAPES[] = {{384, 192, 1, 1940, 1940}, {256, 256, 1, 1510, 1510}, {192, 256, 1, 1320, 1320},
-                            {192, 192, 1, 1170, 1170}, {320, 128, 1, 1390, 1390}, {128, 128, 2, 800, 450},
-                            {128, 64, 3, 600, 375},    {64, 64, 4, 530, 250}};
+                            {192, 192, 1, 1170, 1170}, {128, 128, 2, 800, 450},   {128, 64, 3, 600, 375},
+                            {64, 64, 4, 530, 250}};
 
 struct Choice {
     int shape, splits;
@@ -456,11 +456,22 @@ int with_shape(int i, F &&f)
     case 1: return f(T256x256{});
     case 2: return f(T192x256{});
     case 3: return f(T192x192{});
-    case 4: return f(T320x128{});
-    case 5: return f(T128x128{});
-    case 6: return f(T128x64{});
+    case 4: return f(T128x128{});
+    case 5: return f(T128x64{});
     default: return f(T64x64{});
     }
+}
+
+// Whether dx of M rows takes the packed weights in one stream, or decodes them for tiles. Estimates in ns fitted to
+// measurements; us by the stream and the tiles: 4352 x 5120 23 and 34 at 100 rows, 36 and 43 at 200, 43 and 46 at 256;
+// 2048 x 2048 14 and 15 at 100, 21 and 16 at 200; 512 x 8192 13 and 14 at 100, 24 and 15 at 256.
+bool grad_streams(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= FEW_ROWS) return true;
+    if (M > ST_MAX_M) return false;
+    const int64_t elements = N * K;
+    const int64_t stream = 5000 + elements / 6000 + (M + 15) / 16 * (900 + grad_planes((int)N) * K * 16 * 8 / 5000);
+    return stream < choose(M, K, N).ns + 2500 + elements / 2000;
 }
 
 // The tiles on packed weights, for the gated gradient. Times of a stage of 128 elements (of two with KS = 2, whose groups
@@ -477,7 +488,7 @@ constexpr Shape PACKED[] = {{64, 64, 2, 1200, 800}, {64, 64, 4, 920, 400}, {128,
 enum { CHUNKS = -2, DECODED = -1 };
 int swiglu_way(int64_t M, int64_t rows, int64_t K)
 {
-    if (M <= ST_MAX_M) return CHUNKS;
+    if (M <= FEW_ROWS) return CHUNKS;
     const int64_t elements = rows * K, stages = K / PACKED_STAGE;
     int way = CHUNKS;
     int64_t least = 7000 + elements / 4000 + M * (31 + num_chunks((int)K) * rows * 8 / 5000);  // the planes, there and back
@@ -515,7 +526,7 @@ int launch_swiglu_fold(const float *part, int S, int M, int I, const nvfp4_weigh
 
 size_t linear_grad_ws_bytes(int32_t M, int32_t N, int32_t K)
 {
-    if (M <= ST_MAX_M) return up256((size_t)grad_planes(N) * M * K * sizeof(float));
+    if (grad_streams(M, N, K)) return up256((size_t)grad_planes(N) * M * K * sizeof(float));
     const Choice c = choose(M, K, N);
     const size_t planes = c.splits > 1 ? (size_t)c.splits * M * K * sizeof(float) : 0;
     return up256((size_t)K * padded(N) * 2) + up256(planes);
@@ -531,14 +542,11 @@ int run_linear_grad(const uint16_t *dy, int32_t M, const nvfp4_weights &w, uint1
         return launch(grad_fold_kernel, dim3((unsigned)((plane / 4 + FOLD_THREADS - 1) / FOLD_THREADS)), dim3(FOLD_THREADS), 0, s,
                       part, S, plane, w.global_scale, o);
     };
-    if (M <= ST_MAX_M) {
+    if (grad_streams(M, N, K)) {
         float *part = static_cast<float *>(ws);
         const int S = grad_planes(N);
-        const int mt = (M + 15) / 16;
-        auto *kernel = mt == 1 ? grad_stream_kernel<1> : mt == 2 ? grad_stream_kernel<2> : mt == 3 ? grad_stream_kernel<3>
-                                                                                                  : grad_stream_kernel<4>;
-        const int st = launch(kernel, dim3((unsigned)(K / ST_COLS * S)), dim3(ST_WAVES * 64), 0, s, d, M, w.codes, w.scales, N, K,
-                              part);
+        const int st = launch(grad_stream_kernel, dim3(tile_grid((int64_t)K / ST_COLS * S)), dim3(ST_WAVES * 64), 0, s, d, M,
+                              w.codes, w.scales, N, K, part);
         return st != NVFP4_OK ? st : fold(part, S);
     }
     const int ld = padded(N);

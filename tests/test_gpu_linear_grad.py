@@ -21,7 +21,8 @@ pytestmark = pytest.mark.gpu
 HALF, TINY, ADD = 2.0 ** -11, 2.0 ** -25, 2.0 ** -23
 E2M1 = np.array([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6])
 
-# batch sizes on both sides of every change of kernel: 16-row tiles of the stream up to 64 rows, then decoded weights
+# batch sizes on both sides of every change of kernel: sixteens of rows pass by the stream, always up to 64; with more rows
+# large weights stream too, small ones are decoded for tiles
 BATCHES = [1, 2, 15, 16, 17, 33, 48, 49, 64, 65, 127, 130, 300]
 
 
@@ -84,8 +85,11 @@ def _check_grad(dx, dy, w):
     assert np.all(err <= (HALF + 2.0 ** -20) * np.abs(ref) + TINY + (dy.shape[1] + 2) * ADD * size)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 4352, 5120), (24, 4352, 5120), (64, 80, 5120), (100, 1040, 1152), (333, 2064, 2176),
-                                   (1000, 4352, 896), (4096, 1040, 5120)])
+@pytest.mark.parametrize("m,n,k", [(1, 4352, 5120), (24, 4352, 5120), (64, 80, 5120), (100, 1040, 1152), (150, 4352, 5120),
+                                   (250, 4368, 4992), (333, 2064, 2176), (1000, 4352, 896), (4096, 1040, 5120),
+                                   # one size for each shape of the tiles
+                                   (500, 1040, 2048), (981, 1040, 2176), (907, 1040, 4352), (1573, 1040, 5120),
+                                   (1055, 1040, 8192), (5384, 1040, 2176), (3201, 1040, 5120)])
 def test_grad_random(m, n, k):
     w = _weight(m, n, k, False)
     dy = np.random.default_rng(m).standard_normal((m, n)).astype(np.float16)
@@ -161,7 +165,9 @@ def test_swiglu_grad(m, n, k, layout):
 # and an odd number of stages; then decoded weights and chunk products
 @pytest.mark.parametrize("m,n,k,layout", [(333, 4352, 5120, 1), (397, 4384, 1152, 0), (500, 4352, 896, 1), (1500, 4384, 640, 0),
                                           (1000, 4384, 5120, 0), (1100, 4352, 4992, 1), (2100, 4352, 1152, 0),
-                                          (4100, 2080, 896, 1), (2500, 4352, 5120, 0), (20, 2048, 16384, 0)])
+                                          (4100, 2080, 896, 1), (2500, 4352, 5120, 0), (2017, 2080, 1152, 0),
+                                          (1055, 8192, 1152, 1), (5384, 2080, 1152, 1), (7715, 2080, 128, 0),
+                                          (20, 2048, 16384, 0)])
 def test_swiglu_grad_large(m, n, k, layout):
     w = _weight(m, n, k, False)
     rng = np.random.default_rng(m)
