@@ -70,6 +70,10 @@ __device__ __forceinline__ void decode_columns(f16x8 (&b)[8], const uint32_t (&c
 // Block (column group g, chunk c): plane c, columns 128 g .. + 127, of all rows. Lane (r, q) of a wave holds columns
 // 128 g + 8 r .. + 7 and, per 32-row step, weight rows 8 q .. + 7: it decodes them once, and the rows of dy pass by in
 // sixteens. Weight rows at or past N read as zeros (codes and scales), so do dy's elements there and its rows at or past M.
+// 24 rows of 4352 x 5120: 8.9 us and 1.8 for the fold (10.7 a call). What bounds it: 4-byte loads of 64-byte pieces of the rows,
+// whose lines and whose scales' lines the neighbouring columns' blocks share, so that neighbours on different XCDs cost
+// 10 to 30% (8192 x 8192, 24 rows: 24.8 us dealt out in turn, 20.0 with neighbours on one XCD); from 48 rows on the
+// planes, 1.2 us for 16 rows.
 __global__ __launch_bounds__(ST_WAVES * 64, 4) void grad_stream_kernel(const f16 *__restrict__ dy, int M,
                                                                        const uint8_t *__restrict__ codes,
                                                                        const uint8_t *__restrict__ scales, int N, int K,
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(256) void decode_transposed_kernel(const uint8_t *_
     for (int c = 0; c < 8; ++c) *reinterpret_cast<f16x8 *>(wt + (size_t)(k + c) * ld + n) = b[c];
 }
 
-// w [N][K] to fp16 in the same order, eight elements per thread.
+// w [N][K] to fp16 in the same order, eight elements per thread. 4352 x 5120: 12.0 us (57 MB, 4.7 TB/s).
 __global__ __launch_bounds__(256) void decode_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                      size_t eights, f16 *__restrict__ w)
 {
@@ -244,7 +248,8 @@ __global__ __launch_bounds__(256) void decode_kernel(const uint8_t *__restrict__
     reinterpret_cast<f16x8 *>(w)[i] = decode8(reinterpret_cast<const uint32_t *>(codes)[i], s);
 }
 
-// A [M][red] times B [cols][ld] over all stages or one of `splits` runs of them. PLANE: FP32 sums to plane
+// A [M][red] times B [cols][ld] over all stages or one of `splits` runs of them. 4096 x 2176 outputs of 5120: 87 us in the
+// steady state, 99 traced (920 to 1050 TFLOP/s; 198 tiles on 256 CUs). PLANE: FP32 sums to plane
 // blockIdx.y of `out`; else fp16(global * sum).
 template <class T, bool PLANE>
 __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__restrict__ a, int M, int red,
@@ -298,7 +303,8 @@ __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__r
 
 // x [M][K] times the decoded gate and up rows, and the gradient of SwiGLU on them. Even tiles of a wave hold gate
 // rows and odd ones the up rows of the same i, so that a lane has both: staged row 16 t + 4 q + j of wave column w
-// is pair i0 + 8 NT w + 2 NT q + 4 (t / 2) + j, gate (t even) or up. Each load brings rows of one 16-row tile, and a
+// is pair i0 + 8 NT w + 2 NT q + 4 (t / 2) + j, gate (t even) or up. 4096 rows of 4352 x 5120: 152 us behind the decoding
+// (1200 TFLOP/s, 253 tiles in one round). Each load brings rows of one 16-row tile, and a
 // wave's loads are all gates or all ups (the waves number a multiple of four).
 template <class T>
 __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f16 *__restrict__ x, int M, int K,
@@ -335,16 +341,19 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
     f32x4 acc[T::MT][T::NT];
     tile_product<T>(smem, p, ra, rb, 0, K / 64, STAGE_BYTES, acc);
     const float gs = gscale[0];
+    const int pair0 = i0 + p.wn * 8 * T::NT + 2 * T::NT * p.q;
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
         const int row = m0 + (p.wm * T::MT + m) * 16 + p.r;
+        f16x4 d[T::NT / 2];  // a row's loads at once
+#pragma unroll
+        for (int t = 0; t < T::NT; t += 2)
+            d[t / 2] = *reinterpret_cast<const f16x4 *>(dh + (size_t)min(row, M - 1) * I + min(pair0 + 2 * t, I - 4));
         if (row >= M) continue;
 #pragma unroll
         for (int t = 0; t < T::NT; t += 2) {
-            const int i = i0 + p.wn * 8 * T::NT + 2 * T::NT * p.q + 2 * t;
-            if (i >= I) continue;
-            const f16x4 d = *reinterpret_cast<const f16x4 *>(dh + (size_t)row * I + i);
-            store_dz(dz, row, I, i, layout, acc[m][t], acc[m][t + 1], gs, d);
+            const int i = pair0 + 2 * t;
+            if (i < I) store_dz(dz, row, I, i, layout, acc[m][t], acc[m][t + 1], gs, d[t / 2]);
         }
     }
 }
@@ -383,11 +392,15 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(
     if (i >= I) return;
     typedef _Float16 pairs_t __attribute__((ext_vector_type(NP)));
     typedef _Float16 both_t __attribute__((ext_vector_type(2 * NP)));
+    pairs_t dhs[T::MT];
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m)
+        dhs[m] = *reinterpret_cast<const pairs_t *>(dh + (size_t)min(m0 + 16 * m + p.r, M - 1) * I + i);
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
         const int row = m0 + 16 * m + p.r;
         if (row >= M) continue;
-        const pairs_t d = *reinterpret_cast<const pairs_t *>(dh + (size_t)row * I + i);
+        const pairs_t d = dhs[m];
         pairs_t g, u;
         both_t z;
 #pragma unroll
@@ -411,19 +424,19 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(
 // The tile shapes; their times (Shape) are measured at 4352 x 5120 and 5120 x 2176 (1.0 to 1.35 PFLOP/s in whole rounds
 // of tiles). Rounds decide at many rows: 4096 x 4352 outputs take 167 us in the one round of 384 x 192, 254 in the two of
 // 256 x 256 (272 tiles on 256 CUs), 200 in the two of 192 x 192; 4096 x 2176 outputs 116 us with 192 x 256, 143 with
-// 128 x 128. At some hundred rows the CUs are filled by small tiles with rings of two stages,
-// several to a CU: 512 x 5120 outputs of 4352 rows take 60 us with 64 x 64 (88 with four stages and two blocks), 64 with
-// 128 x 64, 71 with 128 x 128.
+// 128 x 128. At some hundred rows small tiles fill the CUs: 333 x 5120 outputs of 4352 rows take 42 us with 64 x 64, 56 with
+// 128 x 128. Three stages where a CU holds two blocks of them, two of 128 x 128 where its tiles are
+// more than the CUs (1000 x 5120: 83 us, 102 with three stages and one block to a CU; 512 x 5120: 66 against 58).
 using T384x192 = Tile<false, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<false, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<false, 6, 4, 2, 4, 2>;
 using T192x192 = Tile<false, 3, 6, 4, 2, 2>;
 using T128x128 = Tile<false, 4, 4, 2, 2, 2>;
-using T128x64 = Tile<false, 4, 2, 2, 2, 2>;
-using T64x64 = Tile<false, 2, 2, 2, 2, 2>;
+using D128x128 = Tile<false, 4, 4, 2, 2, 3>;
+using T64x64 = Tile<false, 2, 2, 2, 2, 3>;
 constexpr Shape SHAPES[] = {{384, 192, 1, 1940, 1940}, {256, 256, 1, 1510, 1510}, {192, 256, 1, 1320, 1320},
-                            {192, 192, 1, 1170, 1170}, {128, 128, 2, 800, 450},   {128, 64, 3, 600, 375},
-                            {64, 64, 4, 530, 250}};
+                            {192, 192, 1, 1170, 1170}, {128, 128, 2, 800, 470},   {128, 128, 1, 690, 690},
+                            {64, 64, 3, 345, 225}};
 
 struct Choice {
     int shape, splits;
@@ -457,14 +470,14 @@ int with_shape(int i, F &&f)
     case 2: return f(T192x256{});
     case 3: return f(T192x192{});
     case 4: return f(T128x128{});
-    case 5: return f(T128x64{});
+    case 5: return f(D128x128{});
     default: return f(T64x64{});
     }
 }
 
 // Whether dx of M rows takes the packed weights in one stream, or decodes them for tiles. Estimates in ns fitted to
-// measurements; us by the stream and the tiles: 4352 x 5120 23 and 34 at 100 rows, 36 and 43 at 200, 43 and 46 at 256;
-// 2048 x 2048 14 and 15 at 100, 21 and 16 at 200; 512 x 8192 13 and 14 at 100, 24 and 15 at 256.
+// measurements; us by the stream and the tiles: 4352 x 5120 23 and 31 at 100 rows, 36 and 38 at 200, 43 and 40 at 256;
+// 2048 x 2048 14 and 14 at 100, 21 and 15 at 200; 512 x 8192 13 and 13 at 100, 24 and 14 at 256.
 bool grad_streams(int64_t M, int64_t N, int64_t K)
 {
     if (M <= FEW_ROWS) return true;
@@ -479,12 +492,12 @@ bool grad_streams(int64_t M, int64_t N, int64_t K)
 using P64x64x2 = PackedTile<4, 1, 4, 2, 4>;
 using P64x64 = PackedTile<4, 1, 4, 1, 4>;
 using P128x128 = PackedTile<8, 2, 4, 1, 2>;
-constexpr Shape PACKED[] = {{64, 64, 2, 1200, 800}, {64, 64, 4, 920, 400}, {128, 128, 2, 1700, 1000}};
+constexpr Shape PACKED[] = {{64, 64, 2, 1050, 800}, {64, 64, 4, 820, 400}, {128, 128, 2, 1450, 925}};
 
 // How the gated gradient of M rows is computed: by the chunk products of linear.hip in passes of 64 rows and their fold
 // (CHUNKS), in tiles on the packed weights (the number of the shape), or in tiles on decoded ones (DECODED). Estimates in
-// ns fitted to measurements; 4352 x 5120, us by the three: 128 rows 22, 30, 41; 333 rows 48, 35, 53; 512 rows 71, 47, 61;
-// 1000 rows 138, 79, 88; 1900 rows packed 90, 2000 rows 121 decoded; 4096 rows 215 packed, 166 decoded.
+// ns fitted to measurements; 4352 x 5120, us by the three: 128 rows 23, 24, 34; 333 rows 55, 35, 46; 512 rows 81, 50, 61;
+// 1000 rows 74 packed, 89 decoded; 1900 rows packed 88, 2000 rows 121 decoded; 4096 rows 215 packed, 166 decoded.
 enum { CHUNKS = -2, DECODED = -1 };
 int swiglu_way(int64_t M, int64_t rows, int64_t K)
 {

@@ -3,7 +3,13 @@
 //
 // One reduction order at every batch size: a single chain of 128-element MFMA steps from +0, in the order of the
 // reduction axis. Few rows stream the weights once: a block for every 16 columns, whose waves hold the whole axis in
-// flight and hand the chain on from one to the next. More rows take the tiled product of tile_gemm.hpp, whose shape the batch chooses.
+// flight and hand the chain on from one to the next. More rows take the tiled product of tile_gemm.hpp, whose shape the
+// batch chooses.
+//
+// Measured at 4352 x 5120: one row 9.4 us (2.4 TB/s of 22.3 MB: 82 KB a block at what a CU has in flight, start-up, and
+// 1.2 us of the chain's hand-overs), 13 rows 10.4, 333 rows 19.6 (760 TFLOP/s), 8192 rows 167 (2.2 PFLOP/s; the library's
+// product of 8192^3 reaches 2.27). Sums in 512-element chunks, each closed by FP32 additions, reached 1.75 to 2.1 PFLOP/s
+// where the one chain reaches 2.3 to 2.65 in whole rounds.
 #include "dense.hpp"
 #include "nvfp4_device.hpp"
 #include "tile_gemm.hpp"
@@ -13,12 +19,20 @@ namespace {
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int ROWS_STREAM_M = 64;  // most rows of the streaming kernel
+constexpr int ROWS_STREAM_M = 32;  // most rows of the streaming kernel
 constexpr int ROWS_GROUP = 5;  // steps whose operands a wave holds at once
 
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b)
 {
     return __builtin_shufflevector(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Four neighbouring scales, which are 4-byte aligned.
+__device__ __forceinline__ f32x4 load_scales(const float *p)
+{
+    f32x4 v;
+    __builtin_memcpy(&v, p, sizeof(v));
+    return v;
 }
 
 // Block b: columns 16 b .. + 15 of all M <= 16 MT rows. The waves share the steps in groups of ROWS_GROUP, in turn. All
@@ -79,6 +93,7 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void rows_stream_kernel(const
         }
     }
     // lane (r, q) of row tile m: columns 4 q .. 4 q + 3 of row r; a wave a row tile
+    const f32x4 sc = load_scales(cs + n0 + 4 * q);
     for (int m = wave; m < MT; m += waves) {
         const int row = 16 * m + r;
         if (row >= M) continue;
@@ -86,7 +101,7 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void rows_stream_kernel(const
         const float sx = xs[row];
         f16x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = f16_of_f32((sx * cs[n0 + 4 * q + e]) * acc[e]);
+        for (int e = 0; e < 4; ++e) o[e] = f16_of_f32((sx * sc[e]) * acc[e]);
         *reinterpret_cast<f16x4 *>(y + (size_t)row * N + n0 + 4 * q) = o;
     }
 }
@@ -119,49 +134,62 @@ __global__ __launch_bounds__(T::WAVES * 64) void rows_tile_kernel(const uint8_t 
     }
     f32x4 acc[T::MT][T::NT];
     tile_product<T>(smem, p, ra, rb, 0, K / STAGE_BYTES, STAGE_BYTES, acc);
+    // all scales at once: asked for one by one between the stores, each waited for its own way to memory and back
+    const int row0 = m0 + p.wm * T::MT * 16 + p.r, col0 = c0 + p.wn * 16 * T::NT + 4 * T::NT * p.q;
+    f32x4 sc[T::NT];
+    float sx[T::MT];
+#pragma unroll
+    for (int t = 0; t < T::NT; ++t) sc[t] = load_scales(cs + min(col0 + 4 * t, N - 4));
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m) sx[m] = xs[min(row0 + 16 * m, M - 1)];
 #pragma unroll
     for (int m = 0; m < T::MT; ++m) {
-        const int row = m0 + (p.wm * T::MT + m) * 16 + p.r;
+        const int row = row0 + 16 * m;
         if (row >= M) continue;
-        const float sx = xs[row];
 #pragma unroll
         for (int t = 0; t < T::NT; ++t) {
-            const int c = c0 + p.wn * 16 * T::NT + 4 * T::NT * p.q + 4 * t;
+            const int c = col0 + 4 * t;
             if (c >= N) continue;
             f16x4 o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = f16_of_f32((sx * cs[c + e]) * acc[m][t][e]);
+            for (int e = 0; e < 4; ++e) o[e] = f16_of_f32((sx[m] * sc[t][e]) * acc[m][t][e]);
             *reinterpret_cast<f16x4 *>(y + (size_t)row * N + c) = o;
         }
     }
 }
 
-// Up to 16 rows always stream. Up to 64 the stream wins where the reduction axis is long, which it has in flight at
-// once and the tiles walk: 48 rows of 2048 x 8192 take 19.5 us against 26, 64 of 1024 x 16384 41 against 50; of a shorter
-// one the tiles win: 32 rows of 2048 x 2048 take 5.8 us against 6.6, 48 of 4352 x 5120 18 against 25. The two meet
-// near 170 elements a row (5120 elements: 24 rows 16.9 against 17.5 us, 32 rows 18.5 against 17.6).
-bool use_stream(int M, int K) { return M <= 16 || (M <= ROWS_STREAM_M && K >= 170 * M); }
+// The stream has the whole reduction axis in flight, which the tiles walk, but a block for every 16 columns, so it wins at
+// few rows where the blocks have a CU each, us by the stream and in tiles: 2048 x 8192 8.4 and 14.5 at one row, 11.2 and
+// 14.7 at 16, 15.0 and 15.0 at 32; 2048 x 2048 4.0 and 5.4 at one row, 4.9 and 5.6 at 16, 6.0 and 5.6 at 24. With more
+// blocks than CUs it holds at a few rows for a while: 4352 x 5120 9.4 and 10.3 at one, 10.4 and 10.4 at 8, 11.9 and 10.5
+// at 16; 8192 x 8192 16.8 and 15.8 at one.
+bool use_stream(int M, int N, int K)
+{
+    if (N <= 16 * TILE_CUS) return M <= 16 || (M <= ROWS_STREAM_M && K >= 4096);
+    return M <= 4 && N <= 20 * TILE_CUS;
+}
 
 // The tile shapes; their times (Shape) are measured at 40 stages (K = 5120). The shape of the least estimated time is
-// taken. Many tiles: whole rounds over the CUs decide, at 1.0 to 2.65 PFLOP/s; 8192 x 4352 outputs of K = 5120 take 174 us
+// taken. Many tiles: whole rounds over the CUs decide, at 1.0 to 2.65 PFLOP/s; 8192 x 4352 outputs of K = 5120 take 167 us
 // in the two rounds of 384 x 192, 216 in the four of 192 x 256. What bounds the large shapes is the way from the
 // L2s into LDS (64 KB a stage for 256 x 256, 12 to 15 TB/s over the chip) and the matrix pipes, each a little
-// more than half busy. Few tiles: a block alone on its CU waits for its own loads, of which a CU keeps only so many in
-// flight (a ring of 9 stages is no faster than one of 3), so small tiles on all CUs win: 128 x 4352 outputs
-// take 18.8 us with 32 x 32, 20.6 with 64 x 32, 22.7 with 64 x 64; and shallow rings, of which a CU holds more blocks: 512 x 4352
-// outputs take 28.2 us with four blocks of 64 x 64 and two stages to a CU, 44 with two of five stages.
+// more than half busy. Few tiles: the fewer bytes a CU has to bring in, the better, so small tiles on all CUs win, with
+// rings as deep as two or more blocks to a CU allow: 64 x 4352 outputs take 11.4 us with 32 x 32 and five stages, 12.5 with
+// 64 x 32 and three (20.2 with two), 14.9 with 64 x 64 and three (22.5 with two); 333 x 4352 take 19.6 with 64 x 64, 25.7
+// with 64 x 32, 26.6 with 32 x 32. 128 x 128 comes with two stages and two blocks to a CU, and with three and one: 1000 x 4352
+// 36.1 and 56.2, 512 x 8192 of K = 8192 61.1 and 46.8.
 using T384x192 = Tile<true, 6, 6, 4, 2, 2>;
 using T256x256 = Tile<true, 8, 4, 2, 4, 2>;
 using T192x256 = Tile<true, 6, 4, 2, 4, 2>;
-using T192x192 = Tile<true, 6, 3, 2, 4, 2>;
+using T192x192 = Tile<true, 6, 3, 2, 4, 3>;
 using T128x128 = Tile<true, 4, 4, 2, 2, 2>;
-using T64x128 = Tile<true, 2, 4, 2, 2, 3>;
-using T64x64 = Tile<true, 2, 2, 2, 2, 2>;
-using T64x32 = Tile<true, 2, 1, 2, 2, 2>;
-using T32x32 = Tile<true, 1, 1, 2, 2, 3>;
+using D128x128 = Tile<true, 4, 4, 2, 2, 3>;
+using T64x64 = Tile<true, 2, 2, 2, 2, 3>;
+using T64x32 = Tile<true, 2, 1, 2, 2, 3>;
+using T32x32 = Tile<true, 1, 1, 2, 2, 5>;
 constexpr Shape SHAPES[] = {{384, 192, 1, 1950, 1950}, {256, 256, 1, 1620, 1620}, {192, 256, 1, 1300, 1300},
-                            {192, 192, 1, 1070, 1070}, {128, 128, 2, 770, 500},   {64, 128, 2, 600, 355},
-                            {64, 64, 4, 480, 235},     {64, 32, 6, 435, 150},     {32, 32, 6, 385, 105}};
+                            {192, 192, 1, 1075, 1075}, {128, 128, 2, 780, 450},   {128, 128, 1, 640, 640},
+                            {64, 64, 3, 300, 215},     {64, 32, 4, 230, 135},     {32, 32, 4, 190, 103}};
 
 template <class F>
 int with_shape(int i, F &&f)
@@ -172,7 +200,7 @@ int with_shape(int i, F &&f)
     case 2: return f(T192x256{});
     case 3: return f(T192x192{});
     case 4: return f(T128x128{});
-    case 5: return f(T64x128{});
+    case 5: return f(D128x128{});
     case 6: return f(T64x64{});
     case 7: return f(T64x32{});
     default: return f(T32x32{});
@@ -186,11 +214,9 @@ int run_linear_fp8_rows(const uint8_t *xq, const float *xs, int32_t M, const fp8
 {
     const int N = w.rows, K = w.k;
     f16 *o = reinterpret_cast<f16 *>(y);
-    if (use_stream(M, K)) {
+    if (use_stream(M, N, K)) {
         const int groups = (K / STAGE_BYTES + ROWS_GROUP - 1) / ROWS_GROUP, most = M <= 16 ? 16 : 8;
-        const int mt = (M + 15) / 16;
-        auto *kernel = mt == 1 ? rows_stream_kernel<1> : mt == 2 ? rows_stream_kernel<2> : mt == 3 ? rows_stream_kernel<3>
-                                                                                                  : rows_stream_kernel<4>;
+        auto *kernel = M <= 16 ? rows_stream_kernel<1> : rows_stream_kernel<2>;
         return launch(kernel, dim3((unsigned)(N / 16)), dim3((unsigned)(64 * (groups < most ? groups : most))), 0, s, xq, xs, M,
                       w.codes, w.channel_scale, N, K, o);
     }

@@ -4,10 +4,11 @@
 //
 // A block owns BM x BN outputs; its waves stand side by side along B, a wave has MT x NT tiles of 16 x 16. The
 // reduction axis is walked in stages of 128 elements:
-//   * A's rows, 256 bytes each, come into LDS by direct-to-LDS loads a stage ahead, with one block barrier a stage. A
-//     row's sixteen 16-byte units are XOR-ed with the row's number modulo 16, in the lane's global address, so that the
-//     16 lanes of a fragment read fall on the 16 units of 256 bytes;
-//   * each wave loads its own codes a stage ahead, 16 bytes a lane and tile: lane group q owns elements 32 q .. + 31 of
+//   * A's rows, 256 bytes each, come into LDS by direct-to-LDS loads a stage ahead, one block barrier a stage. A
+//     row's sixteen 16-byte units are XOR-ed with row_key(row), in the lane's global address. A 16-byte read serves 16 lanes
+//     at a time, rows 0..3 and 12..15 of one lane group with rows 4..11 of the next and so on: the key's upper bits
+//     make those fall on the 16 units of 256 bytes too (the row's number itself gave conflicts in half of the cycles);
+//   * each wave loads its own codes two stages ahead, 16 bytes a lane and tile: lane group q owns elements 32 q .. + 31 of
 //     the stage, MFMA step d takes elements 32 q + 8 d .. + 7 of them, and A's fragment of that step is unit 4 q + d of
 //     the row. A step's weights are decoded while the products of the step before run.
 // KS wave groups of a block share the reduction axis in runs of stages, and the first group adds the others' sums in
@@ -22,6 +23,13 @@
 namespace nvfp4 {
 
 constexpr int PACKED_STAGE = 128;  // elements
+
+// Rows 4 b .. + 3 of sixteen take 4 (0, 2, 3, 1)[b] + 0..3.
+__device__ __forceinline__ int row_key(int row)
+{
+    const int b = (row >> 2) & 3;
+    return ((b ^ b >> 1) & 1) << 3 | (b >> 1) << 2 | (row & 3);
+}
 
 template <int MT_, int NT_, int WN_, int KS_, int OCC_>
 struct PackedTile {
@@ -64,62 +72,73 @@ __device__ __forceinline__ bool packed_product(unsigned char *smem_all, const Pa
     const int stages = K / PACKED_STAGE, per = (stages + T::KS - 1) / T::KS;
     const int first = min(stages, p.group * per), last = min(stages, first + per);
     unsigned char *const smem = smem_all + p.group * 2 * T::BYTES;
-    const rsrc_t buf = make_rsrc(a, (uint32_t)rows * K * 2u);
+    const rsrc_t from = make_rsrc(a, (uint32_t)rows * K * 2u);
     const int row0 = 4 * p.wave + (p.lane >> 4);  // load i of a wave: rows 4 (wave + WN i) .. + 3, whole sixteens apart
     uint32_t off[T::LA];
 #pragma unroll
     for (int i = 0; i < T::LA; ++i) {
         const int row = row0 + 4 * T::WN * i;
-        off[i] = row < rows ? (uint32_t)row * K * 2u + 16u * ((p.lane & 15) ^ (row0 & 15)) : BUF_OOB;
+        off[i] = row < rows ? (uint32_t)row * K * 2u + 16u * ((p.lane & 15) ^ row_key(row0)) : BUF_OOB;
     }
-    auto load_a = [&](int k) {
-        unsigned char *to = smem + ((k - first) & 1) * T::BYTES + p.wave * 1024;
+    auto load_a = [&](int k, int buf) {
+        unsigned char *to = smem + buf * T::BYTES + p.wave * 1024;
 #pragma unroll
-        for (int i = 0; i < T::LA; ++i) load_to_lds(buf, to + T::WN * i * 1024, off[i], (uint32_t)k * ROW);
+        for (int i = 0; i < T::LA; ++i) load_to_lds(from, to + T::WN * i * 1024, off[i], (uint32_t)k * ROW);
     };
-    u32x4 codes[NT];
-    uint16_t scales[NT];
-    auto load_b = [&](int k) {
+    u32x4 codes[2][NT];
+    uint16_t scales[2][NT];
+    auto load_b = [&](int k, int set) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            codes[t] = *reinterpret_cast<const u32x4 *>(b.codes[t] + (size_t)k * (PACKED_STAGE / 2));
-            scales[t] = *reinterpret_cast<const uint16_t *>(b.scales[t] + (size_t)k * (PACKED_STAGE / 16));
+            codes[set][t] = *reinterpret_cast<const u32x4 *>(b.codes[t] + (size_t)k * (PACKED_STAGE / 2));
+            scales[set][t] = *reinterpret_cast<const uint16_t *>(b.scales[t] + (size_t)k * (PACKED_STAGE / 16));
         }
     };
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (first < last) load_b(first), load_a(first);
+    // In the steady state a stage asks for A of the next and, three scheduling barriers later, for the weights of the one
+    // after, 2 NT loads, which the next stage's start leaves in flight. The first stage and the last wait for all.
+    if (first < last) load_b(first, 0), load_a(first, 0), load_b(min(first + 1, last - 1), 1);
+    int buf = 0;
     const int a0 = p.r * ROW;
     int unit[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) unit[d] = a0 + 16 * ((4 * p.q + d) ^ p.r);
-    for (int k = first; k < first + per; ++k) {  // every group passes every barrier
-        wait_loads<0>();  // this wave's part of stage k
-        lds_barrier();    // everyone's part, and everyone is done with the other buffer
-        if (k >= last) continue;
-        const unsigned char *const at = smem + ((k - first) & 1) * T::BYTES;
-        f16x8 af[4][MT], bf[2][NT];
+    for (int d = 0; d < 4; ++d) unit[d] = a0 + 16 * ((4 * p.q + d) ^ row_key(p.r));
+    for (int k0 = first; k0 < first + per; k0 += 2) {  // every group passes every barrier
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+        for (int set = 0; set < 2; ++set) {
+            const int k = k0 + set;
+            if (k >= first + per) break;
+            // this wave's part of stage k, and its weights
+            if (k > first && k + 1 < last) wait_loads<2 * NT>();
+            else wait_loads<0>();
+            stage_barrier();  // everyone's part, and everyone is done with the buffer that is filled next
+            if (k >= last) continue;
+            const unsigned char *const at = smem + buf * T::BYTES;
+            f16x8 af[4][MT], bf[2][NT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) af[d][m] = *reinterpret_cast<const f16x8 *>(at + unit[d] + m * 16 * ROW);
-        if (k + 1 < last) load_a(k + 1);
-        auto decode = [&](int d) {
+            for (int d = 0; d < 4; ++d)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) bf[d & 1][t] = decode8(codes[t][d], e4m3_pair<false>(scales[t])[d >> 1]);
-        };
-        decode(0);
+                for (int m = 0; m < MT; ++m) af[d][m] = *reinterpret_cast<const f16x8 *>(at + unit[d] + m * 16 * ROW);
+            if (k + 1 < last) load_a(k + 1, buf ^ 1);
+            buf ^= 1;
+            auto decode = [&](int d) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            if (d < 3) decode(d + 1);
-            else if (k + 1 < last) load_b(k + 1);
+                for (int t = 0; t < NT; ++t) bf[d & 1][t] = decode8(codes[set][t][d], e4m3_pair<false>(scales[set][t])[d >> 1]);
+            };
+            decode(0);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int d = 0; d < 4; ++d) {
+                if (d < 3) decode(d + 1);
+                else load_b(min(k + 2, last - 1), set);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[m][t] = mfma_step(bf[d & 1][t], af[d][m], acc[m][t]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[m][t] = mfma_step(bf[d & 1][t], af[d][m], acc[m][t]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
     if constexpr (T::KS > 1) {

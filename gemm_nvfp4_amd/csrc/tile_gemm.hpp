@@ -49,6 +49,13 @@ __device__ __forceinline__ void wait_loads()
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Block barrier between stages: this wave's LDS reads are done, its loads into LDS stay in flight (a release fence would
+// wait for them all, which made every ring one stage deep); wait_loads() in front says which of them have to be there.
+__device__ __forceinline__ void stage_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // 16 bytes a lane from a buffer to LDS: lane i's bytes land at `to` + 16 i. Offsets past the buffer give zeros.
 __device__ __forceinline__ void load_to_lds(rsrc_t from, unsigned char *to, uint32_t voff, uint32_t soff)
 {
@@ -204,7 +211,7 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
         // stage k has landed: at most the NS - 2 stages behind it are still in flight
         if (NS > 2 && k + NS - 2 < last) wait_loads<(NS - 2) * (T::LA + T::LB)>();
         else wait_loads<0>();
-        lds_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
+        stage_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
         if (k + NS - 1 < last) load(k + NS - 1, buf == 0 ? NS - 1 : buf - 1);
         const unsigned char *at = smem + buf * T::BYTES;
         stage_products<T>(at, at + T::BM * STAGE_BYTES, p, acc);

@@ -12,7 +12,7 @@ import gemm_nvfp4_amd as G
 
 pytestmark = pytest.mark.gpu
 
-# batch sizes on both sides of every change of kernel: up to 16 rows stream, up to 64 where K >= 170 rows, more take tiles
+# batch sizes on both sides of every change of kernel: few rows of few columns stream, up to 16 or 32, more take tiles
 BATCHES = [1, 2, 15, 16, 17, 32, 33, 64, 65, 130, 333]
 
 

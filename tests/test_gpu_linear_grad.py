@@ -87,9 +87,10 @@ def _check_grad(dx, dy, w):
 
 @pytest.mark.parametrize("m,n,k", [(1, 4352, 5120), (24, 4352, 5120), (64, 80, 5120), (100, 1040, 1152), (150, 4352, 5120),
                                    (250, 4368, 4992), (333, 2064, 2176), (1000, 4352, 896), (4096, 1040, 5120),
-                                   # one size for each shape of the tiles
-                                   (500, 1040, 2048), (981, 1040, 2176), (907, 1040, 4352), (1573, 1040, 5120),
-                                   (1055, 1040, 8192), (5384, 1040, 2176), (3201, 1040, 5120)])
+                                   # a size for each shape of the tiles; a short last stage, and runs of stages
+                                   (500, 1040, 2048), (532, 32, 6656), (907, 1040, 4352), (388, 32, 7040), (1030, 96, 7296),
+                                   (1159, 32, 7040), (1055, 1040, 8192), (1580, 32, 7296), (2061, 32, 7808),
+                                   (3201, 1040, 5120), (289, 6464, 8064), (588, 6368, 6784)])
 def test_grad_random(m, n, k):
     w = _weight(m, n, k, False)
     dy = np.random.default_rng(m).standard_normal((m, n)).astype(np.float16)
@@ -167,6 +168,8 @@ def test_swiglu_grad(m, n, k, layout):
                                           (1000, 4384, 5120, 0), (1100, 4352, 4992, 1), (2100, 4352, 1152, 0),
                                           (4100, 2080, 896, 1), (2500, 4352, 5120, 0), (2017, 2080, 1152, 0),
                                           (1055, 8192, 1152, 1), (5384, 2080, 1152, 1), (7715, 2080, 128, 0),
+                                          (71, 32, 1664, 1), (3474, 864, 128, 0), (770, 1280, 6912, 1), (988, 2144, 7424, 0),
+                                          (1155, 7136, 128, 1), (1428, 5504, 128, 0), (2060, 7712, 256, 1),
                                           (20, 2048, 16384, 0)])
 def test_swiglu_grad_large(m, n, k, layout):
     w = _weight(m, n, k, False)
@@ -298,4 +301,19 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for r, g in zip(ref, got):
         for t in g:
+            assert torch.equal(t.view(torch.int16), r.view(torch.int16))
+
+
+def test_two_streams_at_once_gated():
+    """Packed tiles of both kinds and decoded ones on two streams, each with a workspace of its own."""
+    n, k = 1056, 640
+    w = G.NVFP4Tensor.from_numpy(_weight(3, n, k, False))
+    ins = [(torch.randn(m, k, device="cuda").half(), torch.randn(m, n // 2, device="cuda").half()) for m in (300, 1500, 3000)]
+    ref = [G.nvfp4_linear_swiglu_grad(x, dh, w) for x, dh in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[G.nvfp4_linear_swiglu_grad(x, dh, w, stream=s) for x, dh in ins] for s in streams]
+    torch.cuda.synchronize()
+    for one in got:
+        for t, r in zip(one, ref):
             assert torch.equal(t.view(torch.int16), r.view(torch.int16))
