@@ -361,8 +361,8 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
 // ---- some hundred rows, gated: packed weights ----------------------------------------------------------------
 // The gated gradient from the packed rows in one launch. Weight row 4 q + j of a wave's tile t is pair
 // i0 + 8 NT w + 2 NT q + 2 t + j % 2, gate (j < 2) or up: a lane has both of 2 NT neighbouring pairs of a row.
-// 4352 x 5120: 333 rows take 34 us (435 TFLOP/s; 47 us by chunk products, 53 decoded), 700 rows 52 us (600; 70 decoded), 1900
-// rows 90 us (940; 115 decoded). A block alone on its CU is bound by a stage's latency (0.9 us: the way into LDS, sixteen
+// 4352 x 5120: 333 rows take 34 us (440 TFLOP/s; 55 us by chunk products, 46 decoded), 700 rows 53 us (590; 74 decoded), 1900
+// rows 88 us (960; 115 decoded). A block alone on its CU is bound by a stage's latency (0.8 us: the way into LDS, sixteen
 // fragment reads, four decodes in a row), several by the LDS reads of A, which NT tiles of a wave share.
 template <class T>
 __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(const f16 *__restrict__ x, int M, int K,

@@ -12,7 +12,7 @@
 //     the stage, MFMA step d takes elements 32 q + 8 d .. + 7 of them, and A's fragment of that step is unit 4 q + d of
 //     the row. A step's weights are decoded while the products of the step before run.
 // KS wave groups of a block share the reduction axis in runs of stages, and the first group adds the others' sums in
-// order: a stage takes about a microsecond of waiting, and few blocks are bound by its number.
+// order: a stage is mostly waiting, 0.8 us of it, and few blocks are bound by the number of stages.
 //
 // The weight rows feed MFMA's first operand, the batch's rows the second: a lane's four results of a tile belong to one
 // row of A, and the kernel chooses which weight rows they are.
