@@ -113,7 +113,9 @@ __global__ __launch_bounds__(ST_WAVES * 64, 4) void grad_stream_kernel(const f16
     load_a(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h) decode_columns(b[h], w[h], sc[h]);
-    const int om = threadIdx.x >> 5, oc = 4 * (threadIdx.x & 31);  // 512 threads: one float4 of the 16 x 128 tile each
+    // 512 threads: one float4 of the 16 x 128 tile each. In LDS a row's first halves of eight columns lie in front of the
+    // second halves, 16 bytes from lane to lane (at their own places, 32, half of the writes' cycles were conflicts).
+    const int om = threadIdx.x >> 5, slot = threadIdx.x & 31, oc = 8 * (slot & 15) + 4 * (slot >> 4);
 #pragma unroll 1
     for (int m0 = 0; m0 < M; m0 += 16) {
         f32x4 acc[8];
@@ -127,14 +129,14 @@ __global__ __launch_bounds__(ST_WAVES * 64, 4) void grad_stream_kernel(const f16
         if (m0 > 0) lds_barrier();  // the previous tile's sums have been read
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4 *o = reinterpret_cast<f32x4 *>(&tiles[wave][4 * q + j][8 * r]);
+            f32x4 *o = reinterpret_cast<f32x4 *>(&tiles[wave][4 * q + j][4 * r]);
             o[0] = f32x4{acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-            o[1] = f32x4{acc[4][j], acc[5][j], acc[6][j], acc[7][j]};
+            o[16] = f32x4{acc[4][j], acc[5][j], acc[6][j], acc[7][j]};
         }
         lds_barrier();
-        f32x4 s = *reinterpret_cast<const f32x4 *>(&tiles[0][om][oc]);
+        f32x4 s = *reinterpret_cast<const f32x4 *>(&tiles[0][om][4 * slot]);
 #pragma unroll
-        for (int v = 1; v < ST_WAVES; ++v) s += *reinterpret_cast<const f32x4 *>(&tiles[v][om][oc]);
+        for (int v = 1; v < ST_WAVES; ++v) s += *reinterpret_cast<const f32x4 *>(&tiles[v][om][4 * slot]);
         if (m0 + om < M) *reinterpret_cast<f32x4 *>(part + ((size_t)c * M + m0 + om) * K + g * ST_COLS + oc) = s;
     }
 }
