@@ -83,7 +83,7 @@ int nvfp4_linear_fp8_rows(const uint8_t *xq, const float *x_scale, int32_t M, co
  * infinity or a NaN in a row of dy, x or dh stays in that row.
  *   ws  device workspace of at least nvfp4_linear_grad_ws_bytes(M, N, K) or nvfp4_linear_swiglu_grad_ws_bytes(M, 2I,
  *       K) bytes, 16-byte aligned; contents ignored on entry, overwritten (large batches hold the decoded weight
- *       in it, 2 bytes an element; smaller ones FP32 partial sums). Calls that share a ws must not run concurrently.
+ *       in it, 2 bytes an element; smaller ones FP32 partial sums; some of the gated ones nothing). Calls that share a ws must not run concurrently.
  * Outputs and ws must not overlap inputs.
  * Requirements: K % 128 == 0, N % 16 == 0 (swiglu: I % 16 == 0), N <= 2^20; K <= 32768 (swiglu: 16384); M <= 2^26;
  * dy, dx, x, dh, dz, codes 16-byte aligned. Errors as in nvfp4moe.h, all before anything is enqueued. The *_ws_bytes

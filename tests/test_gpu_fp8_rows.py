@@ -93,6 +93,22 @@ def test_values_that_are_not_numbers_stay_in_their_row_or_column(m):
     assert (~y[1].isfinite()).all()
 
 
+def test_two_streams_at_once():
+    """Batches of several kernels on two streams at once, again and again, give the bits of one call alone."""
+    n, k = 4352, 5120
+    xq, xs, wq, ws = _case(5, 1000, n, k, False)
+    w = G.FP8ChannelTensor(torch.from_numpy(wq).cuda(), torch.from_numpy(ws).cuda())
+    ins = [(torch.from_numpy(xq[:m]).cuda(), torch.from_numpy(xs[:m]).cuda()) for m in (1, 20, 120, 333, 640, 1000)]
+    ref = [G.nvfp4_linear_fp8_rows(x, s, w) for x, s in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[G.nvfp4_linear_fp8_rows(x, s, w, stream=t) for t in streams for _ in range(3)] for x, s in ins]
+    torch.cuda.synchronize()
+    for r, many in zip(ref, got):
+        for y in many:
+            assert torch.equal(y.view(torch.int16), r.view(torch.int16))
+
+
 def test_no_rows():
     _, _, wq, ws = _case(0, 1, 64, 256, True)
     y = _run(np.zeros((0, 256), np.uint8), np.zeros(0, np.float32), wq, ws)
