@@ -305,8 +305,8 @@ __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__r
 
 // x [M][K] times the decoded gate and up rows, and the gradient of SwiGLU on them. Even tiles of a wave hold gate
 // rows and odd ones the up rows of the same i, so that a lane has both: staged row 16 t + 4 q + j of wave column w
-// is pair i0 + 8 NT w + 2 NT q + 4 (t / 2) + j, gate (t even) or up. 4096 rows of 4352 x 5120: 152 us behind the decoding
-// (1200 TFLOP/s, 253 tiles in one round). Each load brings rows of one 16-row tile, and a
+// is pair i0 + 8 NT w + 2 NT q + 4 (t / 2) + j, gate (t even) or up. 4096 rows of 4352 x 5120: 158 us behind the decoding
+// (1155 TFLOP/s, 253 tiles in one round). Each load brings rows of one 16-row tile, and a
 // wave's loads are all gates or all ups (the waves number a multiple of four).
 template <class T>
 __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f16 *__restrict__ x, int M, int K,
