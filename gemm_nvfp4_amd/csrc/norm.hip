@@ -15,6 +15,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int WAVE_ROWS = 4;  // rows per block where a wave has a row to itself
+// The rows' blocks are split over x and y: a launch holds fewer than 2^32 threads along one axis.
+constexpr int GRID_X = 1 << 20;
 
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -72,9 +74,10 @@ __global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_kernel(
 {
     __shared__ float red[T / 64];
     __shared__ uint32_t red_max[T / 64];
-    const int row = T == 64 ? blockIdx.x * WAVE_ROWS + (threadIdx.x >> 6) : blockIdx.x;
+    const int block = (int)blockIdx.y * GRID_X + (int)blockIdx.x;
+    const int row = T == 64 ? block * WAVE_ROWS + (threadIdx.x >> 6) : block;
     const int j = T == 64 ? threadIdx.x & 63 : threadIdx.x;
-    if (T == 64 && row >= M) return;  // wave-uniform, and no barrier follows
+    if (row >= M) return;  // T = 64: wave-uniform, and no barrier follows; else block-uniform
     const size_t base = (size_t)row * K;
     const int pieces = K >> 3;
     f16x8 a[V], b[V], g[V];
@@ -341,11 +344,11 @@ int run_norm(const uint16_t *x, const uint16_t *r, const uint16_t *w, int32_t M,
 {
     return by_width(K, [&](auto T, auto V) {
         constexpr int t = decltype(T)::value, v = decltype(V)::value;
-        const int rows = t == 64 ? WAVE_ROWS : 1;
-        return launch(q ? norm_kernel<t, v, true> : norm_kernel<t, v, false>, dim3((unsigned)((M + rows - 1) / rows)),
-                      dim3(t * rows), 0, st, reinterpret_cast<const f16 *>(x), reinterpret_cast<const f16 *>(r),
-                      reinterpret_cast<const f16 *>(w), M, K, eps, reinterpret_cast<f16 *>(s), reinterpret_cast<f16 *>(y), q,
-                      q_scale);
+        const int rows = t == 64 ? WAVE_ROWS : 1, blocks = (M + rows - 1) / rows;
+        const dim3 grid((unsigned)(blocks < GRID_X ? blocks : GRID_X), (unsigned)((blocks + GRID_X - 1) / GRID_X));
+        return launch(q ? norm_kernel<t, v, true> : norm_kernel<t, v, false>, grid, dim3(t * rows), 0, st,
+                      reinterpret_cast<const f16 *>(x), reinterpret_cast<const f16 *>(r), reinterpret_cast<const f16 *>(w), M, K,
+                      eps, reinterpret_cast<f16 *>(s), reinterpret_cast<f16 *>(y), q, q_scale);
     });
 }
 

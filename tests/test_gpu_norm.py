@@ -256,3 +256,21 @@ def test_offsets_past_2_31_elements():
     dx, _ = G.nvfp4_add_rms_norm_grad(x, x, want_dweight=False, dx=y)
     ref, _ = G.nvfp4_add_rms_norm_grad(x[-3:].contiguous(), x[-3:].contiguous(), want_dweight=False)
     assert torch.equal(dx[-3:].view(torch.int16), ref.view(torch.int16))
+
+
+@pytest.mark.parametrize("m,k", [(2 ** 26, 8), (2 ** 24 + 1, 2056), (2 ** 22 + 1, 8200)])
+def test_more_rows_than_one_grid_axis_holds(m, k):
+    """A launch holds fewer than 2^32 threads along one axis; a row has 64, 256 and 1024 of them here. In place; the first,
+    the last and the rows around 2^20 blocks against the same rows alone."""
+    x = torch.empty((m, k), dtype=torch.float16, device="cuda")
+    pattern = torch.randn((4093, k), device="cuda").half()  # a prime number of rows: blocks apart hold other rows
+    for lo in range(0, m, 4093 * 64):
+        part = x[lo:lo + 4093 * 64]
+        part.copy_(pattern.repeat(-(-len(part) // 4093), 1)[:len(part)])
+    at = [0, 1, 2 ** 20 - 1, 2 ** 20, 2 ** 22 - 1, 2 ** 22, m // 2, m - 5, m - 2, m - 1]
+    rows = x[at].contiguous()
+    G.nvfp4_add_rms_norm(x, y=x)
+    ref = G.nvfp4_add_rms_norm(rows)[1]
+    assert torch.equal(x[at].view(torch.int16), ref.view(torch.int16))
+    del x
+    torch.cuda.empty_cache()
