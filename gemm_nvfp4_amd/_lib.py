@@ -959,14 +959,19 @@ def _given(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, 
     return t
 
 
+def _unwanted(name: str):
+    raise ValueError(f"{name} is given, but want_{name} is False: it would not be written")
+
+
 def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                        eps: float = 1e-6, s: torch.Tensor | None = None, y: torch.Tensor | None = None,
                        q: torch.Tensor | None = None, q_scale: torch.Tensor | None = None, want_y: bool = True,
                        want_q: bool = False, stream=None):
     """The residual's sum and the root-mean-square norm of fp16 x [M, K]: t = x + residual,
     v = t / sqrt(mean(t^2) + eps) * weight. Returns (s, y, q, q_scale): s = fp16(t) (None without a residual and
-    without s), y = fp16(v) (want_y), q uint8 E4M3 bytes of v / q_scale[m] with q_scale FP32 [M] (want_q, for
-    nvfp4_linear_fp8_rows). s may be x or residual, y too (but not s)."""
+    without s), y = fp16(v) (want_y), q uint8 E4M3 bytes of v / q_scale[m] with q_scale FP32 [M] (want_q, or where one of
+    them is given; for nvfp4_linear_fp8_rows). s may be x or residual, y too (but not s). A y that is given with
+    want_y=False is refused."""
     shape = x.shape
     if len(shape) != 2:
         _matrix(x, "x")
@@ -978,13 +983,11 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, resi
         _shape(residual, "residual", shape)
     if residual is not None or s is not None:
         s = _given(s, "s", shape, f16, x, stream)
-    if not want_y:
-        y = None
-    else:
+    if want_y:
         y = _given(y, "y", shape, f16, x, stream)
-    if not want_q:
-        q = q_scale = None
-    else:
+    elif y is not None:
+        _unwanted("y")
+    if want_q or q is not None or q_scale is not None:
         q, q_scale = _given(q, "q", shape, torch.uint8, x, stream), _given(q_scale, "q_scale", (M,), torch.float32, x, stream)
     dev = _current_device(x)
     x_ptr = _ptr(x, "x", f16, dev)
@@ -1023,7 +1026,7 @@ def nvfp4_add_rms_norm_grad(t: torch.Tensor, dy: torch.Tensor, weight: torch.Ten
                             ws: torch.Tensor | None = None, stream=None):
     """The gradient of nvfp4_add_rms_norm at its input t (the s of the forward call; x without a residual): dy is y's
     gradient, ds the residual stream's own (None: none). Returns (dx fp16 [M, K], the gradient of x and of the
-    residual; dweight FP32 [K]), None for what is not wanted. dx may be dy or ds."""
+    residual; dweight FP32 [K]), None for what is not wanted (and then must not be given). dx may be dy or ds."""
     shape = t.shape
     if len(shape) != 2:
         _matrix(t, "t")
@@ -1035,12 +1038,17 @@ def nvfp4_add_rms_norm_grad(t: torch.Tensor, dy: torch.Tensor, weight: torch.Ten
         _shape(ds, "ds", shape)
     if weight is not None and weight.shape != (K,):
         _shape(weight, "weight", (K,))
-    dx = _given(dx, "dx", shape, f16, t, stream) if want_dx else None
+    if want_dx:
+        dx = _given(dx, "dx", shape, f16, t, stream)
+    elif dx is not None:
+        _unwanted("dx")
     if want_dweight:
         dweight = _given(dweight, "dweight", (K,), torch.float32, t, stream)
         ws = _lora_ws(ws, _norm_grad_ws(M, K), t.device, stream)
     else:
-        dweight = ws = None
+        if dweight is not None:
+            _unwanted("dweight")
+        ws = None
     dev = _current_device(t)
     ds_ptr = None if ds is None else _ptr(ds, "ds", f16, dev)
     weight_ptr = None if weight is None else _ptr(weight, "weight", f16, dev)

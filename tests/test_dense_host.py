@@ -195,3 +195,18 @@ def test_wrappers_refuse_cpu_tensors():
                lambda: G.nvfp4_linear_swiglu_grad(_f16(M, K), _f16(M, N // 2), _w())):
         with pytest.raises(ValueError, match="GPU tensor"):
             fn()
+
+
+def test_given_outputs_are_never_dropped():
+    """A buffer that is given is written, so its shape is checked, or it is refused."""
+    x = _f16(M, K)
+    rows = [
+        (lambda: G.nvfp4_add_rms_norm(x, q=_u8(M, K + 8)), "q must have shape"),
+        (lambda: G.nvfp4_add_rms_norm(x, q_scale=torch.zeros(M + 1)), "q_scale must have shape"),
+        (lambda: G.nvfp4_add_rms_norm(x, y=_f16(M, K), want_y=False, want_q=True), "want_y is False"),
+        (lambda: G.nvfp4_add_rms_norm_grad(x, x, dx=_f16(M, K), want_dx=False), "want_dx is False"),
+        (lambda: G.nvfp4_add_rms_norm_grad(x, x, dweight=torch.zeros(K), want_dweight=False), "want_dweight is False"),
+    ]
+    for fn, what in rows:
+        with pytest.raises(ValueError, match=what):
+            fn()

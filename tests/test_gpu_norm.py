@@ -274,3 +274,15 @@ def test_more_rows_than_one_grid_axis_holds(m, k):
     assert torch.equal(x[at].view(torch.int16), ref.view(torch.int16))
     del x
     torch.cuda.empty_cache()
+
+
+def test_given_8_bit_outputs_are_written():
+    """q or q_scale alone, or both, without want_q: written as with it."""
+    x = torch.randn(5, 520, device="cuda").half()
+    _, y, q, qs = G.nvfp4_add_rms_norm(x, want_q=True)
+    for give in ("q", "q_scale", "both"):
+        mine = torch.full_like(q, 0x7F) if give != "q_scale" else None
+        scale = torch.full_like(qs, float("nan")) if give != "q" else None
+        _, y1, q1, qs1 = G.nvfp4_add_rms_norm(x, q=mine, q_scale=scale)
+        assert (mine is None or q1 is mine) and (scale is None or qs1 is scale)
+        assert torch.equal(q1, q) and torch.equal(qs1, qs) and torch.equal(y1, y)
