@@ -80,7 +80,8 @@ NVFP4_API int nvfp4_linear_fp8_rows(const uint8_t *xq, const float *x_scale, int
     if (!rows_ok(M)) return NVFP4_ERR_SHAPE;
     if (!w || !w->codes || !w->channel_scale) return NVFP4_ERR_NULL;
     if (w->rows < 1 || w->k < 16) return NVFP4_ERR_SHAPE;
-    if (w->k % 128 != 0 || w->k > nvfp4::MAX_LINEAR_FP8_K || w->rows % 16 != 0) return NVFP4_ERR_UNSUPPORTED;
+    if (w->k % 128 != 0 || w->k > nvfp4::MAX_LINEAR_FP8_K || w->rows % 16 != 0 || w->rows > nvfp4::MAX_FP8_ROWS_N)
+        return NVFP4_ERR_UNSUPPORTED;
     if (!aligned(w->codes, 16) || !aligned(w->channel_scale, 4)) return NVFP4_ERR_ALIGN;
     if (M == 0) return NVFP4_OK;
     if (!xq || !x_scale || !y) return NVFP4_ERR_NULL;

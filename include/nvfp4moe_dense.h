@@ -60,8 +60,8 @@ int nvfp4_add_rms_norm_grad(const uint16_t *t, const uint16_t *dy, const uint16_
  *   xq uint8 [M][K] E4M3FN bytes, x_scale FP32 [M], w rows = N, k = K, y fp16 [M][N].
  * The sum is one chain of 128-element steps, in order, at every batch size: a batch is bitwise equal to single-row
  * calls. NaN bytes and infinite or NaN scales follow IEEE rules and stay in their row or column.
- * Requirements: K % 128 == 0 and K <= 16384; N % 16 == 0; M <= 2^26; xq, y, codes 16-byte aligned, FP32 4-byte.
- * Errors: as nvfp4_linear_fp8.
+ * Requirements: K % 128 == 0 and K <= 16384; N % 16 == 0 and N <= 2^29 - 256; M <= 2^26; xq, y, codes 16-byte aligned,
+ * FP32 4-byte. Errors: as nvfp4_linear_fp8.
  * --------------------------------------------------------------------------------------------- */
 int nvfp4_linear_fp8_rows(const uint8_t *xq, const float *x_scale, int32_t M, const fp8_channel_weights *w, uint16_t *y,
                           void *stream);

@@ -210,3 +210,11 @@ def test_given_outputs_are_never_dropped():
     for fn, what in rows:
         with pytest.raises(ValueError, match=what):
             fn()
+
+
+def test_rows_refuse_more_columns_than_a_launch_holds(L):
+    """32 columns are a block of 256 threads for few rows, and a launch holds fewer than 2^32 threads along one axis."""
+    call = lambda rows, M=4: L.nvfp4_linear_fp8_rows(fake, fake, M, C.byref(fp8_channel_weights(fake, fake, rows, 128)), fake, null)  # noqa: E731,E501
+    for rows in ((1 << 29) - 240, 1 << 29, 1 << 30, (1 << 31) - 16):
+        assert call(rows) == UNSUPPORTED and call(rows, 0) == UNSUPPORTED, rows
+    assert call((1 << 29) - 256, 0) == OK
