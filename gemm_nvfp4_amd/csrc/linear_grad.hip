@@ -368,8 +368,8 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
 // fragment reads, four decodes in a row), several by the LDS reads of A, which NT tiles of a wave share.
 template <class T>
 __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(const f16 *__restrict__ x, int M, int K,
-                                                                        const uint8_t *__restrict__ codes,
-                                                                        const uint8_t *__restrict__ scales, int I, int layout,
+                                                                        const uint8_t *codes,
+                                                                        const uint8_t *scales, int I, int layout,
                                                                         const float *__restrict__ gscale,
                                                                         const f16 *__restrict__ dh, f16 *__restrict__ dz)
 {

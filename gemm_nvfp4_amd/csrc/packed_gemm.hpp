@@ -56,11 +56,16 @@ __device__ __forceinline__ PackedPlace packed_place()
     return p;
 }
 
-// The lane's codes and block scales of its weight row in each of its tiles, at its first element of the row.
+// The lane's codes and block scales of its weight row in each of its tiles, at its first element of the row. The kernel must
+// not declare them __restrict__: loads from memory that nothing may write could pass loads_apart().
 template <class T>
 struct PackedRows {
     const uint8_t *codes[T::NT], *scales[T::NT];
 };
+
+// Plain loads behind this stay behind the loads into LDS in front of it, which a count of loads in flight relies on: the
+// compiler has to take it for a write to all memory.
+__device__ __forceinline__ void loads_apart() { asm volatile("" ::: "memory"); }
 
 // acc = A B^T, A's rows from `a` on (`rows` of them, at most BM; the others count as zeros), K % 128 == 0. The result is in
 // the first group's waves; the others return false.
@@ -98,8 +103,8 @@ __device__ __forceinline__ bool packed_product(unsigned char *smem_all, const Pa
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // In the steady state a stage asks for A of the next and, three scheduling barriers later, for the weights of the one
-    // after, 2 NT loads, which the next stage's start leaves in flight. The first stage and the last wait for all.
+    // In the steady state a stage asks for A of the next and, behind loads_apart(), for the weights of the one after, 2 NT
+    // loads, which the next stage's start leaves in flight. The first stage and the last wait for all.
     if (first < last) load_b(first, 0), load_a(first, 0), load_b(min(first + 1, last - 1), 1);
     int buf = 0;
     const int a0 = p.r * ROW;
@@ -131,8 +136,12 @@ __device__ __forceinline__ bool packed_product(unsigned char *smem_all, const Pa
             decode(0);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                if (d < 3) decode(d + 1);
-                else load_b(min(k + 2, last - 1), set);
+                if (d < 3) {
+                    decode(d + 1);
+                } else {
+                    loads_apart();
+                    load_b(min(k + 2, last - 1), set);
+                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
