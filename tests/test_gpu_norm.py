@@ -286,3 +286,31 @@ def test_given_8_bit_outputs_are_written():
         _, y1, q1, qs1 = G.nvfp4_add_rms_norm(x, q=mine, q_scale=scale)
         assert (mine is None or q1 is mine) and (scale is None or qs1 is scale)
         assert torch.equal(q1, q) and torch.equal(qs1, qs) and torch.equal(y1, y)
+
+
+# a turn of the gradient's row loop is 2048, 512 and 256 rows at 64, 256 and 1024 threads a row: several turns, the last ragged
+@pytest.mark.parametrize("m,k", [(5000, 2048), (1301, 2056), (1301, 5120), (1030, 8192), (701, 8200), (520, 16392), (600, 32768)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_gradient_of_several_turns(m, k, residual):
+    x, _, w = _inputs(m + k, m, k, False)
+    rng = np.random.default_rng(m)
+    dy = rng.standard_normal((m, k)).astype(np.float16)
+    ds = rng.standard_normal((m, k)).astype(np.float16) if residual else None
+    dx, dx_ok = _guarded((m, k), torch.float16)
+    dw, dw_ok = _guarded((k,), torch.float32)
+    ws, ws_ok = _guarded((G.nvfp4_add_rms_norm_grad_ws_bytes(m, k),), torch.uint8)
+    cx, cdy, cds, cw = _cuda(x), _cuda(dy), _cuda(ds), _cuda(w)
+    G.nvfp4_add_rms_norm_grad(cx, cdy, cw, ds=cds, dx=dx, dweight=dw, ws=ws)
+    torch.cuda.synchronize()
+    assert dx_ok() and dw_ok() and ws_ok()
+    ref, size, ref_w, size_w = _grad(x, dy, ds, w, 1e-6)
+    _close16(dx, ref, scale=2 * EPS32 * size, what="dx")
+    assert np.all(np.abs(dw.double().cpu().numpy() - ref_w) <= (2 * EPS32 + m / 256 * 2.0 ** -24) * size_w)
+    # a row's dx has one order of adding: the same bits from calls of one turn
+    for lo in range(0, m, 255):
+        part = slice(lo, min(m, lo + 255))
+        one, _ = G.nvfp4_add_rms_norm_grad(cx[part], cdy[part], cw, ds=None if ds is None else cds[part], want_dweight=False)
+        assert torch.equal(one.view(torch.int16), dx[part].view(torch.int16)), lo
+    # dweight again: its order is fixed
+    _, again = G.nvfp4_add_rms_norm_grad(cx, cdy, cw, ds=cds)
+    assert torch.equal(again, dw)
