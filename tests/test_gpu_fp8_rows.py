@@ -152,3 +152,17 @@ def test_behind_the_norm_in_a_graph():
         step8 = (2.0 ** -4 + 2.0 ** -14) * v.abs() + 2.0 ** -10 * 1.001 * qs.double()[:, None]
         bound = step8 @ wd.abs().t() + 2.0 ** -11 * ref.abs() + 2.0 ** -25 + (k + 64) * 2.0 ** -23 * (v.abs() @ wd.abs().t())
         assert bool(((y.double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("n,k", [(64, 5120), (512, 8192), (80, 16384), (4096, 4096)])
+def test_wide_streams_give_the_bits_of_tiles(n, k):
+    """Up to 4096 columns stream up to 16 rows with one row tile, and 17 to 32 with two where K is at least 4096; the
+    larger batches take tiles. On random bytes, whose sums depend on the order of adding."""
+    m = 400
+    xq, xs, wq, ws = _case(n + k, m, n, k, False)
+    w = G.FP8ChannelTensor(torch.from_numpy(wq).cuda(), torch.from_numpy(ws).cuda())
+    x, s = torch.from_numpy(xq).cuda(), torch.from_numpy(xs).cuda()
+    y = G.nvfp4_linear_fp8_rows(x, s, w)
+    for lo, hi in ((0, 1), (399, 400), (7, 23), (77, 94), (100, 130), (368, 400), (200, 233), (0, 64), (50, 200)):
+        part = G.nvfp4_linear_fp8_rows(x[lo:hi].contiguous(), s[lo:hi].contiguous(), w)
+        assert torch.equal(part.view(torch.int16), y[lo:hi].view(torch.int16)), (lo, hi)
