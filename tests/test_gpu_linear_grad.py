@@ -317,3 +317,27 @@ def test_two_streams_at_once_gated():
     for one in got:
         for t, r in zip(one, ref):
             assert torch.equal(t.view(torch.int16), r.view(torch.int16))
+
+
+@pytest.mark.parametrize("m", [5, 40, 100, 600])
+def test_grad_of_a_tall_weight_whole_numbers(m):
+    """297 planes of 512 weight rows, the last one of 128, bit for bit: a row of dy has twenty terms (|dx| <= 20 * 2 * 12 in
+    steps of 1/4 fits fp16's 11 bits), among them one of the last 16 weight rows, one of the last plane and one of the first;
+    the others pass through all planes. 600 rows take decoded weights."""
+    n, k = 151664 + 16, 128
+    w = _weight(m, n, k, True)
+    rng = np.random.default_rng(m)
+    at = np.empty((m, 20), np.int64)
+    at[:, 0], at[:, 1], at[:, 2] = n - 1 - np.arange(m) % 16, n - 17 - np.arange(m) % 112, np.arange(m) % 512
+    at[:, 3:] = (512 * (1 + np.arange(17 * m) % 295) + rng.integers(0, 512, 17 * m)).reshape(m, 17)
+    dy = np.zeros((m, n), np.float16)
+    np.put_along_axis(dy, at, rng.choice(np.array([-2, -1, 1, 2], np.float16), at.shape), axis=1)
+    d = _dense(w)
+    ref = np.stack([dy[i, at[i]].astype(np.float64) @ d[at[i]] for i in range(m)])
+    assert len(set(map(len, map(set, at.tolist())))) == 1 and np.array_equal(ref, ref.astype(np.float16).astype(np.float64))
+    ws, ws_ok = _work(G.nvfp4_linear_grad_ws_bytes(m, n, k))
+    dx, ok = _guarded(m, k)
+    G.nvfp4_linear_grad(_cuda(dy), G.NVFP4Tensor.from_numpy(w), dx=dx, ws=ws)
+    torch.cuda.synchronize()
+    assert ok() and ws_ok()
+    assert np.array_equal(dx.double().cpu().numpy(), ref)
