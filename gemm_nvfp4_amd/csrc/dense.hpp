@@ -8,7 +8,7 @@ namespace nvfp4 {
 
 constexpr int MAX_NORM_K = 32768;            // 1024 threads of four 8-element pieces
 constexpr int MAX_DENSE_M = 1 << 26;
-constexpr int MAX_GRAD_ROWS = 1 << 20;       // N: 256 rows of fp16 stay below the buffer loads' 2^30 byte offsets
+constexpr int MAX_GRAD_ROWS = 1 << 20;       // N: buffer offsets stay below BUF_OOB (asserted in linear_grad.hip)
 // N of the 8-bit rows: a launch holds fewer than 2^32 threads along one axis, and up to 32 rows take tiles of 32 x 32, 256
 // threads each, dealt out in eights. Larger batches that fit in 288 GB (2 M N bytes of y, 128 N of codes) take fewer.
 constexpr int MAX_FP8_ROWS_N = (1 << 29) - 256;

@@ -29,6 +29,8 @@ constexpr int ST_WAVES = 8, ST_ROWS = 64;            // waves per block, weight 
 constexpr int ST_CHUNK = ST_WAVES * ST_ROWS;         // weight rows per plane
 constexpr int ST_COLS = 128;                         // output columns per block
 constexpr int FEW_ROWS = 64, ST_MAX_M = 512;  // always, and at most
+// One buffer holds all of dy, and the offset that feeds zeros has to lie past it: with 512 rows of 2^20 it begins right there.
+static_assert((uint64_t)ST_MAX_M * MAX_GRAD_ROWS * sizeof(f16) <= BUF_OOB, "dy's rows within a buffer");
 
 __host__ __device__ inline int grad_planes(int N) { return (N + ST_CHUNK - 1) / ST_CHUNK; }
 
@@ -258,6 +260,7 @@ __global__ __launch_bounds__(T::WAVES * 64) void grad_tile_kernel(const f16 *__r
                                                                   const f16 *__restrict__ b, int ld, int cols,
                                                                   const float *__restrict__ gscale, void *__restrict__ out)
 {
+    static_assert((uint64_t)(T::BM > T::BN ? T::BM : T::BN) * MAX_GRAD_ROWS * sizeof(f16) <= BUF_OOB, "a tile's rows within a buffer");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[T::NS * T::BYTES];
     int tm, tn;
     if (!tile_of_block(blockIdx.x, (M + T::BM - 1) / T::BM, (cols + T::BN - 1) / T::BN, tm, tn)) return;

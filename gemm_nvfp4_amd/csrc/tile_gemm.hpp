@@ -33,7 +33,8 @@ constexpr int STAGE_BYTES = 128;
 
 __host__ __device__ constexpr int unit_swizzle(int row) { return (row >> 1) & 7; }
 
-// One 16 x 16 x 128 product of E4M3 operands; the exponent scales are 1 (E8M0 127).
+// One 16 x 16 x 128 product of E4M3 operands. Zeros for both operands' scales, as constants, select the instruction without
+// scales (as E8M0 bytes they would be 2^-127).
 __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
