@@ -367,8 +367,9 @@ __global__ __launch_bounds__(T::WAVES * 64) void swiglu_grad_tile_kernel(const f
 // The gated gradient from the packed rows in one launch. Weight row 4 q + j of a wave's tile t is pair
 // i0 + 8 NT w + 2 NT q + 2 t + j % 2, gate (j < 2) or up: a lane has both of 2 NT neighbouring pairs of a row.
 // 4352 x 5120: 333 rows take 34 us (440 TFLOP/s; 55 us by chunk products, 46 decoded), 700 rows 53 us (590; 74 decoded), 1900
-// rows 88 us (960; 115 decoded). A block alone on its CU is bound by a stage's latency (0.8 us: the way into LDS, sixteen
-// fragment reads, four decodes in a row), several by the LDS reads of A, which NT tiles of a wave share.
+// rows 88 us (960; 115 decoded). A block alone on its CU is bound by a stage's latency (0.8 us: the way into LDS, which as
+// compiled no product overlaps (packed_gemm.hpp), sixteen fragment reads, four decodes in a row), several by the LDS reads of
+// A, which NT tiles of a wave share.
 template <class T>
 __global__ __launch_bounds__(T::THREADS, T::OCC) void swiglu_grad_packed_kernel(const f16 *__restrict__ x, int M, int K,
                                                                         const uint8_t *codes,
@@ -481,8 +482,9 @@ int with_shape(int i, F &&f)
 }
 
 // Whether dx of M rows takes the packed weights in one stream, or decodes them for tiles. Estimates in ns fitted to
-// measurements; us by the stream and the tiles: 4352 x 5120 23 and 31 at 100 rows, 36 and 38 at 200, 43 and 40 at 256;
-// 2048 x 2048 14 and 14 at 100, 21 and 15 at 200; 512 x 8192 13 and 13 at 100, 24 and 14 at 256.
+// measurements; us by the stream and the tiles: 4352 x 5120 22.7 and 33.7 at 100 rows, 34.5 and 44.1 at 200, 41.3 and
+// 41.2 at 256, 53.2 and 44.4 at 333; 2048 x 2048 13.4 and 13.5 at 100, 20.0 and 17.0 at 200; 512 x 8192 12.5 and 10.9 at 100,
+// 23.4 and 12.2 at 256.
 bool grad_streams(int64_t M, int64_t N, int64_t K)
 {
     if (M <= FEW_ROWS) return true;

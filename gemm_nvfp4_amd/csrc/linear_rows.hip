@@ -6,10 +6,10 @@
 // flight and hand the chain on from one to the next. More rows take the tiled product of tile_gemm.hpp, whose shape the
 // batch chooses.
 //
-// Measured at 4352 x 5120: one row 9.4 us (2.4 TB/s of 22.3 MB: 82 KB a block at what a CU has in flight, start-up, and
-// 1.2 us of the chain's hand-overs), 13 rows 10.4, 333 rows 19.6 (760 TFLOP/s), 8192 rows 167 (2.2 PFLOP/s; the library's
-// product of 8192^3 reaches 2.27). Sums in 512-element chunks, each closed by FP32 additions, reached 1.75 to 2.1 PFLOP/s
-// where the one chain reaches 2.3 to 2.65 in whole rounds.
+// Measured at 4352 x 5120, calls back to back: one row 9.1 us (2.4 TB/s of 22.3 MB: 82 KB a block at what a CU has in flight,
+// start-up, and 1.2 us of the chain's hand-overs), 13 rows 9.5, 333 rows 18.9 (780 TFLOP/s), 8192 rows 164 (2.2 PFLOP/s; the
+// library's product of 8192^3 reaches 2.27). Sums in 512-element chunks, each closed by FP32 additions, reached 1.75 to 2.1
+// PFLOP/s where the one chain reaches 2.3 to 2.65 in whole rounds.
 #include "dense.hpp"
 #include "nvfp4_device.hpp"
 #include "tile_gemm.hpp"

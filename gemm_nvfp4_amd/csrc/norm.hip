@@ -5,9 +5,9 @@
 // are taken there, and the outputs are written from there. How many threads share a row depends on K alone,
 // so a row's sums have one order whatever the batch: thread j takes pieces j, j + T, j + 2T, ...; its elements
 // are added in ascending order, then a butterfly over the 64 lanes, then the waves in order.
-// Measured: one row of 2048 2.7 us (start-up; the call from Python 6.0), 333 rows of 5120 to 8 bits 5.2 us, 8192 rows of 2048
-// 26.7 us, 5.0 TB/s, a copy's rate; the gradient of 333 rows of 5120 7.0 + 3.1 us, of 8192 rows of 2048 27.4 + 4.6 us
-// (30.2 together, 4.5 TB/s).
+// Measured, the least of twelve traced calls: one row of 2048 2.6 us (start-up; the call from Python 6.2), 333 rows of 5120 to 8
+// bits 5.3 us, 8192 rows of 2048 26.5 us, 5.1 TB/s, a copy's rate; the gradient of 333 rows of 5120 6.9 + 2.3 us, of 8192
+// rows of 2048 26.3 + 4.0 us (30.3 a call back to back, 4.4 TB/s).
 #include "dense.hpp"
 #include "nvfp4_device.hpp"
 
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(T == 64 ? 64 * WAVE_ROWS : T) void norm_kernel(
 // in registers, or in LDS where 1024 threads leave no registers for it. A block's groups meet in LDS in order, and
 // the blocks' sums [G][K] are added by a second launch: G, at most one block per CU, decides how much that moves (333
 // rows of 5120 took 11.5 us with a block a row and 7 MB of sums). The next row's loads are in flight while a row's sums
-// are taken. G depends on M and K alone.
+// are taken. G depends on M and K alone. With few turns what bounds it is latency: ds is asked for after t and dy have come.
 constexpr int GRAD_BLOCKS = 256;
 
 constexpr int grad_groups(int T) { return T == 64 ? 8 : T == 256 ? 2 : 1; }  // 512 threads but for the widest rows

@@ -104,7 +104,9 @@ __device__ __forceinline__ bool packed_product(unsigned char *smem_all, const Pa
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     // In the steady state a stage asks for A of the next and, behind loads_apart(), for the weights of the one after, 2 NT
-    // loads, which the next stage's start leaves in flight. The first stage and the last wait for all.
+    // loads, which the next stage's start leaves in flight. The first stage and the last wait for all. As compiled, A is
+    // waited for behind its loads all the same: over the paths through these conditions the compiler cannot tell which
+    // loads of the codes are still out, and waits for all before the first decode.
     if (first < last) load_b(first, 0), load_a(first, 0), load_b(min(first + 1, last - 1), 1);
     int buf = 0;
     const int a0 = p.r * ROW;

@@ -209,7 +209,7 @@ __device__ __forceinline__ void tile_product(unsigned char *smem, const Place &p
         if (first + s < last) load(first + s, s);
     int buf = 0;
     for (int k = first; k < last; ++k) {
-        // stage k has landed: at most the NS - 2 stages behind it are still in flight
+        // stage k has landed: at most the NS - 2 stages behind it are still in flight (with two stages none)
         if (NS > 2 && k + NS - 2 < last) wait_loads<(NS - 2) * (T::LA + T::LB)>();
         else wait_loads<0>();
         stage_barrier();  // every wave's part of it, and every wave is done with the buffer that is filled next
